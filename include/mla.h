@@ -75,7 +75,8 @@ typedef enum {
 
 typedef enum {
   MLA_DTYPE_BF16 = 0,   /* bf16 inputs/outputs, fp32 accumulation            */
-  MLA_DTYPE_FP32 = 1    /* fp32 inputs/outputs, fp32 arithmetic (CUDA cores) */
+  MLA_DTYPE_FP32 = 1,   /* fp32 inputs/outputs, fp32 arithmetic (CUDA cores) */
+  MLA_DTYPE_E4M3 = 2    /* 8-bit K/V cache elements (paged K/V caches only)  */
 } mla_dtype_t;
 
 /* Head geometry of one MLA layer.  softmax_scale <= 0 selects
@@ -382,6 +383,197 @@ mla_status_t mla_indexer_select(const float* q, const float* pooled, int64_t poo
                                 int32_t* positions_out, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged serving steps around the verify call: the page table and the slots of
+ * a step's new rows, the rows written into the caches, and the drafter's
+ * attention of one new token over an ordinary paged key/value cache.
+ *
+ * A slot is a cache row: slot = page id * page_size + row within the page.
+ * Rows beyond the last real one (padding of a fixed-size step) carry slot -1
+ * and position -1.  None of these calls reads lengths, slots or tables on the
+ * host, so each can be captured into a CUDA graph and replayed while they
+ * change.  The kernels below start only when the kernel before them in the
+ * stream has finished, and mla_page_step and the two appends let no later
+ * kernel start early: a verify or decode call right behind an append reads
+ * what it wrote.
+ * ------------------------------------------------------------------------ */
+
+/* Page tables, cache lengths, positions and slots of one step, on the GPU.
+ *
+ * Sequence b keeps kept_lens[b] cached rows (fewer than before after a
+ * rejection) and appends new_tokens[b] >= 0 rows (0: an idle slot); its table
+ * row holds held_pages[b] pages.  With P = page_size and W =
+ * max_pages_per_seq:
+ *   total  = min(kept + new, W * P)
+ *   grow   = max(0, ceil(total / P) - held)       pages it asks for
+ *   got    = the first `grow` pages left on the free list after the sequences
+ *            before it took theirs (fewer when the list runs out)
+ *   page_table[b][held .. held + got) = the pages got
+ *   held_pages_out[b] = held + got
+ *   cache_lens_out[b] = min(total, (held + got) * P)
+ * Negative inputs count as 0 and held is at most W.  Pages held beyond what
+ * the rows need stay held (a later step fills them).
+ *
+ *  free_pages  device [free_capacity] page ids; the list is the entries
+ *          free_span[0] .. free_span[1] - 1 (device [2]; clamped to the
+ *          capacity), taken from the front in sequence order
+ *  row_start_out  device [batch + 1]: sequence b's new rows are rows
+ *          row_start[b] .. row_start[b + 1] - 1 of the step (saturates at
+ *          INT32_MAX)
+ *  positions_out / slots_out  device [max_rows] int32 / int64: a row's
+ *          position in its sequence (saturates at INT32_MAX), and its slot, or
+ *          -1 for a position at or beyond cache_lens_out (no page, or past the
+ *          table) and for a row whose page id is outside [0, num_pages)
+ *          (recorded as code 300 in the status word); both -1 for rows at or
+ *          beyond row_start[batch].
+ *          Rows beyond max_rows are dropped.
+ *  free_span_out  device [2]: {free_span[0] + pages taken, free_span[1]}
+ *  missing_out  device [1]: pages asked for that the list did not have (0:
+ *          every sequence got its pages; saturates at INT32_MAX)
+ *
+ * batch in [1, 65535]; batch * W at most 2^31 - 1.  max_rows and
+ * free_capacity may be 0.  Outputs must not overlap inputs (page_table is
+ * both), so a call can be repeated with the same result.  Pages within a list
+ * must be distinct; the ids are not checked against each other. */
+mla_status_t mla_page_step(const int32_t* kept_lens, const int32_t* new_tokens,
+                           const int32_t* held_pages, int32_t batch, int32_t* page_table,
+                           int32_t max_pages_per_seq, int32_t page_size, int32_t num_pages,
+                           const int32_t* free_pages, int32_t free_capacity,
+                           const int32_t* free_span, int32_t* cache_lens_out,
+                           int32_t* held_pages_out, int32_t* row_start_out,
+                           int32_t* positions_out, int64_t* slots_out, int32_t max_rows,
+                           int32_t* free_span_out, int32_t* missing_out, void* stream);
+
+/* The rows of a step into the latent cache, with the queries a verify call
+ * takes: per row i with slot s = slots[i] and position p = positions[i]
+ *   q_nope[i]  = q[i][:, :n]                 q_rope[i] = rot_p(q[i][:, n:])
+ *   c_kv[s]    = kv[i][:r] * rsqrt(mean(kv[i][:r]^2) + eps) * norm_weight
+ *   k_rope[s]  = rot_p(kv[i][r:])
+ * Norm and rotation run in fp32 and are rounded once.
+ *
+ *  geom    H, r, n, rope, dtype of the layer (v is not used but must be valid)
+ *  q       device [rows, H, n + rope], q_row_stride elements between rows;
+ *          NULL: only the cache is written
+ *  kv      device [rows, r + rope], kv_row_stride elements between rows
+ *  norm_weight  device [r] in the geometry's dtype; NULL: c_kv is copied
+ *          without a norm
+ *  cos_sin device fp32 [table_rows, rope]: cos of a position's rope/2 angles,
+ *          then sin; rope must be a multiple of 16
+ *  interleaved  rot turns pairs (2i, 2i+1) when nonzero, (i, i + rope/2) when 0:
+ *          (a, b) -> (a cos - b sin, b cos + a sin)
+ *  q_nope / q_rope  device [rows, H, n] / [rows, H, rope], dense
+ *  c_kv / k_rope   the cache, row s at base + s * row stride (cache_rows rows)
+ *
+ * A row with a position outside [0, table_rows) writes nothing at all, and a
+ * row with a slot outside [0, cache_rows) nothing to the cache; what was there
+ * stays.  Slots of a step must be distinct.  Buffers must not overlap, but
+ * k_rope may lie inside c_kv's rows (a packed cache).  rows may be 0. */
+mla_status_t mla_append_latent(const mla_geometry_t* geom, const void* q, int64_t q_row_stride,
+                               const void* kv, int64_t kv_row_stride, const void* norm_weight,
+                               float eps, const float* cos_sin, int32_t table_rows,
+                               int32_t interleaved, const int32_t* positions,
+                               const int64_t* slots, int32_t rows, void* q_nope, void* q_rope,
+                               void* c_kv, void* k_rope, int64_t c_kv_row_stride,
+                               int64_t k_rope_row_stride, int64_t cache_rows, void* stream);
+
+/* Heads of one ordinary attention layer (the drafter's): num_heads query
+ * heads share num_kv_heads key/value heads, head h reading h / (num_heads /
+ * num_kv_heads).  softmax_scale <= 0 selects 1/sqrt(head_dim).  dtype (bf16 or
+ * fp32) is that of q, k, v and the outputs; cache_dtype that of the caches:
+ * dtype itself, or MLA_DTYPE_E4M3 with bf16.  head_dim is at most 256 and a
+ * whole number of 16-byte vectors in both types (a multiple of 8 for bf16, 4
+ * for fp32, 16 for e4m3). */
+typedef struct {
+  int32_t num_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  float softmax_scale;
+  int32_t dtype;
+  int32_t cache_dtype;
+} mla_kv_geometry_t;
+
+/* A paged key/value cache: element (page, row, head, d) of either cache lies
+ * page*page_stride + row*row_stride + head*head_stride + d elements from its
+ * base (any order of the three; whole 16-byte vectors).  k_scale and v_scale
+ * are device fp32 [num_kv_heads] for an e4m3 cache (a cached value stands for
+ * itself times its head's scale; NULL: 1), NULL otherwise. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t page_stride;
+  int64_t row_stride;
+  int64_t head_stride;
+  int32_t page_size;
+  int32_t num_pages;
+  const float* k_scale;
+  const float* v_scale;
+} mla_kv_cache_t;
+
+/* The rows of a step into a paged key/value cache: per row i
+ *   q_out[i] = rot(q[i]),  k_cache[slot] = rot(k[i]) / k_scale,
+ *   v_cache[slot] = v[i] / v_scale
+ * rot turns the first rope_dim elements of each head as in mla_append_latent
+ * and leaves the others (rope_dim 0: no rotation, cos_sin may be NULL;
+ * otherwise a multiple of 16 up to head_dim).  The division applies to e4m3
+ * caches; values are rounded once, to nearest even, and saturate at +-448 in
+ * e4m3 (NaN stays NaN).
+ *
+ *  q / k / v  device [rows, heads, head_dim], heads dense, *_row_stride
+ *          elements between rows (views of one projection's rows will do);
+ *          q NULL: only the cache is written
+ *  q_out   device [rows, num_heads, head_dim], dense; may be q itself when q
+ *          is dense
+ *
+ * Skipped rows, distinct slots and rows == 0: as for mla_append_latent (with
+ * rope_dim 0 only a negative position counts as outside). */
+mla_status_t mla_append_kv(const mla_kv_geometry_t* geom, const void* q, int64_t q_row_stride,
+                           const void* k, int64_t k_row_stride, const void* v,
+                           int64_t v_row_stride, const float* cos_sin, int32_t table_rows,
+                           int32_t rope_dim, int32_t interleaved, const int32_t* positions,
+                           const int64_t* slots, int32_t rows, void* q_out,
+                           const mla_kv_cache_t* cache, void* stream);
+
+/* Bytes of device workspace mla_decode_attention needs (the partial sums of
+ * sequences cut between thread blocks), for a table of max_pages_per_seq
+ * pages of page_size rows.  It needs no initialisation.  Host only. */
+mla_status_t mla_decode_workspace_bytes(const mla_kv_geometry_t* geom, int32_t batch,
+                                        int32_t page_size, int32_t max_pages_per_seq,
+                                        size_t* bytes);
+
+/* Attention of one new token per sequence over a paged key/value cache (a
+ * drafter's decode step).  Sequence b has T_b = cache_lens[b] cached rows, its
+ * new token's row included, and sees rows max(0, T_b - window) .. T_b - 1
+ * (window 0: all of them):
+ *   out[b][h] = sum_t softmax_t(scale * q[b][h] . k[t]) v[t]
+ *   lse[b][h] = log sum_t exp(scale * q[b][h] . k[t])       (natural log)
+ * A sequence with T_b <= 0 (an idle slot) gets zeros and lse = -inf, and so
+ * does a head whose scores are all -inf.  T_b beyond the table's
+ * max_pages_per_seq * page_size rows counts as that many.
+ *
+ *  q       device [batch, num_heads, head_dim], q_row_stride elements between
+ *          sequences, heads dense
+ *  cache_lens  device [batch] int32
+ *  page_table  device [batch, max_pages_per_seq] int32, entries past a
+ *          sequence's last page are not read; an id outside [0, num_pages)
+ *          reads as zero keys and values and is recorded as code 300 in the
+ *          status word
+ *  out     device [batch, num_heads, head_dim], dense
+ *  lse     device fp32 [batch, num_heads], may be NULL
+ *  workspace  mla_decode_workspace_bytes() bytes, 256-byte aligned (may be
+ *          NULL when that is 0)
+ *
+ * The lengths are read on the device: the rows of all sequences and key/value
+ * heads are cut into equal shares for the thread blocks, whatever the lengths,
+ * and the shares of one head are joined in a fixed order, so repeated calls
+ * give the same bits.  Cache rows beyond T_b or before the window are not
+ * read.  Concurrent calls need a workspace each. */
+mla_status_t mla_decode_attention(const mla_kv_geometry_t* geom, const void* q,
+                                  int64_t q_row_stride, const mla_kv_cache_t* cache,
+                                  const int32_t* cache_lens, int32_t batch,
+                                  const int32_t* page_table, int32_t max_pages_per_seq,
+                                  int32_t window, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Per-kernel timing, for benchmarks.  While enabled, every kernel launch the
  * library makes is bracketed by a pair of CUDA events recorded on the call's
  * stream (events come from a library-owned pool; no device memory).  Do not
@@ -403,7 +595,8 @@ mla_status_t mla_kernel_timing_read(char* names, size_t names_len, int32_t* laun
  * MLA_OK when nothing was recorded since the last clear; MLA_ERR_TIMEOUT
  * when a bounded wait inside a kernel ran out (*code receives the site that
  * gave up, 1..299); MLA_ERR_INVALID_ARG when a kernel met a page id outside
- * [0, num_pages) (*code = 300; that page's positions were read as zeros).
+ * [0, num_pages) (*code = 300; that page's positions were read as zeros, or
+ * got no slot from mla_page_step).
  * The kernels never hang on a missing signal: each wait gives up after about
  * a second, records its site here and lets the kernel finish (its outputs are
  * then undefined).  clear != 0 resets the word.

@@ -9,9 +9,10 @@ falling back to anything.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -30,6 +31,8 @@ BRANCH_ABSORBED = 1
 BRANCH_MATERIALISED = 2
 BRANCH_NAMES = {1: "absorbed", 2: "materialised"}
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+# element types of a paged key/value cache
+CACHE_DTYPES = {**DTYPES, torch.float8_e4m3fn: 2}
 
 
 class MlaError(RuntimeError):
@@ -43,6 +46,20 @@ class Geometry(ctypes.Structure):
                 ("qk_nope_dim", ctypes.c_int32), ("v_dim", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
                 ("dtype", ctypes.c_int32)]
+
+
+class KVGeometry(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("cache_dtype", ctypes.c_int32)]
+
+
+class KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -76,6 +93,15 @@ _SIGS = {
                                     _I32, _P, _P]),
     "mla_rollback_valid_prefix": (_I32, [_P, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32,
                                          _P, _P]),
+    "mla_page_step": (_I32, [_P, _P, _P, _I32, _P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P,
+                             _P, _I32, _P, _P, _P]),
+    "mla_append_latent": (_I32, [_P, _P, _I64, _P, _I64, _P, ctypes.c_float, _P, _I32, _I32, _P,
+                                 _P, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "mla_append_kv": (_I32, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I32, _I32, _P, _P, _I32,
+                             _P, _P, _P]),
+    "mla_decode_workspace_bytes": (_I32, [_P, _I32, _I32, _I32, _P]),
+    "mla_decode_attention": (_I32, [_P, _P, _I64, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P,
+                                    ctypes.c_size_t, _P]),
     "mla_kernel_timing_enable": (_I32, [_I32]),
     "mla_kernel_timing_read": (_I32, [ctypes.c_char_p, ctypes.c_size_t, _P, _P, _I32, _P,
                                       _I32]),
@@ -535,3 +561,420 @@ def mla_indexer_select(q: torch.Tensor, pooled: torch.Tensor, cache_len: int, k_
                                     S, int(k_windows), _ptr(wins), _ptr(pos), _ptr(ws),
                                     ws.numel(), stream), "mla_indexer_select")
     return wins, pos
+
+
+# ---------------------------------------------------------------------------
+# Paged serving steps: page tables, appends, the drafter's decode attention
+# ---------------------------------------------------------------------------
+
+def _tensor(name: str, t: torch.Tensor, shape=None, dtype=None, dense: bool = True):
+    """Check one tensor argument (a None in `shape` matches any size)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(w is not None and int(w) != g
+                                  for w, g in zip(shape, t.shape))):
+        want = "[" + ", ".join("*" if w is None else str(w) for w in shape) + "]"
+        raise ValueError(f"{name} must be {want}, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
+    return t
+
+
+def _one_device(**tensors) -> torch.device:
+    """The CUDA device that every given tensor is on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+        dev = t.device
+    return dev
+
+
+def _allocating_on(stream, dev: torch.device):
+    """Allocate for kernels of `stream` (a raw handle; None: the current one), so
+    that freed memory is only reused behind them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev))
+
+
+class _PreparedCall:
+    """A C call whose arguments are marshalled once and issued by run()."""
+
+    def _prepare(self, name: str, args, dev: torch.device, keep, made=()):
+        self._name = name
+        self._fn = getattr(lib(), name)
+        types = _SIGS[name][1]
+        # plain numbers become ctypes values now, so a run converts nothing
+        self._args = [types[i](a) if isinstance(a, (int, float)) else a
+                      for i, a in enumerate(args)]
+        self._dev = dev.index if dev.index is not None else torch.cuda.current_device()
+        self._keep = keep
+        self._made = [t for t in made if t is not None]
+        self._home = _current_stream(torch.device("cuda", self._dev))
+        self._streams = {self._home}
+
+    def run(self, stream=None) -> None:
+        """Issue the call on the current stream of the tensors' device (or on
+        ``stream``, a raw handle) with what the buffers hold then."""
+        if stream is None:
+            stream = (_raw_stream(self._dev) if _raw_stream is not None else
+                      torch.cuda.current_stream(self._dev).cuda_stream)
+        if stream not in self._streams:
+            # the buffers made here must not be reused before this stream is done with them
+            s = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", self._dev))
+            for t in self._made:
+                t.record_stream(s)
+            self._streams.add(stream)
+        if torch.cuda.current_device() != self._dev:
+            with torch.cuda.device(self._dev):
+                st = self._fn(*self._args, stream)
+        else:
+            st = self._fn(*self._args, stream)
+        if st != MLA_OK:
+            _check(st, self._name)
+
+
+class PageStep(NamedTuple):
+    """The outputs of mla_page_step (device tensors)."""
+    cache_lens: torch.Tensor   # int32 [batch]
+    held_pages: torch.Tensor   # int32 [batch]
+    row_start: torch.Tensor    # int32 [batch + 1]
+    positions: torch.Tensor    # int32 [max_rows]
+    slots: torch.Tensor        # int64 [max_rows]
+    free_span: torch.Tensor    # int32 [2]
+    missing: torch.Tensor      # int32 [1]
+
+
+class PreparedPageStep(_PreparedCall):
+    """mla_page_step with its arguments marshalled once (fixed buffers, as in a
+    serving loop or a captured graph); ``run()`` issues it and ``out`` holds
+    its outputs.  The tensors must outlive the object."""
+
+    def __init__(self, kept_lens, new_tokens, held_pages, page_table, free_pages, free_span,
+                 page_size: int, num_pages: int, max_rows: int,
+                 out: Optional[PageStep] = None):
+        i32 = torch.int32
+        _tensor("page_table", page_table, (None, None), i32)
+        B, W = page_table.shape
+        for name, t in (("kept_lens", kept_lens), ("new_tokens", new_tokens),
+                        ("held_pages", held_pages)):
+            _tensor(name, t, (B,), i32)
+        _tensor("free_pages", free_pages, (None,), i32)
+        _tensor("free_span", free_span, (2,), i32)
+        max_rows = int(max_rows)
+        if max_rows < 0:
+            raise ValueError("max_rows must not be negative")
+        shapes = (("cache_lens", (B,), i32), ("held_pages", (B,), i32),
+                  ("row_start", (B + 1,), i32), ("positions", (max_rows,), i32),
+                  ("slots", (max_rows,), torch.int64), ("free_span", (2,), i32),
+                  ("missing", (1,), i32))
+        if out is not None:
+            for (name, shape, dtype), t in zip(shapes, out):
+                _tensor("out." + name, t, shape, dtype)
+        dev = _one_device(kept_lens=kept_lens, new_tokens=new_tokens, held_pages=held_pages,
+                          page_table=page_table, free_pages=free_pages, free_span=free_span,
+                          **({} if out is None else {"out_" + n[0]: t
+                                                     for n, t in zip(shapes, out)}))
+        made = ()
+        if out is None:
+            out = made = PageStep(*[torch.empty(shape, dtype=dtype, device=dev)
+                                    for _, shape, dtype in shapes])
+        self.out = out
+        args = [_ptr(kept_lens), _ptr(new_tokens), _ptr(held_pages), B, _ptr(page_table), W,
+                int(page_size), int(num_pages), _ptr(free_pages), free_pages.numel(),
+                _ptr(free_span), _ptr(out.cache_lens), _ptr(out.held_pages), _ptr(out.row_start),
+                _ptr(out.positions), _ptr(out.slots), max_rows, _ptr(out.free_span),
+                _ptr(out.missing)]
+        keep = (kept_lens, new_tokens, held_pages, page_table, free_pages, free_span, out)
+        self._prepare("mla_page_step", args, dev, keep, made)
+
+
+def mla_page_step(kept_lens, new_tokens, held_pages, page_table, free_pages, free_span,
+                  page_size: int, num_pages: int, max_rows: int, out: Optional[PageStep] = None,
+                  stream=None) -> PageStep:
+    """Page table, cache lengths, positions and slots of one step, on the GPU.
+
+    ``kept_lens``, ``new_tokens``, ``held_pages`` int32 [B]; ``page_table``
+    int32 [B, max_pages] (its new entries are written); ``free_pages`` int32
+    ids of which entries ``free_span[0] .. free_span[1] - 1`` are free.  The
+    step's rows are the sequences' new tokens in order, at most ``max_rows``;
+    rows behind them get slot and position -1.  ``missing`` counts the pages
+    that the free list did not have.  Returns a :class:`PageStep`; its
+    ``cache_lens``, ``held_pages`` and ``free_span`` are the next step's
+    inputs."""
+    with _allocating_on(stream, page_table.device):
+        call = PreparedPageStep(kept_lens, new_tokens, held_pages, page_table, free_pages,
+                                free_span, page_size, num_pages, max_rows, out)
+        call.run(stream)
+    return call.out
+
+
+def _head_rows(name: str, t: torch.Tensor, dtype=None):
+    """(rows, heads, width, elements between rows) of [rows, heads, width] with dense heads."""
+    _tensor(name, t, (None, None, None), dtype, dense=False)
+    N, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return N, H, D, (t.stride(0) if N > 1 else H * D)
+
+
+def _row_cache(name: str, t: torch.Tensor, width: int, dtype):
+    """(rows, elements between rows) of a cache [pages, page, width] or [rows, width]."""
+    if t.dim() == 2:
+        t = t.unsqueeze(0)
+    _tensor(name, t, (None, None, width), dtype, dense=False)
+    P, S, _ = t.shape
+    stride = t.stride(1) if S > 1 else (t.stride(0) if P > 1 else width)
+    if (width > 1 and t.stride(2) != 1) or (P > 1 and t.stride(0) != S * stride):
+        raise ValueError(f"{name}: pages must be contiguous runs of rows")
+    return P * S, stride
+
+
+def _step_rows(positions, slots, rows: int):
+    _tensor("positions", positions, (rows,), torch.int32)
+    _tensor("slots", slots, (rows,), torch.int64)
+
+
+class PreparedAppendLatent(_PreparedCall):
+    """mla_append_latent with its arguments marshalled once; ``run()`` issues it,
+    ``q_nope`` and ``q_rope`` are its outputs.  The tensors must outlive the
+    object."""
+
+    def __init__(self, q, kv, cos_sin, positions, slots, c_kv, k_rope, norm_weight=None,
+                 eps: float = 1e-6, interleaved: bool = True, q_nope=None, q_rope=None):
+        _tensor("kv", kv, (None, None), dense=False)
+        if kv.dtype not in DTYPES:
+            raise ValueError(f"kv must be bf16 or fp32, got {kv.dtype}")
+        dt = kv.dtype
+        _tensor("cos_sin", cos_sin, (None, None), torch.float32)
+        rope, N = cos_sin.shape[1], kv.shape[0]
+        r = kv.shape[1] - rope
+        if r < 1 or (kv.shape[1] > 1 and kv.stride(1) != 1):
+            raise ValueError("kv rows must be contiguous and hold the latent and the RoPE key")
+        kvs = kv.stride(0) if N > 1 else kv.shape[1]
+        _step_rows(positions, slots, N)
+        rows, cs = _row_cache("c_kv", c_kv, r, dt)
+        rows2, ks = _row_cache("k_rope", k_rope, rope, dt)
+        if rows != rows2:
+            raise ValueError("c_kv and k_rope must have the same rows")
+        if norm_weight is not None:
+            _tensor("norm_weight", norm_weight, (r,), dt)
+        H, n, qs = 1, 16, 0
+        if q is not None:
+            _, H, width, qs = _head_rows("q", q, dt)
+            n = width - rope
+            if q.shape[0] != N or n < 1:
+                raise ValueError("q must be [rows, H, n + rope] with kv's rows")
+            if q_nope is not None:
+                _tensor("q_nope", q_nope, (N, H, n), dt)
+            if q_rope is not None:
+                _tensor("q_rope", q_rope, (N, H, rope), dt)
+        elif q_nope is not None or q_rope is not None:
+            raise ValueError("q_nope and q_rope need q")
+        dev = _one_device(kv=kv, q=q, cos_sin=cos_sin, positions=positions, slots=slots,
+                          c_kv=c_kv, k_rope=k_rope, norm_weight=norm_weight, q_nope=q_nope,
+                          q_rope=q_rope)
+        made = []
+        if q is not None:
+            # (a skipped row is not written: it starts as zeros, not as whatever was there)
+            if q_nope is None:
+                q_nope = torch.zeros((N, H, n), dtype=dt, device=dev)
+                made.append(q_nope)
+            if q_rope is None:
+                q_rope = torch.zeros((N, H, rope), dtype=dt, device=dev)
+                made.append(q_rope)
+        self.q_nope, self.q_rope = q_nope, q_rope
+        geom = _geometry(H, r, n, n, rope, dt, None)
+        args = [ctypes.byref(geom), _ptr(q), qs, _ptr(kv), kvs, _ptr(norm_weight), float(eps),
+                _ptr(cos_sin), cos_sin.shape[0], 1 if interleaved else 0, _ptr(positions),
+                _ptr(slots), N, _ptr(q_nope), _ptr(q_rope), _ptr(c_kv), _ptr(k_rope), cs, ks,
+                rows]
+        keep = (q, kv, cos_sin, positions, slots, c_kv, k_rope, norm_weight, q_nope, q_rope)
+        self._prepare("mla_append_latent", args, dev, keep, made)
+
+
+def mla_append_latent(q, kv, cos_sin, positions, slots, c_kv, k_rope, norm_weight=None,
+                      eps: float = 1e-6, interleaved: bool = True, q_nope=None, q_rope=None,
+                      stream=None):
+    """The rows of a step into the paged latent cache.  Returns (q_nope, q_rope).
+
+    ``q`` [N, H, n + rope] (or None), ``kv`` [N, r + rope] as the projections
+    leave them; ``cos_sin`` fp32 [table, rope] (cosines, then sines);
+    ``positions`` int32 [N], ``slots`` int64 [N] as mla_page_step gives them.
+    c_kv gets the RMS-normalised latent (``norm_weight`` None: as it is),
+    k_rope the rotated key; q is split into q_nope and the rotated q_rope, which
+    mla_verify_attention takes as [B, L, H, *] views.  Rows with position -1
+    are skipped."""
+    with _allocating_on(stream, kv.device):
+        call = PreparedAppendLatent(q, kv, cos_sin, positions, slots, c_kv, k_rope, norm_weight,
+                                    eps, interleaved, q_nope, q_rope)
+        call.run(stream)
+    return call.q_nope, call.q_rope
+
+
+def _kv_cache(k_cache, v_cache, dtype, kv_heads: int, dim: int, k_scale, v_scale):
+    """The C description of a paged key/value cache, and its element type."""
+    if dtype not in DTYPES:
+        raise ValueError(f"q, k and v must be bf16 or fp32, got {dtype}")
+    _tensor("k_cache", k_cache, (None, None, kv_heads, dim), dense=False)
+    _tensor("v_cache", v_cache, k_cache.shape, k_cache.dtype, dense=False)
+    if k_cache.dtype not in CACHE_DTYPES:
+        raise ValueError(f"a cache must be bf16, fp32 or float8_e4m3fn, got {k_cache.dtype}")
+    strides = [k_cache.stride(i) if k_cache.shape[i] > 1 else 0 for i in range(3)]
+    if strides != [v_cache.stride(i) if v_cache.shape[i] > 1 else 0 for i in range(3)]:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    if dim > 1 and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
+        raise ValueError("cache rows must be contiguous in their last dimension")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None:
+            _tensor(name, t, (kv_heads,), torch.float32)
+    return KVCache(_ptr(k_cache), _ptr(v_cache), strides[0], strides[1], strides[2],
+                   k_cache.shape[1], k_cache.shape[0], _ptr(k_scale), _ptr(v_scale))
+
+
+class PreparedAppendKV(_PreparedCall):
+    """mla_append_kv with its arguments marshalled once; ``run()`` issues it and
+    ``q_out`` is its output.  The tensors must outlive the object."""
+
+    def __init__(self, q, k, v, cos_sin, positions, slots, k_cache, v_cache,
+                 interleaved: bool = False, k_scale=None, v_scale=None, q_out=None):
+        N, Hk, D, ks = _head_rows("k", k)
+        dt = k.dtype
+        _tensor("v", v, (N, Hk, D), dt, dense=False)
+        vs = _head_rows("v", v)[3]
+        cache = _kv_cache(k_cache, v_cache, dt, Hk, D, k_scale, v_scale)
+        _step_rows(positions, slots, N)
+        rope = table = 0
+        if cos_sin is not None:
+            _tensor("cos_sin", cos_sin, (None, None), torch.float32)
+            table, rope = cos_sin.shape
+            if rope < 1:
+                raise ValueError("cos_sin must not be empty (None: no rotation)")
+        H, qs = Hk, 0
+        if q is not None:
+            _tensor("q", q, (N, None, D), dt, dense=False)
+            _, H, _, qs = _head_rows("q", q)
+            if q_out is not None:
+                _tensor("q_out", q_out, (N, H, D), dt)
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
+        dev = _one_device(k=k, q=q, v=v, cos_sin=cos_sin, positions=positions, slots=slots,
+                          k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                          q_out=q_out)
+        made = []
+        if q is not None and q_out is None:
+            q_out = torch.zeros((N, H, D), dtype=dt, device=dev)
+            made.append(q_out)
+        self.q_out = q_out
+        geom = KVGeometry(H, Hk, D, 0.0, DTYPES[dt], CACHE_DTYPES[k_cache.dtype])
+        args = [ctypes.byref(geom), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cos_sin), table,
+                rope, 1 if interleaved else 0, _ptr(positions), _ptr(slots), N, _ptr(q_out),
+                ctypes.byref(cache)]
+        keep = (geom, cache, q, k, v, cos_sin, positions, slots, k_cache, v_cache, k_scale,
+                v_scale, q_out)
+        self._prepare("mla_append_kv", args, dev, keep, made)
+
+
+def mla_append_kv(q, k, v, cos_sin, positions, slots, k_cache, v_cache, interleaved: bool = False,
+                  k_scale=None, v_scale=None, q_out=None, stream=None):
+    """The rows of a step into a paged key/value cache.  Returns the rotated q.
+
+    ``q`` [N, H, D] (or None), ``k`` and ``v`` [N, Hkv, D] (views of one
+    projection's rows will do); ``cos_sin`` fp32 [table, rope_dim] or None;
+    caches [num_pages, page_size, Hkv, D] in any stride order (a cache laid
+    out [pages, Hkv, page, D] is passed as ``cache.transpose(1, 2)``), of q's
+    type or float8_e4m3fn with fp32 ``k_scale`` / ``v_scale`` [Hkv].  Rows
+    with position -1 are skipped.  ``q_out`` may be ``q``."""
+    with _allocating_on(stream, k.device):
+        call = PreparedAppendKV(q, k, v, cos_sin, positions, slots, k_cache, v_cache, interleaved,
+                                k_scale, v_scale, q_out)
+        call.run(stream)
+    return call.q_out
+
+
+def mla_decode_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: int, batch: int,
+                               page_size: int, max_pages: int, dtype=torch.bfloat16,
+                               cache_dtype=None) -> int:
+    geom = KVGeometry(num_heads, num_kv_heads, head_dim, 0.0, DTYPES[dtype],
+                      CACHE_DTYPES[cache_dtype if cache_dtype is not None else dtype])
+    out = ctypes.c_size_t(0)
+    _check(lib().mla_decode_workspace_bytes(ctypes.byref(geom), batch, page_size, max_pages,
+                                            ctypes.byref(out)), "mla_decode_workspace_bytes")
+    return out.value
+
+
+class PreparedDecodeAttention(_PreparedCall):
+    """mla_decode_attention with its arguments marshalled once, for a decode loop
+    over fixed buffers (lengths and tables are read on the device, so they may
+    change between runs and under a captured graph); ``run()`` issues it,
+    ``out`` and ``lse`` are its outputs.  The tensors must outlive the
+    object."""
+
+    def __init__(self, q, k_cache, v_cache, cache_lens, page_table, window: int = 0,
+                 scale: Optional[float] = None, k_scale=None, v_scale=None, out=None, lse=None,
+                 return_lse: bool = False, workspace=None):
+        B, H, D, qs = _head_rows("q", q)
+        _tensor("k_cache", k_cache, (None, None, None, D), dense=False)
+        Hk = k_cache.shape[2]
+        cache = _kv_cache(k_cache, v_cache, q.dtype, Hk, D, k_scale, v_scale)
+        _tensor("cache_lens", cache_lens, (B,), torch.int32)
+        _tensor("page_table", page_table, (B, None), torch.int32)
+        if out is not None:
+            _tensor("out", out, (B, H, D), q.dtype)
+        if lse is not None:
+            _tensor("lse", lse, (B, H), torch.float32)
+        if workspace is not None:
+            _tensor("workspace", workspace)
+        dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, cache_lens=cache_lens,
+                          page_table=page_table, k_scale=k_scale, v_scale=v_scale, out=out,
+                          lse=lse, workspace=workspace)
+        geom = KVGeometry(H, Hk, D, float(scale) if scale is not None else 0.0, DTYPES[q.dtype],
+                          CACHE_DTYPES[k_cache.dtype])
+        made = []
+        if out is None:
+            out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
+            made.append(out)
+        if lse is None and return_lse:
+            lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+            made.append(lse)
+        if workspace is None:
+            nbytes = ctypes.c_size_t(0)
+            with torch.cuda.device(dev):
+                _check(lib().mla_decode_workspace_bytes(
+                    ctypes.byref(geom), B, k_cache.shape[1], page_table.shape[1],
+                    ctypes.byref(nbytes)), "mla_decode_workspace_bytes")
+            workspace = new_workspace(nbytes.value, dev)
+            made.append(workspace)
+        self.out, self.lse = out, lse
+        args = [ctypes.byref(geom), _ptr(q), qs, ctypes.byref(cache), _ptr(cache_lens), B,
+                _ptr(page_table), page_table.shape[1], int(window), _ptr(out), _ptr(lse),
+                _ptr(workspace), workspace.numel() * workspace.element_size()]
+        keep = (geom, cache, q, k_cache, v_cache, cache_lens, page_table, k_scale, v_scale, out,
+                lse, workspace)
+        self._prepare("mla_decode_attention", args, dev, keep, made)
+
+
+def mla_decode_attention(q, k_cache, v_cache, cache_lens, page_table, window: int = 0,
+                         scale: Optional[float] = None, k_scale=None, v_scale=None, out=None,
+                         lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged key/value cache.
+    Returns out, or (out, lse) with ``return_lse`` or ``lse``.
+
+    ``q`` [B, H, D]; caches [num_pages, page_size, Hkv, D] in any stride order
+    (see mla_append_kv), of q's type or float8_e4m3fn; ``cache_lens`` int32 [B]
+    on the device, the new token included (0: an idle slot, zeros come back);
+    ``page_table`` int32 [B, max_pages]; ``window`` > 0 keeps the last
+    ``window`` positions."""
+    with _allocating_on(stream, q.device):
+        call = PreparedDecodeAttention(q, k_cache, v_cache, cache_lens, page_table, window, scale,
+                                       k_scale, v_scale, out, lse, return_lse, workspace)
+        call.run(stream)
+    return (call.out, call.lse) if call.lse is not None else call.out

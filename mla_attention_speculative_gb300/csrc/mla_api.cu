@@ -82,7 +82,7 @@ namespace mla {
 // Validation and planning
 // ---------------------------------------------------------------------------
 
-static bool geometry_ok(const mla_geometry_t* g) {
+bool geometry_ok(const mla_geometry_t* g) {
   if (g == nullptr) { set_error("geometry is NULL"); return false; }
   if (g->num_heads < 1 || g->kv_lora_rank < 1 || g->qk_nope_dim < 1 || g->v_dim < 1 ||
       g->rope_dim < 0) {
@@ -640,9 +640,10 @@ extern "C" const char* mla_status_string(int32_t s) {
 extern "C" const char* mla_last_error(void) { return g_err; }
 
 extern "C" mla_status_t mla_device_status(int32_t* code, int32_t clear) {
-  const int words[5] = {absorbed_device_status(clear != 0), materialised_device_status(clear != 0),
+  const int words[7] = {absorbed_device_status(clear != 0), materialised_device_status(clear != 0),
                         generic_device_status(clear != 0), selftest_device_status(clear != 0),
-                        indexer_device_status(clear != 0)};
+                        indexer_device_status(clear != 0), paged_device_status(clear != 0),
+                        decode_device_status(clear != 0)};
   int v = 0;
   for (int w : words) {
     if (w < 0) {
@@ -658,7 +659,7 @@ extern "C" mla_status_t mla_device_status(int32_t* code, int32_t clear) {
   }
   if (v >= kBadPageSite) {
     set_error("a kernel met a page id outside [0, num_pages) (site %d); the positions of that "
-              "page read as zeros",
+              "page read as zeros, or got no slot",
               v);
     return MLA_ERR_INVALID_ARG;
   }
@@ -678,4 +679,4 @@ extern "C" mla_status_t mla_selftest_bounded_wait(void* stream) {
   return MLA_OK;
 }
 
-extern "C" int32_t mla_version(void) { return 100; }
+extern "C" int32_t mla_version(void) { return 101; }

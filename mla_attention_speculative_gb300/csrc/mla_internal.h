@@ -134,6 +134,17 @@ int materialised_device_status(bool clear);
 // Status word of the indexer kernels (0 = no wait ran out); synchronises.
 int indexer_device_status(bool clear);
 
+// Status words of the paged-cache kernels (page step) and of the decode
+// attention (kBadPageSite or 0); they synchronise.
+int paged_device_status(bool clear);
+int decode_device_status(bool clear);
+
+// Argument checks shared by the entry points; false / a failing status means
+// set_error() has said why.
+bool geometry_ok(const mla_geometry_t* g);
+mla_status_t kv_geometry_ok(const mla_kv_geometry_t* g);
+mla_status_t kv_cache_ok(const mla_kv_geometry_t* g, const mla_kv_cache_t* c);
+
 // Records a one-line failure description for mla_last_error().
 void set_error(const char* fmt, ...);
 

@@ -1,0 +1,852 @@
+// The paged-cache side of a serving step: page tables and slots built on the
+// GPU (mla_page_step), and the step's rows written into the latent cache
+// (mla_append_latent) or a key/value cache (mla_append_kv).
+//
+// None of these triggers the next kernel early, so a verify or decode call
+// that follows (and may read the cache before its own wait) starts after the
+// rows are in place.
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <climits>
+#include <type_traits>
+
+#include "mla_internal.h"
+
+namespace mla {
+
+static __device__ int g_paged_status;
+
+int paged_device_status(bool clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_paged_status, sizeof(int)) != cudaSuccess) return -1;
+  if (clear && v != 0) {
+    const int z = 0;
+    if (cudaMemcpyToSymbol(g_paged_status, &z, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
+}
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Page step
+// ---------------------------------------------------------------------------
+//
+// Two exclusive sums over the sequences (rows, pages asked for) place every
+// row and every new page; the rest is one lookup per row.  Each CTA computes
+// both sums itself, 2048 sequences at a time, so no CTA waits for another:
+// the counts (12 bytes a sequence) stay in L2, and a step has far more rows
+// than sequences or is bound by launch latency anyway.  The rows are split
+// over the CTAs evenly, whatever their sequences; a row finds its sequence by
+// a binary search over the sums in shared memory.  New pages are read from
+// the free list by position, never from the table that this launch writes.
+
+constexpr int kStepThreads = 512;
+constexpr int kSeqPerThread = 4;
+constexpr int kSeqPerPass = kStepThreads * kSeqPerThread;
+constexpr int kRowsPerThread = 4;
+
+struct PageStepParams {
+  const int32_t* kept;
+  const int32_t* fresh;
+  const int32_t* held;
+  int32_t* table;
+  const int32_t* free_pages;
+  const int32_t* free_span;
+  int32_t* lens_out;
+  int32_t* held_out;
+  int32_t* row_start;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* span_out;
+  int32_t* missing;
+  int batch, width, page, num_pages, free_capacity, max_rows;
+  int rows_per_cta;
+};
+
+struct Pair64 {
+  long long rows, pages;
+};
+
+__device__ __forceinline__ int sat32(long long x) { return x > INT_MAX ? INT_MAX : (int)x; }
+
+// The pages sequence b asks for, and its (clamped) counts.
+__device__ __forceinline__ void sequence_counts(const PageStepParams& p, int b, int& kept,
+                                                int& fresh, int& held, int& grow) {
+  kept = max(p.kept[b], 0);
+  fresh = max(p.fresh[b], 0);
+  held = min(max(p.held[b], 0), p.width);
+  const long long total = min((long long)kept + fresh, (long long)p.width * p.page);
+  const int need = (int)((total + p.page - 1) / p.page);
+  grow = max(0, need - held);
+}
+
+__global__ void __launch_bounds__(kStepThreads) page_step_kernel(PageStepParams p) {
+  __shared__ long long s_row[kSeqPerPass + 1];   // first row of each sequence
+  __shared__ int s_base[kSeqPerPass + 1];        // pages asked for before it
+  __shared__ int s_kept[kSeqPerPass];
+  __shared__ int s_held[kSeqPerPass];
+  __shared__ Pair64 s_warp[kStepThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int first = min(max(p.free_span[0], 0), p.free_capacity);
+  const int end = min(max(p.free_span[1], first), p.free_capacity);
+  const int have = end - first;
+  const long long r0 = (long long)blockIdx.x * p.rows_per_cta;
+  const long long r1 = min(r0 + p.rows_per_cta, (long long)p.max_rows);
+  Pair64 carry = {0, 0};
+
+  for (int b0 = 0; b0 < p.batch; b0 += kSeqPerPass) {
+    const int nb = min(kSeqPerPass, p.batch - b0);
+    int kept[kSeqPerThread], fresh[kSeqPerThread], held[kSeqPerThread], grow[kSeqPerThread];
+    Pair64 mine = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kSeqPerThread; ++i) {
+      const int s = tid * kSeqPerThread + i;
+      kept[i] = fresh[i] = held[i] = grow[i] = 0;
+      if (s < nb) sequence_counts(p, b0 + s, kept[i], fresh[i], held[i], grow[i]);
+      mine.rows += fresh[i];
+      mine.pages += grow[i];
+    }
+    Pair64 sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long r = __shfl_up_sync(~0u, sum.rows, o);
+      const long long g = __shfl_up_sync(~0u, sum.pages, o);
+      if (lane >= o) {
+        sum.rows += r;
+        sum.pages += g;
+      }
+    }
+    __syncthreads();  // the previous pass has read the arrays
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    Pair64 base = carry;
+    for (int w = 0; w < kStepThreads / 32; ++w) {
+      const Pair64 x = s_warp[w];
+      if (w < warp) {
+        base.rows += x.rows;
+        base.pages += x.pages;
+      }
+      carry.rows += x.rows;
+      carry.pages += x.pages;
+    }
+    base.rows += sum.rows - mine.rows;
+    base.pages += sum.pages - mine.pages;
+    // (batch * width < 2^31, so the pages asked for fit an int)
+#pragma unroll
+    for (int i = 0; i < kSeqPerThread; ++i) {
+      const int s = tid * kSeqPerThread + i;
+      if (s < nb) {
+        s_row[s] = base.rows;
+        s_base[s] = (int)base.pages;
+        s_kept[s] = kept[i];
+        s_held[s] = held[i];
+        if ((b0 / kSeqPerPass) % gridDim.x == blockIdx.x) {
+          const int got = min(grow[i], max(0, have - (int)base.pages));
+          const int b = b0 + s;
+          const long long total = min((long long)kept[i] + fresh[i], (long long)p.width * p.page);
+          p.held_out[b] = held[i] + got;
+          p.lens_out[b] = (int)min(min(total, (long long)(held[i] + got) * p.page),
+                                   (long long)INT_MAX);
+          p.row_start[b] = sat32(base.rows);
+        }
+      }
+      base.rows += fresh[i];
+      base.pages += grow[i];
+    }
+    if (tid == 0) {
+      s_row[nb] = carry.rows;
+      s_base[nb] = (int)carry.pages;
+    }
+    __syncthreads();
+
+    // new table entries: a warp per sequence, the sequences dealt over all warps
+    for (int s = blockIdx.x * (kStepThreads / 32) + warp; s < nb;
+         s += gridDim.x * (kStepThreads / 32)) {
+      const int got = min(s_base[s + 1] - s_base[s], max(0, have - s_base[s]));
+      const int32_t* src = p.free_pages + first + s_base[s];
+      int32_t* dst = p.table + (long long)(b0 + s) * p.width + s_held[s];
+      for (int j = lane; j < got; j += 32) dst[j] = src[j];
+    }
+
+    // this CTA's rows among the pass's sequences, four consecutive rows a thread
+    const long long lo = max(r0, s_row[0]), hi = min(r1, s_row[nb]);
+    const long long start = lo & ~(long long)(kRowsPerThread - 1);
+    for (long long g = start + tid * kRowsPerThread; g < hi;
+         g += kStepThreads * kRowsPerThread) {
+      const long long from = max(g, lo), to = min(g + kRowsPerThread, hi);
+      int a = 0, z = nb;  // the last sequence whose first row is at or before `from`
+      while (z - a > 1) {
+        const int m = (a + z) >> 1;
+        if (s_row[m] <= from) a = m; else z = m;
+      }
+      int pos4[kRowsPerThread];
+      long long slot4[kRowsPerThread];
+#pragma unroll
+      for (int i = 0; i < kRowsPerThread; ++i) {
+        const long long row = g + i;
+        pos4[i] = -1;
+        slot4[i] = -1;
+        if (row < from || row >= to) continue;
+        while (row >= s_row[a + 1]) ++a;
+        const long long pos = s_kept[a] + (row - s_row[a]);
+        pos4[i] = sat32(pos);
+        const long long page_no = (pos >> 32) == 0
+                                      ? (long long)((uint32_t)pos / (uint32_t)p.page)
+                                      : pos / p.page;
+        const int off = (int)(pos - page_no * p.page);
+        const int have_pages =
+            s_held[a] + min(s_base[a + 1] - s_base[a], max(0, have - s_base[a]));
+        if (page_no < have_pages) {
+          const int j = (int)page_no;
+          const int id = j < s_held[a]
+                             ? p.table[(long long)(b0 + a) * p.width + j]
+                             : p.free_pages[first + s_base[a] + (j - s_held[a])];
+          if (id >= 0 && id < p.num_pages) {
+            slot4[i] = (long long)id * p.page + off;
+          } else {
+            atomicCAS(&g_paged_status, 0, kBadPageSite);
+          }
+        }
+      }
+      if (from == g && to == g + kRowsPerThread) {
+        *reinterpret_cast<int4*>(p.positions + g) = make_int4(pos4[0], pos4[1], pos4[2], pos4[3]);
+        longlong2* d = reinterpret_cast<longlong2*>(p.slots + g);
+        d[0] = make_longlong2(slot4[0], slot4[1]);
+        d[1] = make_longlong2(slot4[2], slot4[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRowsPerThread; ++i) {
+          if (g + i < from || g + i >= to) continue;
+          p.positions[g + i] = pos4[i];
+          p.slots[g + i] = slot4[i];
+        }
+      }
+    }
+  }
+
+  // rows behind the last sequence
+  for (long long row = max(r0, carry.rows) + tid; row < r1; row += kStepThreads) {
+    p.positions[row] = -1;
+    p.slots[row] = -1;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    p.row_start[p.batch] = sat32(carry.rows);
+    const int taken = (int)min(carry.pages, (long long)have);
+    p.span_out[0] = first + taken;
+    p.span_out[1] = end;
+    p.missing[0] = sat32(carry.pages - taken);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows into the caches
+// ---------------------------------------------------------------------------
+//
+// Both appends only move data (a row's heads in, the same bytes out, a few
+// multiplications between), so they are bound by memory.  A thread moves two
+// 16-byte vectors at a time: the two that a rotation mixes (vector i and i +
+// half of the rotated part, or two neighbours when pairs are interleaved), so
+// the rotation needs no exchange between threads and reads the same run of
+// cosines and sines in both forms.  A thread keeps its place within the head
+// and walks over heads, so the row's cosines and sines are loaded once.
+
+template <typename T>
+struct Vec {
+  static constexpr int N = 16 / (int)sizeof(T);
+  float v[N];
+};
+
+__device__ __forceinline__ void load_vec(const float* p, Vec<float>& x) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  x.v[0] = a.x; x.v[1] = a.y; x.v[2] = a.z; x.v[3] = a.w;
+}
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, Vec<__nv_bfloat16>& x) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.v[2 * i] = __uint_as_float(w[i] << 16);
+    x.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void store_vec(float* p, const Vec<float>& x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+}
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const Vec<__nv_bfloat16>& x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[2 * i], x.v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Eight values as e4m3, saturating (NaN stays NaN).
+__device__ __forceinline__ void store_vec(__nv_fp8_e4m3* p, const Vec<__nv_bfloat16>& x) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x.v[4 * i], x.v[4 * i + 1]),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x.v[4 * i + 2], x.v[4 * i + 3]),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | (hi << 16);
+  }
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+// The cosines and sines of one item: Vec::N angles.
+template <typename T>
+struct Angles {
+  static constexpr int N = Vec<T>::N;
+  float c[N], s[N];
+  __device__ __forceinline__ void load(const float* table, long long row, int rope, int item) {
+    const float* p = table + row * rope + item * N;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p + i);
+      const float4 b = *reinterpret_cast<const float4*>(p + rope / 2 + i);
+      c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
+      s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
+    }
+  }
+  __device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, bool interleaved) const {
+    if (interleaved) {  // pairs within the two neighbouring vectors
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        Vec<T>& z = i < N / 2 ? x : y;
+        const int k = 2 * (i % (N / 2));
+        const float a = z.v[k], b = z.v[k + 1];
+        z.v[k] = fmaf(a, c[i], -(b * s[i]));
+        z.v[k + 1] = fmaf(b, c[i], a * s[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float a = x.v[i], b = y.v[i];
+        x.v[i] = fmaf(a, c[i], -(b * s[i]));
+        y.v[i] = fmaf(b, c[i], a * s[i]);
+      }
+    }
+  }
+};
+
+// The two vectors of item i of a head: `turned` rotated items first (the
+// rotated part starts at vector `rot0`), then pairs of the `rest` others from
+// vector `rest0`.  v1 < 0: the item has one vector only.
+__device__ __forceinline__ void item_vectors(int i, int turned, int rot0, int rest0, int rest,
+                                             bool interleaved, int& v0, int& v1) {
+  if (i < turned) {
+    v0 = rot0 + (interleaved ? 2 * i : i);
+    v1 = interleaved ? v0 + 1 : v0 + turned;
+  } else {
+    const int j = 2 * (i - turned);
+    v0 = rest0 + j;
+    v1 = j + 1 < rest ? v0 + 1 : -1;
+  }
+}
+
+struct AppendKVParams {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int64_t* slots;
+  void* q_out;
+  void *k_cache, *v_cache;
+  int64_t page_stride, row_stride, head_stride, cache_rows;
+  const float *k_scale, *v_scale;
+  int page, table_rows, rope, interleaved;
+  int q_heads, kv_heads, dim;  // q_heads 0: the cache only
+  int items, turned, heads_per_cta;
+};
+
+template <typename T, typename CT>
+__global__ void __launch_bounds__(256) append_kv_kernel(AppendKVParams p) {
+  constexpr int N = Vec<T>::N;
+  const long long row = blockIdx.x;
+  const int pos = p.positions[row];
+  if (pos < 0 || (p.rope > 0 && pos >= p.table_rows)) return;
+  const int64_t slot = p.slots[row];
+  const bool cached = slot >= 0 && slot < p.cache_rows;
+  int64_t at = 0;
+  if (cached) {
+    const int64_t pg = (slot >> 32) == 0 ? (int64_t)((uint32_t)slot / (uint32_t)p.page)
+                                         : slot / p.page;
+    at = pg * p.page_stride + (slot - pg * p.page) * p.row_stride;
+  }
+  const int item = threadIdx.x;
+  int v0, v1;
+  item_vectors(item, p.turned, 0, 2 * p.turned, p.dim / N - 2 * p.turned, p.interleaved != 0, v0,
+               v1);
+  Angles<T> ang;
+  if (item < p.turned) ang.load(p.cos_sin, pos, p.rope, item);
+  const int heads = p.q_heads + 2 * p.kv_heads;
+  const int h1 = min(heads, (int)(blockIdx.y + 1) * p.heads_per_cta);
+#pragma unroll 2
+  for (int h = blockIdx.y * p.heads_per_cta + threadIdx.y; h < h1; h += blockDim.y) {
+    const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
+    const int hk = is_q ? 0 : is_k ? h - p.q_heads : h - p.q_heads - p.kv_heads;
+    if (!is_q && !cached) continue;
+    const T* src = is_q ? (const T*)p.q + row * p.q_stride + (int64_t)h * p.dim
+                 : is_k ? (const T*)p.k + row * p.k_stride + (int64_t)hk * p.dim
+                        : (const T*)p.v + row * p.v_stride + (int64_t)hk * p.dim;
+    Vec<T> x, y;
+    load_vec(src + v0 * N, x);
+    if (v1 >= 0) load_vec(src + v1 * N, y);
+    if (item < p.turned && (is_q || is_k)) ang.turn(x, y, p.interleaved != 0);
+    if (is_q) {
+      T* dst = (T*)p.q_out + (row * p.q_heads + h) * p.dim;
+      store_vec(dst + v0 * N, x);
+      if (v1 >= 0) store_vec(dst + v1 * N, y);
+    } else {
+      CT* dst = (CT*)(is_k ? p.k_cache : p.v_cache) + at + hk * p.head_stride;
+      if constexpr (sizeof(CT) == 1) {
+        const float* sc = is_k ? p.k_scale : p.v_scale;
+        if (sc) {
+          const float s = sc[hk];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            x.v[i] = __fdiv_rn(x.v[i], s);
+            if (v1 >= 0) y.v[i] = __fdiv_rn(y.v[i], s);
+          }
+        }
+      }
+      store_vec(dst + v0 * N, x);
+      if (v1 >= 0) store_vec(dst + v1 * N, y);
+    }
+  }
+}
+
+struct AppendLatentParams {
+  const void *q, *kv, *weight;
+  int64_t q_stride, kv_stride;
+  float eps;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int64_t* slots;
+  void *q_nope, *q_rope, *c_kv, *k_rope;
+  int64_t ckv_stride, kr_stride, cache_rows;
+  int table_rows, interleaved;
+  int heads, rank, nope, rope;
+  int items, turned, heads_per_cta;
+};
+
+// CTAs (row, 0): the row's latent, normed, and its key, rotated, into the
+// cache.  CTAs (row, y > 0): a run of the row's query heads.
+template <typename T>
+__global__ void __launch_bounds__(256) append_latent_kernel(AppendLatentParams p) {
+  constexpr int N = Vec<T>::N;
+  const long long row = blockIdx.x;
+  const int pos = p.positions[row];
+  if (pos < 0 || pos >= p.table_rows) return;
+  if (blockIdx.y > 0) {
+    const int item = threadIdx.x;
+    int v0, v1;
+    item_vectors(item, p.turned, p.nope / N, 0, p.nope / N, p.interleaved != 0, v0, v1);
+    Angles<T> ang;
+    if (item < p.turned) ang.load(p.cos_sin, pos, p.rope, item);
+    const int h1 = min(p.heads, (int)blockIdx.y * p.heads_per_cta);
+#pragma unroll 2
+    for (int h = (blockIdx.y - 1) * p.heads_per_cta + threadIdx.y; h < h1; h += blockDim.y) {
+      const T* src = (const T*)p.q + row * p.q_stride + (int64_t)h * (p.nope + p.rope);
+      const int64_t head = row * p.heads + h;
+      Vec<T> x, y;
+      load_vec(src + v0 * N, x);
+      if (v1 >= 0) load_vec(src + v1 * N, y);
+      T* dst = (T*)p.q_nope + head * p.nope;
+      if (item < p.turned) {
+        ang.turn(x, y, p.interleaved != 0);
+        dst = (T*)p.q_rope + head * p.rope - p.nope;
+      }
+      store_vec(dst + v0 * N, x);
+      if (v1 >= 0) store_vec(dst + v1 * N, y);
+    }
+    return;
+  }
+  const int64_t slot = p.slots[row];
+  if (slot < 0 || slot >= p.cache_rows) return;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, nt = blockDim.x * blockDim.y;
+  const T* src = (const T*)p.kv + row * p.kv_stride;
+  T* c = (T*)p.c_kv + slot * p.ckv_stride;
+  T* kr = (T*)p.k_rope + slot * p.kr_stride;
+  const int nv = p.rank / N;
+  // rank <= 1024 is at most 256 vectors; a CTA has 64 threads or more
+  constexpr int kMost = 4;
+  Vec<T> x[kMost];
+  float sum = 0.f;
+#pragma unroll
+  for (int m = 0; m < kMost; ++m) {
+    const int i = tid + m * nt;
+    if (i >= nv) break;
+    load_vec(src + i * N, x[m]);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum = fmaf(x[m].v[e], x[m].v[e], sum);
+  }
+  float scale = 1.f;
+  if (p.weight) {
+    __shared__ float part[8];
+    // the last warp may be partial: only its live lanes take part
+    const int left = nt - (tid & ~31);
+    const unsigned mask = left >= 32 ? ~0u : (1u << left) - 1u;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float other = __shfl_down_sync(mask, sum, o);
+      if ((tid & 31) + o < left) sum += other;
+    }
+    if ((tid & 31) == 0) part[tid >> 5] = sum;
+    __syncthreads();
+    float all = 0.f;
+    for (int w = 0; w < (nt + 31) / 32; ++w) all += part[w];
+    scale = __frsqrt_rn(all / p.rank + p.eps);
+  }
+#pragma unroll
+  for (int m = 0; m < kMost; ++m) {
+    const int i = tid + m * nt;
+    if (i >= nv) break;
+    if (p.weight) {
+      Vec<T> w;
+      load_vec((const T*)p.weight + i * N, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[m].v[e] = x[m].v[e] * scale * w.v[e];
+    }
+    store_vec(c + i * N, x[m]);
+  }
+  for (int i = nt - 1 - tid; i < p.turned; i += nt) {
+    int v0, v1;
+    item_vectors(i, p.turned, nv, 0, 0, p.interleaved != 0, v0, v1);
+    Angles<T> ang;
+    ang.load(p.cos_sin, pos, p.rope, i);
+    Vec<T> a, b;
+    load_vec(src + v0 * N, a);
+    load_vec(src + v1 * N, b);
+    ang.turn(a, b, p.interleaved != 0);
+    store_vec(kr + (v0 - nv) * N, a);
+    store_vec(kr + (v1 - nv) * N, b);
+  }
+}
+
+bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
+
+struct Named {
+  const void* p;
+  const char* name;
+  bool optional;
+};
+
+mla_status_t check_pointers(const char* what, const Named* list, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (list[i].p == nullptr) {
+      if (list[i].optional) continue;
+      set_error("%s: %s is NULL", what, list[i].name);
+      return MLA_ERR_INVALID_ARG;
+    }
+    if (misaligned(list[i].p)) {
+      set_error("%s: %s is not 16-byte aligned", what, list[i].name);
+      return MLA_ERR_INVALID_ARG;
+    }
+  }
+  return MLA_OK;
+}
+
+mla_status_t launched(cudaError_t e) {
+  if (e == cudaSuccess) return MLA_OK;
+  set_error("CUDA error %d (%s)", (int)e, cudaGetErrorString(e));
+  return MLA_ERR_CUDA;
+}
+
+struct Range {
+  uintptr_t lo, hi;
+};
+Range range(const void* p, int64_t bytes) {
+  return {(uintptr_t)p, (uintptr_t)p + (uintptr_t)(p ? bytes : 0)};
+}
+bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Threads of an append: blockDim.x items of a head, blockDim.y heads.
+dim3 item_block(int items) { return dim3((unsigned)items, (unsigned)(128 / items < 1 ? 1 : 128 / items)); }
+
+// Heads per CTA: one head per thread when the rows are few (the more CTAs the
+// better), up to four, which share one load of the cosines, when there are
+// enough rows to fill the machine anyway.
+int heads_per_cta(int heads, int by, int rows) {
+  const int64_t fill = (int64_t)device_sm_count() * 16;
+  int k = 1;
+  while (k < 4 && (int64_t)rows * ((heads + 2 * k * by - 1) / (2 * k * by)) >= fill) k *= 2;
+  return k * by;
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status_t mla_page_step(
+    const int32_t* kept_lens, const int32_t* new_tokens, const int32_t* held_pages, int32_t batch,
+    int32_t* page_table, int32_t max_pages_per_seq, int32_t page_size, int32_t num_pages,
+    const int32_t* free_pages, int32_t free_capacity, const int32_t* free_span,
+    int32_t* cache_lens_out, int32_t* held_pages_out, int32_t* row_start_out,
+    int32_t* positions_out, int64_t* slots_out, int32_t max_rows, int32_t* free_span_out,
+    int32_t* missing_out, void* stream) {
+  if (batch < 1 || batch > 65535 || max_pages_per_seq < 1 || page_size < 1 || num_pages < 1 ||
+      free_capacity < 0 || max_rows < 0 || (int64_t)batch * max_pages_per_seq > INT_MAX) {
+    set_error("page step: need 1 <= batch <= 65535, max_pages_per_seq, page_size and num_pages "
+              ">= 1, batch * max_pages_per_seq < 2^31, free_capacity and max_rows >= 0 "
+              "(batch=%d max_pages=%d page_size=%d num_pages=%d free=%d rows=%d)",
+              batch, max_pages_per_seq, page_size, num_pages, free_capacity, max_rows);
+    return MLA_ERR_INVALID_ARG;
+  }
+  const Named ptrs[] = {{kept_lens, "kept_lens", false},
+                        {new_tokens, "new_tokens", false},
+                        {held_pages, "held_pages", false},
+                        {page_table, "page_table", false},
+                        {free_pages, "free_pages", free_capacity == 0},
+                        {free_span, "free_span", false},
+                        {cache_lens_out, "cache_lens_out", false},
+                        {held_pages_out, "held_pages_out", false},
+                        {row_start_out, "row_start_out", false},
+                        {positions_out, "positions_out", max_rows == 0},
+                        {slots_out, "slots_out", max_rows == 0},
+                        {free_span_out, "free_span_out", false},
+                        {missing_out, "missing_out", false}};
+  mla_status_t st = check_pointers("page step", ptrs, 13);
+  if (st != MLA_OK) return st;
+  const int64_t seqs = (int64_t)batch * 4;
+  const Range in[] = {range(kept_lens, seqs), range(new_tokens, seqs), range(held_pages, seqs),
+                      range(free_pages, (int64_t)free_capacity * 4), range(free_span, 8)};
+  const Range out[] = {range(page_table, (int64_t)batch * max_pages_per_seq * 4),
+                       range(cache_lens_out, seqs), range(held_pages_out, seqs),
+                       range(row_start_out, seqs + 4), range(positions_out, (int64_t)max_rows * 4),
+                       range(slots_out, (int64_t)max_rows * 8), range(free_span_out, 8),
+                       range(missing_out, 4)};
+  for (int i = 0; i < 8; ++i) {
+    bool bad = false;
+    for (const Range& r : in) bad = bad || overlap(out[i], r);
+    for (int j = 0; j < i; ++j) bad = bad || overlap(out[i], out[j]);
+    if (bad) {
+      set_error("page step: an output overlaps another buffer of the call");
+      return MLA_ERR_INVALID_ARG;
+    }
+  }
+  PageStepParams p;
+  p.kept = kept_lens;
+  p.fresh = new_tokens;
+  p.held = held_pages;
+  p.table = page_table;
+  p.free_pages = free_pages;
+  p.free_span = free_span;
+  p.lens_out = cache_lens_out;
+  p.held_out = held_pages_out;
+  p.row_start = row_start_out;
+  p.positions = positions_out;
+  p.slots = slots_out;
+  p.span_out = free_span_out;
+  p.missing = missing_out;
+  p.batch = batch;
+  p.width = max_pages_per_seq;
+  p.page = page_size;
+  p.num_pages = num_pages;
+  p.free_capacity = free_capacity;
+  p.max_rows = max_rows;
+  // one pass of every thread over its rows, or two CTAs per SM with longer walks
+  const int64_t per_pass = kStepThreads * kRowsPerThread;
+  int64_t ctas = ((int64_t)max_rows + per_pass - 1) / per_pass;
+  const int64_t most = 2 * (int64_t)device_sm_count();
+  if (ctas > most) ctas = most;
+  if (ctas < 1) ctas = 1;
+  const int64_t share = ((int64_t)max_rows + ctas - 1) / ctas;
+  p.rows_per_cta = (int)((share + 3) / 4 * 4);
+  const cudaStream_t s = (cudaStream_t)stream;
+  {
+    KernelTimer kt("page_step", s);
+    page_step_kernel<<<(unsigned)ctas, kStepThreads, 0, s>>>(p);
+  }
+  return launched(cudaGetLastError());
+}
+
+extern "C" mla_status_t mla_append_latent(
+    const mla_geometry_t* g, const void* q, int64_t q_row_stride, const void* kv,
+    int64_t kv_row_stride, const void* norm_weight, float eps, const float* cos_sin,
+    int32_t table_rows, int32_t interleaved, const int32_t* positions, const int64_t* slots,
+    int32_t rows, void* q_nope, void* q_rope, void* c_kv, void* k_rope, int64_t c_kv_row_stride,
+    int64_t k_rope_row_stride, int64_t cache_rows, void* stream) {
+  if (!geometry_ok(g)) return MLA_ERR_INVALID_ARG;
+  const int eb = g->dtype == MLA_DTYPE_BF16 ? 2 : 4;
+  const int H = g->num_heads, r = g->kv_lora_rank, n = g->qk_nope_dim, d = g->rope_dim;
+  if (d < 16 || d % 16 != 0) {
+    set_error("append latent: rope_dim %d is not a positive multiple of 16", d);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (rows < 0 || table_rows < 1 || cache_rows < 1 || !(eps >= 0.f)) {
+    set_error("append latent: need rows >= 0, table_rows and cache_rows >= 1, eps >= 0 (rows=%d "
+              "table_rows=%d cache_rows=%lld)", rows, table_rows, (long long)cache_rows);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (rows == 0) return MLA_OK;
+  const bool no_q = q == nullptr;
+  const Named ptrs[] = {{q, "q", true},
+                        {kv, "kv", false},
+                        {norm_weight, "norm_weight", true},
+                        {cos_sin, "cos_sin", false},
+                        {positions, "positions", false},
+                        {slots, "slots", false},
+                        {q_nope, "q_nope", no_q},
+                        {q_rope, "q_rope", no_q},
+                        {c_kv, "c_kv", false},
+                        {k_rope, "k_rope", false}};
+  mla_status_t st = check_pointers("append latent", ptrs, 10);
+  if (st != MLA_OK) return st;
+  const int64_t strides[] = {q_row_stride, kv_row_stride, c_kv_row_stride, k_rope_row_stride};
+  const int64_t least[] = {(int64_t)H * (n + d), r + d, r, d};
+  const char* names[] = {"q_row_stride", "kv_row_stride", "c_kv_row_stride", "k_rope_row_stride"};
+  for (int i = no_q ? 1 : 0; i < 4; ++i) {
+    if (strides[i] < least[i] || strides[i] * eb % 16 != 0) {
+      set_error("append latent: %s %lld must be at least %lld and a multiple of 16 bytes",
+                names[i], (long long)strides[i], (long long)least[i]);
+      return MLA_ERR_INVALID_ARG;
+    }
+  }
+  AppendLatentParams p;
+  p.q = q;
+  p.kv = kv;
+  p.weight = norm_weight;
+  p.q_stride = q_row_stride;
+  p.kv_stride = kv_row_stride;
+  p.eps = eps;
+  p.cos_sin = cos_sin;
+  p.positions = positions;
+  p.slots = slots;
+  p.q_nope = q_nope;
+  p.q_rope = q_rope;
+  p.c_kv = c_kv;
+  p.k_rope = k_rope;
+  p.ckv_stride = c_kv_row_stride;
+  p.kr_stride = k_rope_row_stride;
+  p.cache_rows = cache_rows;
+  p.table_rows = table_rows;
+  p.interleaved = interleaved;
+  p.heads = H;
+  p.rank = r;
+  p.nope = n;
+  p.rope = d;
+  const int N = 16 / eb;
+  p.turned = d / 2 / N;
+  p.items = p.turned + (n / N + 1) / 2;
+  const dim3 block = item_block(p.items);
+  p.heads_per_cta = heads_per_cta(H, (int)block.y, rows);
+  const unsigned head_ctas = no_q ? 0u : (unsigned)((H + p.heads_per_cta - 1) / p.heads_per_cta);
+  const dim3 grid((unsigned)rows, 1 + head_ctas);
+  if (grid.y > 65535u) {
+    set_error("append latent: %d heads are too many", H);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  {
+    KernelTimer kt("append_latent", s);
+    if (eb == 2) append_latent_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(p);
+    else append_latent_kernel<float><<<grid, block, 0, s>>>(p);
+  }
+  return launched(cudaGetLastError());
+}
+
+extern "C" mla_status_t mla_append_kv(
+    const mla_kv_geometry_t* g, const void* q, int64_t q_row_stride, const void* k,
+    int64_t k_row_stride, const void* v, int64_t v_row_stride, const float* cos_sin,
+    int32_t table_rows, int32_t rope_dim, int32_t interleaved, const int32_t* positions,
+    const int64_t* slots, int32_t rows, void* q_out, const mla_kv_cache_t* cache, void* stream) {
+  mla_status_t st = kv_geometry_ok(g);
+  if (st != MLA_OK) return st;
+  st = kv_cache_ok(g, cache);
+  if (st != MLA_OK) return st;
+  const int eb = g->dtype == MLA_DTYPE_BF16 ? 2 : 4;
+  const int H = g->num_heads, Hk = g->num_kv_heads, D = g->head_dim;
+  if (rows < 0 || rope_dim < 0 || rope_dim > D || rope_dim % 16 != 0 ||
+      (rope_dim > 0 && table_rows < 1)) {
+    set_error("append kv: need rows >= 0, rope_dim a multiple of 16 up to head_dim, table_rows "
+              ">= 1 with a rotation (rows=%d rope_dim=%d table_rows=%d)", rows, rope_dim,
+              table_rows);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (rows == 0) return MLA_OK;
+  const bool no_q = q == nullptr;
+  const Named ptrs[] = {{q, "q", true},
+                        {k, "k", false},
+                        {v, "v", false},
+                        {cos_sin, "cos_sin", rope_dim == 0},
+                        {positions, "positions", false},
+                        {slots, "slots", false},
+                        {q_out, "q_out", no_q}};
+  st = check_pointers("append kv", ptrs, 7);
+  if (st != MLA_OK) return st;
+  const int64_t strides[] = {q_row_stride, k_row_stride, v_row_stride};
+  const int64_t least[] = {(int64_t)H * D, (int64_t)Hk * D, (int64_t)Hk * D};
+  const char* names[] = {"q_row_stride", "k_row_stride", "v_row_stride"};
+  for (int i = no_q ? 1 : 0; i < 3; ++i) {
+    if (strides[i] < least[i] || strides[i] * eb % 16 != 0) {
+      set_error("append kv: %s %lld must be at least %lld and a multiple of 16 bytes", names[i],
+                (long long)strides[i], (long long)least[i]);
+      return MLA_ERR_INVALID_ARG;
+    }
+  }
+  if (!no_q) {
+    // in place only row for row
+    const bool same = q == q_out && q_row_stride == least[0];
+    const Range a = range(q, ((int64_t)(rows - 1) * q_row_stride + least[0]) * eb);
+    const Range b = range(q_out, (int64_t)rows * least[0] * eb);
+    if (!same && overlap(a, b)) {
+      set_error("append kv: q_out overlaps q without being q");
+      return MLA_ERR_INVALID_ARG;
+    }
+  }
+  AppendKVParams p;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_row_stride;
+  p.k_stride = k_row_stride;
+  p.v_stride = v_row_stride;
+  p.cos_sin = cos_sin;
+  p.positions = positions;
+  p.slots = slots;
+  p.q_out = q_out;
+  p.k_cache = cache->k;
+  p.v_cache = cache->v;
+  p.page_stride = cache->page_stride;
+  p.row_stride = cache->row_stride;
+  p.head_stride = cache->head_stride;
+  p.cache_rows = (int64_t)cache->num_pages * cache->page_size;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.page = cache->page_size;
+  p.table_rows = table_rows;
+  p.rope = rope_dim;
+  p.interleaved = interleaved;
+  p.q_heads = no_q ? 0 : H;
+  p.kv_heads = Hk;
+  p.dim = D;
+  const int N = 16 / eb;
+  p.turned = rope_dim / 2 / N;
+  p.items = p.turned + ((D / N - 2 * p.turned) + 1) / 2;
+  const int heads = p.q_heads + 2 * Hk;
+  const dim3 block = item_block(p.items);
+  p.heads_per_cta = heads_per_cta(heads, (int)block.y, rows);
+  const dim3 grid((unsigned)rows, (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
+  if (grid.y > 65535u) {
+    set_error("append kv: %d heads are too many", heads);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  {
+    KernelTimer kt("append_kv", s);
+    if (eb == 4)
+      append_kv_kernel<float, float><<<grid, block, 0, s>>>(p);
+    else if (g->cache_dtype == MLA_DTYPE_E4M3)
+      append_kv_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, block, 0, s>>>(p);
+    else
+      append_kv_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, block, 0, s>>>(p);
+  }
+  return launched(cudaGetLastError());
+}
