@@ -1,30 +1,26 @@
 // Attention of one new token per sequence over a paged key/value cache
-// (mla_decode_attention): the drafter's decode step.
-//
-//   s_t = scale q . k_t,   out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m)
-//
-// One pass over the cache with the running maximum m and sum: a CTA takes one
-// query head of one sequence, a warp every fourth position, the lanes the
-// head's elements.
+// (mla_decode_attention): argument checks, the choice of kernel, and the
+// kernel that joins the parts of sequences cut between CTAs.  The attention
+// itself is in decode_kernel.cuh.
 
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <climits>
 #include <cmath>
+#include <mutex>
 
-#include "mla_internal.h"
+#include "decode_attention.h"
+#include "sm103_ptx.cuh"
 
 namespace mla {
 
-static __device__ int g_decode_status;
-
 int decode_device_status(bool clear) {
+  const int words[3] = {decode::bf16_status(clear), decode::e4m3_status(clear),
+                        decode::fp32_status(clear)};
   int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_decode_status, sizeof(int)) != cudaSuccess) return -1;
-  if (clear && v != 0) {
-    const int z = 0;
-    if (cudaMemcpyToSymbol(g_decode_status, &z, sizeof(int)) != cudaSuccess) return -1;
+  for (int w : words) {
+    if (w < 0) return -1;
+    if (v == 0) v = w;
   }
   return v;
 }
@@ -98,106 +94,192 @@ mla_status_t kv_cache_ok(const mla_kv_geometry_t* g, const mla_kv_cache_t* c) {
   return MLA_OK;
 }
 
+namespace decode {
 namespace {
 
-struct DecodeParams {
-  const void* q;
-  int64_t q_stride;
-  const void *k, *v;
-  int64_t page_stride, row_stride, head_stride;
-  const float *k_scale, *v_scale;
-  const int32_t* lens;
-  const int32_t* table;
-  void* out;
-  float* lse;
-  int heads, kv_heads, dim, batch, page, width, num_pages, window;
-  float scale;
+constexpr int kJoinThreads = 128;
+
+// One CTA per (share, row): where a segment's first part ends a share, the
+// parts of this row, in this share and the next ones, are weighted by
+// exp(m - max m) and summed in order.  The parts are few and small (16 rows of
+// 512 bytes a share at most), so this is bound by latency: every weight is
+// made at once, then groups of threads walk over the parts side by side.
+__global__ void __launch_bounds__(kJoinThreads)
+    decode_join_kernel(const Params p, const int rows_max, const int dp, const int kind) {
+  __shared__ float s_w[kMaxCtas];
+  __shared__ float s_red[kJoinThreads / 32];
+  __shared__ float4 s_acc[kJoinThreads];
+  sm103::pdl_wait();
+  const int cta = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  const Record rec = p.rec[cta];
+  if (rec.parts == 0) return;
+  const int kvh = rec.hr / p.row_tiles, rt = rec.hr - kvh * p.row_tiles;
+  if (row >= p.group - rt * rows_max) return;
+  // part k: the last segment of this share, then the first one of the shares behind it
+  auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
+  float M = -INFINITY;
+  for (int k = tid; k < rec.parts; k += kJoinThreads)
+    M = fmaxf(M, p.part_ml[slot(k) * rows_max + row].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+  if ((tid & 31) == 0) s_red[tid >> 5] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int k = tid; k < rec.parts; k += kJoinThreads) {
+    const float2 ml = p.part_ml[slot(k) * rows_max + row];
+    const float w = sm103::ex2(ml.x - base);
+    s_w[k] = w;
+    L += w * ml.y;
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+  __syncthreads();
+  if ((tid & 31) == 0) s_red[tid >> 5] = L;
+  __syncthreads();
+  L = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+
+  const int cols = dp / 4, groups = kJoinThreads / cols;
+  const int grp = tid / cols, c = tid - grp * cols;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (grp < groups) {
+#pragma unroll 4
+    for (int k = grp; k < rec.parts; k += groups) {
+      const float4 x = *reinterpret_cast<const float4*>(
+          p.part_o + (slot(k) * rows_max + row) * dp + c * 4);
+      const float w = s_w[k];
+      a.x = fmaf(w, x.x, a.x);
+      a.y = fmaf(w, x.y, a.y);
+      a.z = fmaf(w, x.z, a.z);
+      a.w = fmaf(w, x.w, a.w);
+    }
+  }
+  s_acc[tid] = a;
+  __syncthreads();
+  const int64_t head = (int64_t)rec.b * p.heads + kvh * p.group + rt * rows_max + row;
+  if (tid < cols && c * 4 < p.dim) {
+    for (int x = 1; x < groups; ++x) {
+      const float4 y = s_acc[x * cols + c];
+      a.x += y.x;
+      a.y += y.y;
+      a.z += y.z;
+      a.w += y.w;
+    }
+    const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
+    const float inv = L == 0.f ? 0.f : vs / L;
+    if (kind == kFp32)
+      *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c * 4) =
+          make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    else
+      *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c * 4) = make_uint2(
+          sm103::pack_bf16(a.x * inv, a.y * inv), sm103::pack_bf16(a.z * inv, a.w * inv));
+  }
+  if (tid == 0 && p.lse)
+    p.lse[head] = L == 0.f ? -INFINITY
+                           : (M + log2f(L) - (kind == kE4m3 ? kShift : 0.f)) * 0.6931471805599453f;
+}
+
+// The kernel of a geometry, how its work is cut, and the workspace.
+struct Plan {
+  Kernel k;
+  int kind, row_tiles, ctas;
+  bool cut;  // a segment may fall into several shares
+  size_t off_ml, off_o, bytes;
 };
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__nv_fp8_e4m3 x) { return (float)x; }
-__device__ __forceinline__ void from_float(float x, float* p) { *p = x; }
-__device__ __forceinline__ void from_float(float x, __nv_bfloat16* p) { *p = __float2bfloat16_rn(x); }
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-constexpr int kPerLane = 8;  // head_dim <= 256
+mla_status_t make_plan(const mla_kv_geometry_t* g, int32_t batch, int32_t page_size,
+                       int32_t max_pages, Plan* out) {
+  Plan& d = *out;
+  d.kind = g->dtype == MLA_DTYPE_FP32 ? kFp32 : g->cache_dtype == MLA_DTYPE_E4M3 ? kE4m3 : kBf16;
+  const int group = g->num_heads / g->num_kv_heads;
+  // one row multiple when the group fits it: half the products and registers
+  const int nt = group <= (d.kind == kFp32 ? 4 : 8) ? 1 : 2;
+  d.k = d.kind == kFp32   ? kernel_fp32(g->head_dim, nt)
+        : d.kind == kE4m3 ? kernel_e4m3(g->head_dim, nt)
+                          : kernel_bf16(g->head_dim, nt);
+  d.row_tiles = (group + d.k.rows - 1) / d.k.rows;
+  const int64_t hrs = (int64_t)g->num_kv_heads * d.row_tiles;
+  const int64_t tiles = ((int64_t)page_size * max_pages + d.k.tile - 1) / d.k.tile;
+  const int64_t most = (int64_t)batch * hrs * tiles;
+  if (most > ((int64_t)1 << 48)) {
+    set_error("decode: batch %d x %lld rows of a table is beyond what is planned for", batch,
+              (long long)page_size * max_pages);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  int64_t ctas = (int64_t)device_sm_count() * d.k.occupancy;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  if (ctas > most) ctas = most;
+  d.ctas = (int)ctas;
+  d.cut = tiles > 1;
+  size_t off = align256(sizeof(Record) * ctas);
+  d.off_ml = off;
+  off = align256(off + sizeof(float2) * 2 * ctas * d.k.rows);
+  d.off_o = off;
+  off = align256(off + sizeof(float) * 2 * ctas * d.k.rows * d.k.dp);
+  d.bytes = d.cut ? off : 0;
+  return MLA_OK;
+}
 
-template <typename T, typename CT>
-__global__ void __launch_bounds__(128) decode_rows_kernel(DecodeParams p) {
-  __shared__ float s_m[4], s_l[4], s_o[4][256];
-  const int h = blockIdx.x, b = blockIdx.y, hk = h / (p.heads / p.kv_heads);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int T_b = (int)min((long long)max(p.lens[b], 0), (long long)p.width * p.page);
-  const int lo = p.window > 0 ? max(0, T_b - p.window) : 0;
-  float q[kPerLane], o[kPerLane];
-  const float ks = p.k_scale ? p.k_scale[hk] : 1.f, vs = p.v_scale ? p.v_scale[hk] : 1.f;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int d = lane + 32 * i;
-    q[i] = d < p.dim ? to_float(((const T*)p.q)[b * p.q_stride + (int64_t)h * p.dim + d]) : 0.f;
-    o[i] = 0.f;
+// Allow a kernel its shared memory, once per kernel and device.
+cudaError_t allow_smem(const Kernel& k) {
+  struct Done {
+    int device;
+    void (*fn)(Params);
+  };
+  constexpr int kMost = 512;
+  static std::mutex mu;
+  static Done done[kMost];
+  static int count = 0;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  for (int i = 0; i < count; ++i)
+    if (done[i].device == dev && done[i].fn == k.fn) return cudaSuccess;
+  e = cudaFuncSetAttribute((const void*)k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+  if (e == cudaSuccess && count < kMost) done[count++] = {dev, k.fn};
+  return e;
+}
+
+cudaError_t launch(const Plan& d, const Params& p, cudaStream_t stream) {
+  cudaError_t e = allow_smem(d.k);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)d.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = d.k.smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  {
+    KernelTimer kt("decode_attn", stream);
+    e = cudaLaunchKernelEx(&cfg, d.k.fn, p);
   }
-  float m = -INFINITY, l = 0.f;
-  for (int t = lo + warp; t < T_b; t += 4) {
-    const int id = p.table[(int64_t)b * p.width + t / p.page];
-    const bool good = id >= 0 && id < p.num_pages;
-    if (!good && lane == 0) atomicCAS(&g_decode_status, 0, kBadPageSite);
-    const int64_t at = good ? id * p.page_stride + (int64_t)(t % p.page) * p.row_stride +
-                                  hk * p.head_stride
-                            : 0;
-    float s = 0.f, v[kPerLane];
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int d = lane + 32 * i;
-      const bool live = good && d < p.dim;
-      s = fmaf(q[i], live ? to_float(((const CT*)p.k)[at + d]) : 0.f, s);
-      v[i] = live ? to_float(((const CT*)p.v)[at + d]) : 0.f;
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    s *= p.scale * ks;
-    const float m2 = fmaxf(m, s);
-    const float base = m2 == -INFINITY ? 0.f : m2;
-    const float f = __expf(m - base), w = __expf(s - base);
-    l = l * f + w;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) o[i] = o[i] * f + w * v[i];
-    m = m2;
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) s_o[warp][lane + 32 * i] = o[i];
-  __syncthreads();
-  float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, f[4];
-  for (int w = 0; w < 4; ++w) {
-    f[w] = __expf(s_m[w] - base);
-    L += f[w] * s_l[w];
-  }
-  for (int d = threadIdx.x; d < p.dim; d += 128) {
-    float acc = 0.f;
-    for (int w = 0; w < 4; ++w) acc += f[w] * s_o[w][d];
-    from_float(L == 0.f ? 0.f : acc / L * vs,
-               (T*)p.out + ((int64_t)b * p.heads + h) * p.dim + d);
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(int64_t)b * p.heads + h] = L == 0.f ? -INFINITY : base + logf(L);
+  if (e != cudaSuccess || !d.cut) return e;
+  cfg.gridDim = dim3((unsigned)d.ctas, (unsigned)(p.group < d.k.rows ? p.group : d.k.rows));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  KernelTimer kt("decode_join", stream);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel, p, d.k.rows, d.k.dp, d.kind);
 }
 
 }  // namespace
+}  // namespace decode
 
 static mla_status_t decode_sizes_ok(const mla_kv_geometry_t* g, int32_t batch, int32_t page_size,
                                     int32_t max_pages) {
   const mla_status_t st = kv_geometry_ok(g);
   if (st != MLA_OK) return st;
   if (batch < 1 || batch > 65535 || page_size < 1 || max_pages < 1 ||
-      (int64_t)page_size * max_pages > INT_MAX) {
+      (int64_t)page_size * max_pages > INT_MAX - 1023) {
     set_error("decode: need 1 <= batch <= 65535, page_size and max_pages_per_seq >= 1 with at "
-              "most 2^31 - 1 rows between them (batch=%d page_size=%d max_pages=%d)",
+              "most 2^31 - 1024 rows between them (batch=%d page_size=%d max_pages=%d)",
               batch, page_size, max_pages);
     return MLA_ERR_INVALID_ARG;
   }
@@ -217,7 +299,10 @@ extern "C" mla_status_t mla_decode_workspace_bytes(const mla_kv_geometry_t* g, i
   }
   const mla_status_t st = decode_sizes_ok(g, batch, page_size, max_pages_per_seq);
   if (st != MLA_OK) return st;
-  *bytes = 0;
+  decode::Plan d;
+  const mla_status_t pst = decode::make_plan(g, batch, page_size, max_pages_per_seq, &d);
+  if (pst != MLA_OK) return pst;
+  *bytes = d.bytes;
   return MLA_OK;
 }
 
@@ -254,19 +339,19 @@ extern "C" mla_status_t mla_decode_attention(
               (long long)q_row_stride, (long long)g->num_heads * g->head_dim);
     return MLA_ERR_INVALID_ARG;
   }
-  size_t need = 0;
-  st = mla_decode_workspace_bytes(g, batch, cache->page_size, max_pages_per_seq, &need);
+  decode::Plan d;
+  st = decode::make_plan(g, batch, cache->page_size, max_pages_per_seq, &d);
   if (st != MLA_OK) return st;
-  if (workspace_bytes < need || (need > 0 && workspace == nullptr)) {
+  if (workspace_bytes < d.bytes || (d.bytes > 0 && workspace == nullptr)) {
     set_error("workspace of %zu bytes is smaller than the %zu this call needs", workspace_bytes,
-              need);
+              d.bytes);
     return MLA_ERR_WORKSPACE;
   }
   if ((uintptr_t)workspace & 255u) {
     set_error("workspace is not 256-byte aligned");
     return MLA_ERR_INVALID_ARG;
   }
-  DecodeParams p;
+  decode::Params p;
   p.q = q;
   p.q_stride = q_row_stride;
   p.k = cache->k;
@@ -280,28 +365,23 @@ extern "C" mla_status_t mla_decode_attention(
   p.table = page_table;
   p.out = out;
   p.lse = lse;
+  p.rec = d.cut ? (decode::Record*)workspace : nullptr;
+  p.part_ml = d.cut ? (float2*)((char*)workspace + d.off_ml) : nullptr;
+  p.part_o = d.cut ? (float*)((char*)workspace + d.off_o) : nullptr;
   p.heads = g->num_heads;
   p.kv_heads = g->num_kv_heads;
+  p.group = g->num_heads / g->num_kv_heads;
+  p.row_tiles = d.row_tiles;
   p.dim = g->head_dim;
   p.batch = batch;
   p.page = cache->page_size;
   p.width = max_pages_per_seq;
   p.num_pages = cache->num_pages;
   p.window = window;
-  p.scale = g->softmax_scale > 0.f ? g->softmax_scale
-                                   : (float)(1.0 / std::sqrt((double)g->head_dim));
-  const cudaStream_t s = (cudaStream_t)stream;
-  const dim3 grid((unsigned)p.heads, (unsigned)batch);
-  {
-    KernelTimer kt("decode_rows", s);
-    if (eb == 4)
-      decode_rows_kernel<float, float><<<grid, 128, 0, s>>>(p);
-    else if (g->cache_dtype == MLA_DTYPE_E4M3)
-      decode_rows_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, 128, 0, s>>>(p);
-    else
-      decode_rows_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 128, 0, s>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const double scale = g->softmax_scale > 0.f ? (double)g->softmax_scale
+                                              : 1.0 / std::sqrt((double)g->head_dim);
+  p.scale_log2 = (float)(scale * 1.4426950408889634);
+  const cudaError_t e = decode::launch(d, p, (cudaStream_t)stream);
   if (e != cudaSuccess) {
     set_error("CUDA error %d (%s)", (int)e, cudaGetErrorString(e));
     return MLA_ERR_CUDA;

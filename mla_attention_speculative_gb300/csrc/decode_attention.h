@@ -1,0 +1,90 @@
+// Interface between the decode attention's entry point and its kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "mla_internal.h"
+
+namespace mla {
+namespace decode {
+
+// Element types of a call: q/out and cache bf16; q/out bf16 beside an e4m3
+// cache; all fp32.
+enum Kind { kBf16 = 0, kE4m3 = 1, kFp32 = 2 };
+
+constexpr int kWarps = 4;            // of a CTA, each with its own ring of tiles
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCtas = 512;        // the join holds one weight per CTA
+
+// Weights beside an e4m3 cache are scaled by 2^kShift.
+constexpr float kShift = 15.f;
+
+// Shape of one kernel: everything that follows from the padded head width DP,
+// the element types and the row multiple NT.
+template <int DP, int KIND, int NT>
+struct Shape {
+  static constexpr int CB = KIND == kBf16 ? 2 : KIND == kE4m3 ? 1 : 4;  // bytes of an element
+  static constexpr int ROWB = DP * CB;                                  // bytes of a tile row
+  static constexpr int CH = ROWB / 16;                                  // its 16-byte chunks
+  // positions of a warp's tile: a tile's K and V are about 8 KB
+  static constexpr int WP = KIND == kFp32 ? 8 : ROWB >= 192 ? 16 : 32;
+  static constexpr int TILE = kWarps * WP;  // positions of a CTA's tile
+  static constexpr int ROWS = KIND == kFp32 ? 4 * NT : 8 * NT;  // query heads of a row tile
+  static constexpr int STAGE = 2 * WP * ROWB;  // K, then V
+  // two CTAs per SM where a ring of three tiles per warp fits half the shared
+  // memory, else one with the whole
+  static constexpr int OCC = 98304 / (kWarps * STAGE) >= 3 ? 2 : 1;
+  static constexpr int FIT = (OCC == 2 ? 98304 : 196608) / (kWarps * STAGE);
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int MSTRIDE = 36;  // floats of a merge row: 32 columns, padded
+  static constexpr int MERGE = kWarps * ROWS * MSTRIDE * 4;
+  static constexpr int STATS = kWarps * ROWS * 8;
+  // fp32: the row tile's queries, and each warp's weights
+  static constexpr int QTILE = KIND == kFp32 ? ROWS * DP * 4 : 0;
+  static constexpr int WEIGHTS = KIND == kFp32 ? kWarps * WP * ROWS * 4 : 0;
+  static constexpr int SMEM = RING + MERGE + STATS + QTILE + WEIGHTS;
+  static_assert(STAGES >= 3, "a warp's ring needs three tiles");
+};
+
+// What a CTA leaves for the join: the segment whose first part it holds (as
+// its last one), and in how many parts, in this CTA and the next ones.
+struct Record {
+  int b, hr, parts, pad;
+};
+
+struct Params {
+  const void* q;
+  int64_t q_stride;
+  const void *k, *v;
+  int64_t page_stride, row_stride, head_stride;
+  const float *k_scale, *v_scale;
+  const int32_t* lens;
+  const int32_t* table;
+  void* out;
+  float* lse;
+  Record* rec;     // [ctas]; NULL: no sequence is cut
+  float2* part_ml; // [2 * ctas][ROWS] running maximum (base 2) and sum
+  float* part_o;   // [2 * ctas][ROWS][DP] unnormalised
+  int heads, kv_heads, group, row_tiles, dim, batch, page, width, num_pages, window;
+  float scale_log2;  // softmax scale * log2(e)
+};
+
+struct Kernel {
+  void (*fn)(Params);
+  int smem, occupancy, tile, rows, dp;
+};
+
+// The kernel for padded width dp (64, 128, 192, 256) and row multiple nt (1, 2).
+Kernel kernel_bf16(int dp, int nt);
+Kernel kernel_e4m3(int dp, int nt);
+Kernel kernel_fp32(int dp, int nt);
+
+int bf16_status(bool clear);
+int e4m3_status(bool clear);
+int fp32_status(bool clear);
+
+}  // namespace decode
+}  // namespace mla

@@ -1,0 +1,705 @@
+// Decode attention over a paged key/value cache: the kernel.
+//
+//   s_t = scale q . k_t,   out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m)
+//
+// One pass over the cache with a running maximum m and sum.  A key/value
+// element is used by the `group` query heads that share it, 2 group flops a
+// byte in bf16: far below what the matrix units would need to be the limit,
+// so the kernel is built to keep the memory system full.
+//
+// Work.  The cache rows a call reads form segments (sequence, key/value head,
+// row tile of up to ROWS query heads), each a run of tiles of TILE positions.
+// All tiles, in that order, are dealt out in equal contiguous shares to as
+// many CTAs as are resident at once, whatever the lengths, so a batch of
+// ragged sequences and one long sequence load the machine alike.  The lengths
+// are read here, so a captured graph follows them.  A segment that falls into
+// several shares leaves its parts (unnormalised sums, m, sum of weights) in
+// the workspace, at most two per CTA, and a second kernel joins them in order.
+//
+// Loads.  Each warp owns a quarter of every tile and a ring of STAGES of its
+// quarters in shared memory, filled by 16-byte asynchronous copies (any page
+// size, any strides; rows beyond the sequence are zero-filled without being
+// read).  The warps share nothing until a segment ends, so there is no
+// barrier in the loop, and the copies run on across segments.  The page ids
+// of a tile are loaded one tile before its copies need them.
+//
+// Products.  The heads of a group are few, so they take the narrow side of the
+// matrix instruction: S^T = K Q^T and O^T = V^T P^T with positions (head
+// elements) as its 16 rows and 8 heads as its columns.  Tiles come from shared
+// memory by ldmatrix (chunks of a row XORed with its number, so eight rows'
+// chunks lie in different banks), and the weights P^T change from accumulator
+// to operand layout by movmatrix.  tcgen05 would need 128 rows of one operand,
+// its softmax a trip through tensor memory, and the loop has nothing to gain:
+// it waits for DRAM.
+//
+// Roundings.  bf16: the products are exact in fp32, and the weights enter the
+// second product as two bf16 parts, hi + lo (2^-16 relative), so that the
+// output's own rounding is the only one that shows (an infinite v therefore
+// gives NaN).  e4m3: keys and values become fp16 (exact), queries fp16 scaled
+// by a power of two per head (exact down to 2^-24 of the head's largest
+// element), weights fp16 scaled by 2^15, so that even many weights far below
+// the largest keep their sum.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "decode_attention.h"
+#include "sm103_ptx.cuh"
+
+namespace mla {
+namespace decode {
+
+using namespace sm103;
+
+static __device__ int g_status;
+
+static int read_status(bool clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return -1;
+  if (clear && v != 0) {
+    const int z = 0;
+    if (cudaMemcpyToSymbol(g_status, &z, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
+}
+
+struct Span {  // the positions a sequence sees, and its tiles (one at least)
+  int lo, T, n;
+};
+
+template <int TILE>
+__device__ __forceinline__ Span span_of(const Params& p, int b) {
+  Span s;
+  s.T = (int)min((long long)max(p.lens[b], 0), (long long)p.width * p.page);
+  s.lo = p.window > 0 ? max(0, s.T - p.window) : 0;
+  s.n = max(1, (s.T - s.lo + TILE - 1) / TILE);
+  return s;
+}
+
+// A place in the list of tiles: tile j of segment (b, hr).
+template <int TILE>
+struct Cursor {
+  int b, hr, j;
+  Span s;
+  __device__ __forceinline__ void next(const Params& p) {
+    if (++j < s.n) return;
+    j = 0;
+    if (++hr < p.kv_heads * p.row_tiles) return;
+    hr = 0;
+    s = span_of<TILE>(p, ++b);
+  }
+};
+
+// Where a lane's row of a tile lies: the page id is loaded, not yet used.
+struct RowAt {
+  int64_t off;  // within the page, -1: beyond the sequence
+  int id;
+};
+
+template <int DP, int KIND, int NT>
+__global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
+    decode_attn_sm103(const Params p) {
+  using S = Shape<DP, KIND, NT>;
+  constexpr int ROWS = S::ROWS, WP = S::WP, CH = S::CH, STAGES = S::STAGES;
+  extern __shared__ __align__(128) char smem[];
+  float* const s_merge = reinterpret_cast<float*>(smem + S::RING);
+  float2* const s_ml = reinterpret_cast<float2*>(smem + S::RING + S::MERGE);
+  float* const s_q = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::STATS);
+  float* const s_w = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::STATS + S::QTILE);
+  __shared__ long long s_sum[kWarps];
+  __shared__ long long s_rem;
+  __shared__ int s_b;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * S::STAGE;
+  const int chunks = p.dim * S::CB / 16;  // of a row; the rest of a tile row stays zero
+  if (chunks < CH) {
+    char* mine = smem + warp * STAGES * S::STAGE;
+    for (int i = lane * 16; i < STAGES * S::STAGE; i += 512)
+      *reinterpret_cast<uint4*>(mine + i) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's share of the tiles
+  const int hrs = p.kv_heads * p.row_tiles;
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += span_of<S::TILE>(p, b).n;
+  mine *= hrs;
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) s_sum[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += s_sum[w];
+    total += s_sum[w];
+  }
+  const long long ctas = min((long long)gridDim.x, total);
+  const int cta = blockIdx.x;
+  if (cta >= ctas) {
+    if (tid == 0 && p.rec) p.rec[cta].parts = 0;
+    return;
+  }
+  const long long quot = total / ctas, left = total % ctas;
+  const long long t0 = quot * cta + left * cta / ctas;
+  const long long t1 = quot * (cta + 1) + left * (cta + 1) / ctas;
+  if (upto - mine <= t0 && t0 < upto) {
+    long long at = upto - mine;
+    for (int b = b0; b < b1; ++b) {
+      const long long n = (long long)span_of<S::TILE>(p, b).n * hrs;
+      if (t0 < at + n) {
+        s_b = b;
+        s_rem = t0 - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  Cursor<S::TILE> cc;  // the tile being computed
+  cc.b = s_b;
+  cc.s = span_of<S::TILE>(p, cc.b);
+  cc.hr = (int)(s_rem / cc.s.n);
+  cc.j = (int)(s_rem % cc.s.n);
+
+  // ---- copies
+  Cursor<S::TILE> lc = cc;  // the tile whose page ids were last asked for
+  auto locate = [&]() {
+    RowAt r;
+    const int pos = lc.s.lo + lc.j * S::TILE + warp * WP + (lane & (WP - 1));
+    r.off = -1;
+    r.id = 0;
+    if (pos < lc.s.T) {
+      const int pg = (int)((uint32_t)pos / (uint32_t)p.page);
+      r.id = p.table[(int64_t)lc.b * p.width + pg];
+      r.off = (int64_t)(pos - pg * p.page) * p.row_stride +
+              (int64_t)(lc.hr / p.row_tiles) * p.head_stride;
+    }
+    return r;
+  };
+  auto copy = [&](const RowAt& r, int stage) {
+    int64_t at = -1;
+    if (r.off >= 0) {
+      if (r.id >= 0 && r.id < p.num_pages) at = (int64_t)r.id * p.page_stride + r.off;
+      else atomicCAS(&g_status, 0, kBadPageSite);
+    }
+    const uint32_t base = ring + stage * S::STAGE;
+#pragma unroll
+    for (int i = 0; i < WP * CH / 32; ++i) {
+      const int idx = lane + 32 * i, row = idx / CH, c = idx % CH;
+      const int64_t src = __shfl_sync(~0u, at, row);
+      if (c < chunks) {
+        const int x = CH % 8 == 0 ? (row & 7) : ((row >> 1) & 3);
+        const uint32_t dst = base + row * S::ROWB + ((c ^ x) << 4);
+        const int64_t off = src < 0 ? 0 : src * S::CB + c * 16;
+        const uint32_t bytes = src < 0 ? 0u : 16u;
+        cp_async16(dst, (const char*)p.k + off, bytes);
+        cp_async16(dst + WP * S::ROWB, (const char*)p.v + off, bytes);
+      }
+    }
+  };
+  RowAt ahead;  // of the next tile to copy
+  {
+    RowAt first[STAGES];
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+      first[s].off = -1;
+      first[s].id = 0;
+      if (t0 + s < t1) {
+        if (s > 0) lc.next(p);
+        first[s] = locate();
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+      if (t0 + s < t1) copy(first[s], s);
+      cp_async_commit();
+    }
+    ahead = first[STAGES - 1];
+  }
+
+  // ---- state of a segment, per lane
+  // matrix kinds: heads 8 nt + 2 (lane % 4) + {0, 1}; fp32: all ROWS heads
+  constexpr int MT = DP / 16;
+  constexpr int NSTAT = KIND == kFp32 ? ROWS : 2 * NT;
+  constexpr int NB = (DP + 127) / 128;
+  float m[NSTAT], l[NSTAT];
+  float o[KIND == kFp32 ? 1 : MT][KIND == kFp32 ? 1 : NT][4];
+  float of[KIND == kFp32 ? NB : 1][KIND == kFp32 ? ROWS : 1][4];
+  uint32_t qf[KIND == kFp32 ? 1 : MT][KIND == kFp32 ? 1 : NT][2];
+  float sc[KIND == kE4m3 ? 2 * NT : 1];  // base-2 scale of a score, per head where it differs
+  const int g = lane >> 2, quad = lane & 3;
+  bool whole = false;  // the segment began in this share
+  int stage = 0;
+  Record rec = {0, 0, 0, 0};
+
+  for (long long t = t0; t < t1; ++t) {
+    cp_async_wait_group<STAGES - 2>();
+    __syncwarp();
+    if (t + STAGES - 1 < t1) {
+      copy(ahead, stage == 0 ? STAGES - 1 : stage - 1);
+      if (t + STAGES < t1) {
+        lc.next(p);
+        ahead = locate();
+      }
+    }
+    cp_async_commit();
+
+    const int kvh = cc.hr / p.row_tiles, rt = cc.hr - kvh * p.row_tiles;
+    const int head0 = kvh * p.group + rt * ROWS;
+    const int rows = min(ROWS, p.group - rt * ROWS);
+
+    if (t == t0 || cc.j == 0) {
+      whole = cc.j == 0;
+#pragma unroll
+      for (int i = 0; i < NSTAT; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+      const float ks = KIND == kE4m3 && p.k_scale ? p.k_scale[kvh] : 1.f;
+      if constexpr (KIND == kFp32) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) of[nb][r][e] = 0.f;
+        const float* q = (const float*)p.q + cc.b * p.q_stride + (int64_t)head0 * p.dim;
+        // (the merge of the segment before ends with a barrier)
+        for (int i = tid * 4; i < ROWS * DP; i += kThreads * 4) {
+          const int r = i / DP, d = i % DP;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < rows && d < p.dim) x = *reinterpret_cast<const float4*>(q + r * p.dim + d);
+          *reinterpret_cast<float4*>(s_q + i) = x;
+        }
+        __syncthreads();
+        sc[0] = p.scale_log2;
+      } else {
+        const __nv_bfloat16* q =
+            (const __nv_bfloat16*)p.q + cc.b * p.q_stride + (int64_t)head0 * p.dim;
+        if constexpr (KIND == kBf16) {
+          sc[0] = p.scale_log2;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int r = nt * 8 + g;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int d = mt * 16 + i * 8 + quad * 2;
+                qf[mt][nt][i] = r < rows && d < p.dim
+                                    ? *reinterpret_cast<const uint32_t*>(q + r * p.dim + d)
+                                    : 0u;
+              }
+            }
+        } else {
+          // elements 16 mt + 4 quad .. + 3: the order in which ldmatrix hands out bytes
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            uint2 x[MT];
+            float top = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const int d = mt * 16 + quad * 4;
+              x[mt] = r < rows && d < p.dim
+                          ? *reinterpret_cast<const uint2*>(q + r * p.dim + d)
+                          : make_uint2(0u, 0u);
+              const uint32_t w[2] = {x[mt].x, x[mt].y};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                top = fmaxf(top, fabsf(__uint_as_float(w[i] << 16)));
+                top = fmaxf(top, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+              }
+            }
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            // 2^e with top in [2^e, 2^(e+1)); its inverse stays a normal number
+            const int e = min(max((int)((__float_as_uint(top) >> 23) & 255u) - 127, -120), 120);
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const uint32_t w[2] = {x[mt].x, x[mt].y};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * down,
+                                                    __uint_as_float(w[i] & 0xFFFF0000u) * down);
+                qf[mt][nt][i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            }
+            // lanes of row r know 2^e of head r; a score's columns are heads 2 quad + {0, 1}
+            const float mine_sc = p.scale_log2 * ks * up;
+            sc[2 * nt] = __shfl_sync(~0u, mine_sc, (2 * quad) * 4);
+            sc[2 * nt + 1] = __shfl_sync(~0u, mine_sc, (2 * quad + 1) * 4);
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+      }
+    }
+
+    // ---- one tile: positions pos0 .. pos0 + WP - 1
+    const int pos0 = cc.s.lo + cc.j * S::TILE + warp * WP;
+    const uint32_t kb = ring + stage * S::STAGE, vb = kb + WP * S::ROWB;
+    if (pos0 < cc.s.T) {
+      if constexpr (KIND != kFp32) {
+        constexpr int SUB = WP / 16;
+        float s[SUB][NT][4];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+        const int r8 = lane & 7, mi = lane >> 3;
+        const int row_k = r8 + (mi & 1) * 8;  // matrices: rows 0-7, 8-15, then the next chunk
+        const int swz_k = CH % 8 == 0 ? (row_k & 7) : ((row_k >> 1) & 3);
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const uint32_t at = kb + (u * 16 + row_k) * S::ROWB;
+          if constexpr (KIND == kBf16) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t a[4];
+              ldmatrix4(at + (((2 * mt + (mi >> 1)) ^ swz_k) << 4), a);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_16816_bf16(s[u][nt], a, qf[mt][nt][0], qf[mt][nt][1]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < MT; c += 2) {
+              uint32_t x[4];
+              ldmatrix4(at + (((c + (mi >> 1)) ^ swz_k) << 4), x);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a[4] = {e4m3x2_to_half2(x[2 * h]), e4m3x2_to_half2(x[2 * h + 1]),
+                                       e4m3x2_to_half2(x[2 * h] >> 16),
+                                       e4m3x2_to_half2(x[2 * h + 1] >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_16816_f16(s[u][nt], a, qf[c + h][nt][0], qf[c + h][nt][1]);
+              }
+            }
+          }
+        }
+        // scores: rows are positions u 16 + g (+ 8), columns this lane's two heads
+        float top[2 * NT];
+        bool grew = false;
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) top[i] = m[i];
+        const int live = cc.s.T - pos0;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& x = s[u][nt][e];
+              x *= KIND == kE4m3 ? sc[2 * nt + (e & 1)] : sc[0];
+              if (u * 16 + g + (e >> 1) * 8 >= live) x = -INFINITY;
+              top[2 * nt + (e & 1)] = fmaxf(top[2 * nt + (e & 1)], x);
+            }
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 4));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 8));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 16));
+          grew = grew || top[i] > m[i];
+        }
+        if (__any_sync(~0u, grew)) {
+#pragma unroll
+          for (int i = 0; i < 2 * NT; ++i) {
+            const float f = ex2(m[i] - (top[i] == -INFINITY ? 0.f : top[i]));
+            m[i] = top[i];
+            l[i] *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][i >> 1][i & 1] *= f;
+              o[mt][i >> 1][2 + (i & 1)] *= f;
+            }
+          }
+        }
+        uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float w[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float base = m[2 * nt + e] == -INFINITY ? 0.f : m[2 * nt + e];
+                w[e] = ex2(s[u][nt][2 * half + e] - base + (KIND == kE4m3 ? kShift : 0.f));
+                l[2 * nt + e] += w[e];
+              }
+              if constexpr (KIND == kBf16) {
+                const uint32_t h = pack_bf16(w[0], w[1]);
+                hi[u][nt][half] = movmatrix_trans(h);
+                lo[u][nt][half] = movmatrix_trans(pack_bf16(
+                    w[0] - __uint_as_float(h << 16), w[1] - __uint_as_float(h & 0xFFFF0000u)));
+              } else {
+                const __half2 h = __floats2half2_rn(w[0], w[1]);
+                hi[u][nt][half] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h));
+              }
+            }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          if constexpr (KIND == kBf16) {
+            // matrices: chunk 2 mt and 2 mt + 1 of rows 0-7, then of rows 8-15
+            const int row_v = r8 + (mi >> 1) * 8;
+            const int swz_v = CH % 8 == 0 ? (row_v & 7) : ((row_v >> 1) & 3);
+            const uint32_t at = vb + (u * 16 + row_v) * S::ROWB;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t a[4];
+              ldmatrix4_trans(at + (((2 * mt + (mi & 1)) ^ swz_v) << 4), a);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_16816_bf16(o[mt][nt], a, hi[u][nt][0], hi[u][nt][1]);
+                mma_16816_bf16(o[mt][nt], a, lo[u][nt][0], lo[u][nt][1]);
+              }
+            }
+          } else {
+            // rows 0-7 and 8-15 of chunk c, then of chunk c + 1; a 16-bit unit holds
+            // elements 2g and 2g + 1 of a position: even ones are rows 0-7 of the
+            // operand, odd ones rows 8-15
+            const uint32_t at = vb + (u * 16 + row_k) * S::ROWB;
+#pragma unroll
+            for (int c = 0; c < MT; c += 2) {
+              uint32_t x[4];
+              ldmatrix4_trans(at + (((c + (mi >> 1)) ^ swz_k) << 4), x);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t y0 = __byte_perm(x[2 * h], 0, 0x3120);
+                const uint32_t y1 = __byte_perm(x[2 * h + 1], 0, 0x3120);
+                const uint32_t a[4] = {e4m3x2_to_half2(y0), e4m3x2_to_half2(y0 >> 16),
+                                       e4m3x2_to_half2(y1), e4m3x2_to_half2(y1 >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_16816_f16(o[c + h][nt], a, hi[u][nt][0], hi[u][nt][1]);
+              }
+            }
+          }
+        }
+      } else {
+        // lane: position lane % 8, every fourth chunk from lane / 8
+        const int row = lane & 7, part = lane >> 3;
+        const char* kp = smem + (kb - smem_u32(smem)) + row * S::ROWB;
+        float s[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) s[r] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < CH / 4; ++i) {
+          const int c = part + 4 * i;
+          const float4 x = *reinterpret_cast<const float4*>(kp + ((c ^ row) << 4));
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const float4 q = *reinterpret_cast<const float4*>(s_q + r * DP + c * 4);
+            s[r] = fmaf(x.x, q.x, fmaf(x.y, q.y, fmaf(x.z, q.z, fmaf(x.w, q.w, s[r]))));
+          }
+        }
+        float* ws = s_w + warp * WP * ROWS;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          s[r] += __shfl_xor_sync(~0u, s[r], 8);
+          s[r] += __shfl_xor_sync(~0u, s[r], 16);
+          s[r] = pos0 + row < cc.s.T ? s[r] * sc[0] : -INFINITY;
+          float top = fmaxf(m[r], s[r]);
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+          const float base = top == -INFINITY ? 0.f : top;
+          if (__any_sync(~0u, top > m[r])) {
+            const float f = ex2(m[r] - base);
+            l[r] *= f;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) of[nb][r][e] *= f;
+          }
+          m[r] = top;
+          s[r] = ex2(s[r] - base);
+          l[r] += s[r];
+          if (r / (ROWS / 4) == part) ws[row * ROWS + r] = s[r];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int t8 = 0; t8 < WP; ++t8) {
+          float w[ROWS];
+#pragma unroll
+          for (int r = 0; r < ROWS; r += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(ws + t8 * ROWS + r);
+            w[r] = x.x; w[r + 1] = x.y; w[r + 2] = x.z; w[r + 3] = x.w;
+          }
+          const char* vp = smem + (vb - smem_u32(smem)) + t8 * S::ROWB;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int c = nb * 32 + lane;
+            if (c < CH) {
+              const float4 x = *reinterpret_cast<const float4*>(vp + ((c ^ (t8 & 7)) << 4));
+#pragma unroll
+              for (int r = 0; r < ROWS; ++r) {
+                of[nb][r][0] = fmaf(w[r], x.x, of[nb][r][0]);
+                of[nb][r][1] = fmaf(w[r], x.y, of[nb][r][1]);
+                of[nb][r][2] = fmaf(w[r], x.z, of[nb][r][2]);
+                of[nb][r][3] = fmaf(w[r], x.w, of[nb][r][3]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+
+    // ---- the segment ends here, or this share does
+    const bool ends = cc.j == cc.s.n - 1;
+    if (ends || t == t1 - 1) {
+      // the warps' parts, joined over shared memory 32 columns at a time
+      if constexpr (KIND == kFp32) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          l[r] += __shfl_xor_sync(~0u, l[r], 1);
+          l[r] += __shfl_xor_sync(~0u, l[r], 2);
+          l[r] += __shfl_xor_sync(~0u, l[r], 4);
+          if (lane == 0) s_ml[warp * ROWS + r] = make_float2(m[r], l[r]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+          l[i] += __shfl_xor_sync(~0u, l[i], 4);
+          l[i] += __shfl_xor_sync(~0u, l[i], 8);
+          l[i] += __shfl_xor_sync(~0u, l[i], 16);
+          if (g == 0)
+            s_ml[warp * ROWS + (i >> 1) * 8 + quad * 2 + (i & 1)] = make_float2(m[i], l[i]);
+        }
+      }
+      __syncthreads();
+      float f[NSTAT];
+#pragma unroll
+      for (int i = 0; i < NSTAT; ++i) {
+        const int r = KIND == kFp32 ? i : (i >> 1) * 8 + quad * 2 + (i & 1);
+        float top = s_ml[r].x;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w * ROWS + r].x);
+        f[i] = ex2(m[i] - (top == -INFINITY ? 0.f : top));
+      }
+      // the reducing threads' row: its maximum and sum
+      const int rr = tid >> 3, c4 = (tid & 7) * 4;
+      float M = -INFINITY, L = 0.f;
+      if (rr < ROWS) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * ROWS + rr].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 x = s_ml[w * ROWS + rr];
+          L += x.y * ex2(x.x - (M == -INFINITY ? 0.f : M));
+        }
+      }
+      const bool cut = !(whole && ends);
+      const int slot = whole ? 2 * cta + 1 : 2 * cta;
+      const float vs = KIND == kE4m3 && p.v_scale ? p.v_scale[kvh] : 1.f;
+      const float inv = L == 0.f ? 0.f : vs / L;
+      const int64_t head = (int64_t)cc.b * p.heads + head0 + rr;
+#pragma unroll
+      for (int c0 = 0; c0 < DP; c0 += 32) {
+        float* mine_buf = s_merge + warp * ROWS * S::MSTRIDE;
+        if constexpr (KIND == kFp32) {
+          if ((lane >> 3) == (c0 >> 5) % 4) {
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+              *reinterpret_cast<float4*>(mine_buf + r * S::MSTRIDE + (lane & 7) * 4) =
+                  make_float4(of[c0 / 128][r][0] * f[r], of[c0 / 128][r][1] * f[r],
+                              of[c0 / 128][r][2] * f[r], of[c0 / 128][r][3] * f[r]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = nt * 8 + quad * 2 + (e & 1);
+                const int d = k * 16 + (KIND == kBf16 ? g + (e >> 1) * 8 : 2 * g + (e >> 1));
+                mine_buf[r * S::MSTRIDE + d] = o[c0 / 16 + k][nt][e] * f[2 * nt + (e & 1)];
+              }
+        }
+        __syncthreads();
+        if (rr < rows && c0 + c4 < p.dim) {
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(
+                s_merge + (w * ROWS + rr) * S::MSTRIDE + c4);
+            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+          }
+          if (cut) {
+            *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * ROWS + rr) * DP + c0 + c4) = a;
+          } else if constexpr (KIND == kFp32) {
+            *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c0 + c4) =
+                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+          } else {
+            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c0 + c4) =
+                make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+          }
+        }
+        __syncthreads();
+      }
+      if (rr < rows && c4 == 0) {
+        if (cut)
+          p.part_ml[(int64_t)slot * ROWS + rr] = make_float2(M, L);
+        else if (p.lse)
+          p.lse[head] = L == 0.f ? -INFINITY
+                                 : (M + log2f(L) - (KIND == kE4m3 ? kShift : 0.f)) * 0.6931471805599453f;
+      }
+      if (whole && !ends) {
+        // the segment's last tile lies in CTA ((te + 1) ctas - 1) / total
+        const long long te = t + (cc.s.n - 1 - cc.j);
+        rec.b = cc.b;
+        rec.hr = cc.hr;
+        rec.parts = (int)(((te + 1) * ctas - 1) / total) - cta + 1;
+      }
+    }
+    if (t + 1 < t1) cc.next(p);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+  }
+  if (tid == 0 && p.rec) p.rec[cta] = rec;
+}
+
+template <int DP, int KIND, int NT>
+Kernel kernel_of() {
+  using S = Shape<DP, KIND, NT>;
+  return {decode_attn_sm103<DP, KIND, NT>, S::SMEM, S::OCC, S::TILE, S::ROWS, DP};
+}
+
+template <int KIND>
+Kernel kernel_for(int dp, int nt) {
+  if (nt == 1)
+    return dp <= 64    ? kernel_of<64, KIND, 1>()
+           : dp <= 128 ? kernel_of<128, KIND, 1>()
+           : dp <= 192 ? kernel_of<192, KIND, 1>()
+                       : kernel_of<256, KIND, 1>();
+  return dp <= 64    ? kernel_of<64, KIND, 2>()
+         : dp <= 128 ? kernel_of<128, KIND, 2>()
+         : dp <= 192 ? kernel_of<192, KIND, 2>()
+                     : kernel_of<256, KIND, 2>();
+}
+
+}  // namespace decode
+}  // namespace mla
