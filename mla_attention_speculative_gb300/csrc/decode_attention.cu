@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int cta = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   const Record rec = p.rec[cta];
   if (rec.parts == 0) return;
-  const int kvh = rec.hr / p.row_tiles, rt = rec.hr - kvh * p.row_tiles;
+  const int kvh = rec.kvh, rt = rec.rt;
   if (row >= p.group - rt * rows_max) return;
   // part k: the last segment of this share, then the first one of the shares behind it
   auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
@@ -252,7 +252,7 @@ cudaError_t launch(const Plan& d, const Params& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)d.ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(d.k.threads);
   cfg.dynamicSmemBytes = d.k.smem;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -375,6 +375,12 @@ extern "C" mla_status_t mla_decode_attention(
   p.dim = g->head_dim;
   p.batch = batch;
   p.page = cache->page_size;
+  // with 2^(s-1) < page <= 2^s, m = ceil(2^(31+s) / page) < 2^32 overshoots by
+  // less than page, so pos m / 2^(31+s) is off by less than pos / 2^31 / 2^s < 1 / page
+  int s = 0;
+  while (((int64_t)1 << s) < p.page) ++s;
+  p.page_shift = 31 + s;
+  p.page_magic = (uint32_t)((((uint64_t)1 << (31 + s)) + (uint64_t)p.page - 1) / (uint64_t)p.page);
   p.width = max_pages_per_seq;
   p.num_pages = cache->num_pages;
   p.window = window;

@@ -14,9 +14,11 @@ namespace decode {
 // cache; all fp32.
 enum Kind { kBf16 = 0, kE4m3 = 1, kFp32 = 2 };
 
-constexpr int kWarps = 4;            // of a CTA, each with its own ring of tiles
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCtas = 512;        // the join holds one weight per CTA
+constexpr int kMaxCtas = 512;  // the join holds one weight per CTA
+
+// A segment counts as this many tiles more than it has when the work is dealt
+// out: its queries, its merge and its outputs take about as long as one tile.
+constexpr int kSegmentCost = 1;
 
 // Weights beside an e4m3 cache are scaled by 2^kShift.
 constexpr float kShift = 15.f;
@@ -28,31 +30,44 @@ struct Shape {
   static constexpr int CB = KIND == kBf16 ? 2 : KIND == kE4m3 ? 1 : 4;  // bytes of an element
   static constexpr int ROWB = DP * CB;                                  // bytes of a tile row
   static constexpr int CH = ROWB / 16;                                  // its 16-byte chunks
-  // positions of a warp's tile: a tile's K and V are about 8 KB
+  // warps of a CTA, each with its own ring of tiles
+  static constexpr int NW = 4;
+  static constexpr int THREADS = NW * 32;
+  // positions of a warp's tile: its K and V are about 8 KB
   static constexpr int WP = KIND == kFp32 ? 8 : ROWB >= 192 ? 16 : 32;
-  static constexpr int TILE = kWarps * WP;  // positions of a CTA's tile
+  static constexpr int TILE = NW * WP;  // positions of a CTA's tile
   static constexpr int ROWS = KIND == kFp32 ? 4 * NT : 8 * NT;  // query heads of a row tile
   static constexpr int STAGE = 2 * WP * ROWB;  // K, then V
-  // two CTAs per SM where a ring of three tiles per warp fits half the shared
-  // memory, else one with the whole
-  static constexpr int OCC = 98304 / (kWarps * STAGE) >= 3 ? 2 : 1;
-  static constexpr int FIT = (OCC == 2 ? 98304 : 196608) / (kWarps * STAGE);
+  // Three CTAs per SM with rings of two tiles per warp where the registers of
+  // 168 a thread suffice (up to 128 elements, one row multiple): the third
+  // CTA's warps cover more latency than a third tile in each ring would (bf16,
+  // 32 sequences: 327 us against 340; e4m3, 64 sequences: 170 against 181).
+  // Else two CTAs, or one with the whole shared memory for wide heads.
+  static constexpr int OCC = KIND != kFp32 && DP <= 128 && NT == 1 ? 3
+                             : 98304 / (NW * STAGE) >= 3           ? 2
+                                                                   : 1;
+  static constexpr int FIT = 196608 / OCC / (NW * STAGE);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
-  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int RING = NW * STAGES * STAGE;
   static constexpr int MSTRIDE = 36;  // floats of a merge row: 32 columns, padded
-  static constexpr int MERGE = kWarps * ROWS * MSTRIDE * 4;
-  static constexpr int STATS = kWarps * ROWS * 8;
+  // two buffers, so that a round of the merge needs one barrier, where they fit
+  static constexpr int MBUFS = NW * ROWS <= 32 && OCC < 3 ? 2 : 1;
+  static constexpr int MBUF = NW * ROWS * MSTRIDE;  // floats of one
+  static constexpr int MERGE = MBUFS * MBUF * 4;
+  static constexpr int STATS = NW * ROWS * 8;
   // fp32: the row tile's queries, and each warp's weights
   static constexpr int QTILE = KIND == kFp32 ? ROWS * DP * 4 : 0;
-  static constexpr int WEIGHTS = KIND == kFp32 ? kWarps * WP * ROWS * 4 : 0;
+  static constexpr int WEIGHTS = KIND == kFp32 ? NW * WP * ROWS * 4 : 0;
   static constexpr int SMEM = RING + MERGE + STATS + QTILE + WEIGHTS;
-  static_assert(STAGES >= 3, "a warp's ring needs three tiles");
+  static_assert(STAGES >= 2, "a warp's ring needs two tiles");
+  // 228 KB of an SM, 1 KB of which each CTA costs besides (and a little static)
+  static_assert(OCC * (SMEM + 1024 + 256) <= 228 * 1024, "OCC CTAs do not fit an SM");
 };
 
 // What a CTA leaves for the join: the segment whose first part it holds (as
 // its last one), and in how many parts, in this CTA and the next ones.
 struct Record {
-  int b, hr, parts, pad;
+  int b, kvh, rt, parts;
 };
 
 struct Params {
@@ -69,12 +84,15 @@ struct Params {
   float2* part_ml; // [2 * ctas][ROWS] running maximum (base 2) and sum
   float* part_o;   // [2 * ctas][ROWS][DP] unnormalised
   int heads, kv_heads, group, row_tiles, dim, batch, page, width, num_pages, window;
+  // pos / page == (pos * page_magic) >> page_shift for 0 <= pos < 2^31
+  uint32_t page_magic;
+  int page_shift;
   float scale_log2;  // softmax scale * log2(e)
 };
 
 struct Kernel {
   void (*fn)(Params);
-  int smem, occupancy, tile, rows, dp;
+  int smem, threads, occupancy, tile, rows, dp;
 };
 
 // The kernel for padded width dp (64, 128, 192, 256) and row multiple nt (1, 2).

@@ -64,7 +64,7 @@ static int read_status(bool clear) {
   return v;
 }
 
-struct Span {  // the positions a sequence sees, and its tiles (one at least)
+struct Span {  // the positions a sequence sees, and its tiles
   int lo, T, n;
 };
 
@@ -73,23 +73,50 @@ __device__ __forceinline__ Span span_of(const Params& p, int b) {
   Span s;
   s.T = (int)min((long long)max(p.lens[b], 0), (long long)p.width * p.page);
   s.lo = p.window > 0 ? max(0, s.T - p.window) : 0;
-  s.n = max(1, (s.T - s.lo + TILE - 1) / TILE);
+  s.n = (s.T - s.lo + TILE - 1) / TILE;
   return s;
 }
 
-// A place in the list of tiles: tile j of segment (b, hr).
+// What a sequence's segments count for, each, when the work is dealt out.
+__device__ __forceinline__ int cost_of(const Span& s) { return s.n > 0 ? s.n + kSegmentCost : 0; }
+
+// A place in the work: tile j of segment (b, kvh, rt), and its place t in the
+// list in which a segment's tiles come behind kSegmentCost places without one.
 template <int TILE>
 struct Cursor {
-  int b, hr, j;
+  int b, kvh, rt, j;
+  long long t;
   Span s;
-  __device__ __forceinline__ void next(const Params& p) {
+  // To the next tile; beyond `end` the place alone is right.
+  __device__ __forceinline__ void next(const Params& p, long long end) {
+    ++t;
     if (++j < s.n) return;
+    t += kSegmentCost;
+    if (t >= end) return;
     j = 0;
-    if (++hr < p.kv_heads * p.row_tiles) return;
-    hr = 0;
-    s = span_of<TILE>(p, ++b);
+    if (++rt < p.row_tiles) return;
+    rt = 0;
+    if (++kvh < p.kv_heads) return;
+    kvh = 0;
+    do {
+      s = span_of<TILE>(p, ++b);
+    } while (s.n == 0);
   }
 };
+
+// Sequences with nothing to see have no tiles: their outputs, dealt over the CTAs.
+template <int TILE, int KIND>
+__device__ __forceinline__ void zero_idle(const Params& p) {
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    if (span_of<TILE>(p, b).n > 0) continue;
+    const int64_t row = (int64_t)p.heads * p.dim * (KIND == kFp32 ? 4 : 2);
+    uint4* dst = reinterpret_cast<uint4*>((char*)p.out + b * row);
+    for (int i = threadIdx.x; i < row / 16; i += blockDim.x) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse)
+      for (int h = threadIdx.x; h < p.heads; h += blockDim.x)
+        p.lse[(int64_t)b * p.heads + h] = -INFINITY;
+  }
+}
 
 // Where a lane's row of a tile lies: the page id is loaded, not yet used.
 struct RowAt {
@@ -97,17 +124,23 @@ struct RowAt {
   int id;
 };
 
+// a / b, a 32-bit division where the values allow.
+__device__ __forceinline__ long long div_small(long long a, int b) {
+  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 template <int DP, int KIND, int NT>
-__global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
+__global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIND, NT>::OCC))
     decode_attn_sm103(const Params p) {
   using S = Shape<DP, KIND, NT>;
-  constexpr int ROWS = S::ROWS, WP = S::WP, CH = S::CH, STAGES = S::STAGES;
+  constexpr int ROWS = S::ROWS, WP = S::WP, CH = S::CH, STAGES = S::STAGES, NW = S::NW;
+  constexpr int THREADS = S::THREADS;
   extern __shared__ __align__(128) char smem[];
   float* const s_merge = reinterpret_cast<float*>(smem + S::RING);
   float2* const s_ml = reinterpret_cast<float2*>(smem + S::RING + S::MERGE);
   float* const s_q = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::STATS);
   float* const s_w = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::STATS + S::QTILE);
-  __shared__ long long s_sum[kWarps];
+  __shared__ long long s_sum[NW];
   __shared__ long long s_rem;
   __shared__ int s_b;
 
@@ -125,10 +158,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
 
   // ---- this CTA's share of the tiles
   const int hrs = p.kv_heads * p.row_tiles;
-  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int per = (p.batch + THREADS - 1) / THREADS;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of<S::TILE>(p, b).n;
+  for (int b = b0; b < b1; ++b) mine += cost_of(span_of<S::TILE>(p, b));
   mine *= hrs;
   long long upto = mine;
 #pragma unroll
@@ -140,37 +173,111 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < NW; ++w) {
     if (w < warp) upto += s_sum[w];
     total += s_sum[w];
   }
-  const long long ctas = min((long long)gridDim.x, total);
+  const int ctas = (int)min((long long)gridDim.x, total);
   const int cta = blockIdx.x;
   if (cta >= ctas) {
     if (tid == 0 && p.rec) p.rec[cta].parts = 0;
+    zero_idle<S::TILE, KIND>(p);
     return;
   }
-  const long long quot = total / ctas, left = total % ctas;
-  const long long t0 = quot * cta + left * cta / ctas;
-  const long long t1 = quot * (cta + 1) + left * (cta + 1) / ctas;
+  // share i is places floor(total i / ctas) up to the next one's first
+  const long long quot = div_small(total, ctas);
+  const int left = (int)(total - quot * ctas);
+  const long long t0 = quot * cta + (uint32_t)(left * cta) / (uint32_t)ctas;
+  const long long t1 = quot * (cta + 1) + (uint32_t)(left * (cta + 1)) / (uint32_t)ctas;
   if (upto - mine <= t0 && t0 < upto) {
     long long at = upto - mine;
-    for (int b = b0; b < b1; ++b) {
-      const long long n = (long long)span_of<S::TILE>(p, b).n * hrs;
-      if (t0 < at + n) {
-        s_b = b;
-        s_rem = t0 - at;
-        break;
+    int b = b0;
+    if (per > 1) {
+      for (; b < b1 - 1; ++b) {
+        const long long n = (long long)cost_of(span_of<S::TILE>(p, b)) * hrs;
+        if (t0 < at + n) break;
+        at += n;
       }
-      at += n;
     }
+    s_b = b;
+    s_rem = t0 - at;
   }
   __syncthreads();
   Cursor<S::TILE> cc;  // the tile being computed
   cc.b = s_b;
   cc.s = span_of<S::TILE>(p, cc.b);
-  cc.hr = (int)(s_rem / cc.s.n);
-  cc.j = (int)(s_rem % cc.s.n);
+  const int hr = (int)div_small(s_rem, cost_of(cc.s));
+  const int place = (int)(s_rem - (long long)hr * cost_of(cc.s)) - kSegmentCost;
+  cc.j = max(place, 0);
+  cc.t = t0 + max(-place, 0);
+  cc.kvh = hr / p.row_tiles;
+  cc.rt = hr - cc.kvh * p.row_tiles;
+
+  // ---- state of a segment, per lane
+  // matrix kinds: heads 8 nt + 2 (lane % 4) + {0, 1}; fp32: all ROWS heads
+  constexpr int MT = DP / 16;
+  constexpr int NSTAT = KIND == kFp32 ? ROWS : 2 * NT;
+  constexpr int NB = (DP + 127) / 128;
+  float m[NSTAT], l[NSTAT];
+  float o[KIND == kFp32 ? 1 : MT][KIND == kFp32 ? 1 : NT][4];
+  float of[KIND == kFp32 ? NB : 1][KIND == kFp32 ? ROWS : 1][4];
+  uint32_t qf[KIND == kFp32 ? 1 : MT][KIND == kFp32 ? 1 : NT][2];
+  float sc[KIND == kE4m3 ? 2 * NT : 1];  // base-2 scale of a score, per head where it differs
+  const int g = lane >> 2, quad = lane & 3;
+  bool whole = false;  // the segment began in this share
+  int stage = 0;
+  Record rec = {0, 0, 0, 0};
+
+  // A segment's queries: asked for while the segment before is merged (the
+  // first one's before any copy), so that they do not wait behind the copies.
+  // bf16 has them in the operand's layout; e4m3 converts them when the segment
+  // begins; fp32 stages them in shared memory.
+  constexpr int QV = KIND == kFp32 ? (ROWS * DP / 4 + THREADS - 1) / THREADS : 1;
+  float4 qv[QV];
+  float ks = 1.f, vs = 1.f;  // e4m3: the head's scales
+  auto load_queries = [&](const Cursor<S::TILE>& c) {
+    const int rows = min(ROWS, p.group - c.rt * ROWS);
+    const int64_t base = c.b * p.q_stride + (int64_t)(c.kvh * p.group + c.rt * ROWS) * p.dim;
+    if constexpr (KIND == kFp32) {
+#pragma unroll
+      for (int i = 0; i < QV; ++i) {
+        const int at = (tid + i * THREADS) * 4, r = at / DP, d = at % DP;
+        qv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && d < p.dim)
+          qv[i] = *reinterpret_cast<const float4*>((const float*)p.q + base + r * p.dim + d);
+      }
+    } else {
+      const __nv_bfloat16* q = (const __nv_bfloat16*)p.q + base;
+      if constexpr (KIND == kE4m3) {
+        ks = p.k_scale ? p.k_scale[c.kvh] : 1.f;
+        vs = p.v_scale ? p.v_scale[c.kvh] : 1.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = nt * 8 + g;
+          if constexpr (KIND == kBf16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int d = mt * 16 + i * 8 + quad * 2;
+              qf[mt][nt][i] = r < rows && d < p.dim
+                                  ? *reinterpret_cast<const uint32_t*>(q + r * p.dim + d)
+                                  : 0u;
+            }
+          } else {
+            // elements 16 mt + 4 quad .. + 3: the order in which ldmatrix hands out bytes
+            const int d = mt * 16 + quad * 4;
+            const uint2 x = r < rows && d < p.dim
+                                ? *reinterpret_cast<const uint2*>(q + r * p.dim + d)
+                                : make_uint2(0u, 0u);
+            qf[mt][nt][0] = x.x;
+            qf[mt][nt][1] = x.y;
+          }
+        }
+    }
+  };
+  load_queries(cc);
 
   // ---- copies
   Cursor<S::TILE> lc = cc;  // the tile whose page ids were last asked for
@@ -180,10 +287,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
     r.off = -1;
     r.id = 0;
     if (pos < lc.s.T) {
-      const int pg = (int)((uint32_t)pos / (uint32_t)p.page);
+      const int pg = (int)(((uint64_t)(uint32_t)pos * p.page_magic) >> p.page_shift);
       r.id = p.table[(int64_t)lc.b * p.width + pg];
-      r.off = (int64_t)(pos - pg * p.page) * p.row_stride +
-              (int64_t)(lc.hr / p.row_tiles) * p.head_stride;
+      r.off = (int64_t)(pos - pg * p.page) * p.row_stride + lc.kvh * p.head_stride;
     }
     return r;
   };
@@ -215,58 +321,38 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
     for (int s = 0; s < STAGES; ++s) {
       first[s].off = -1;
       first[s].id = 0;
-      if (t0 + s < t1) {
-        if (s > 0) lc.next(p);
-        first[s] = locate();
-      }
+      if (s > 0 && lc.t < t1) lc.next(p, t1);
+      if (lc.t < t1) first[s] = locate();
     }
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
-      if (t0 + s < t1) copy(first[s], s);
+      copy(first[s], s);
       cp_async_commit();
     }
     ahead = first[STAGES - 1];
   }
 
-  // ---- state of a segment, per lane
-  // matrix kinds: heads 8 nt + 2 (lane % 4) + {0, 1}; fp32: all ROWS heads
-  constexpr int MT = DP / 16;
-  constexpr int NSTAT = KIND == kFp32 ? ROWS : 2 * NT;
-  constexpr int NB = (DP + 127) / 128;
-  float m[NSTAT], l[NSTAT];
-  float o[KIND == kFp32 ? 1 : MT][KIND == kFp32 ? 1 : NT][4];
-  float of[KIND == kFp32 ? NB : 1][KIND == kFp32 ? ROWS : 1][4];
-  uint32_t qf[KIND == kFp32 ? 1 : MT][KIND == kFp32 ? 1 : NT][2];
-  float sc[KIND == kE4m3 ? 2 * NT : 1];  // base-2 scale of a score, per head where it differs
-  const int g = lane >> 2, quad = lane & 3;
-  bool whole = false;  // the segment began in this share
-  int stage = 0;
-  Record rec = {0, 0, 0, 0};
+  bool begin = true;  // a segment, or this share of one
 
-  for (long long t = t0; t < t1; ++t) {
+  while (cc.t < t1) {
     cp_async_wait_group<STAGES - 2>();
     __syncwarp();
-    if (t + STAGES - 1 < t1) {
+    if (lc.t < t1) {
       copy(ahead, stage == 0 ? STAGES - 1 : stage - 1);
-      if (t + STAGES < t1) {
-        lc.next(p);
-        ahead = locate();
-      }
+      lc.next(p, t1);
+      if (lc.t < t1) ahead = locate();
     }
     cp_async_commit();
 
-    const int kvh = cc.hr / p.row_tiles, rt = cc.hr - kvh * p.row_tiles;
-    const int head0 = kvh * p.group + rt * ROWS;
-    const int rows = min(ROWS, p.group - rt * ROWS);
-
-    if (t == t0 || cc.j == 0) {
+    if (begin) {
+      begin = false;
       whole = cc.j == 0;
 #pragma unroll
       for (int i = 0; i < NSTAT; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
       }
-      const float ks = KIND == kE4m3 && p.k_scale ? p.k_scale[kvh] : 1.f;
+      sc[0] = p.scale_log2;
       if constexpr (KIND == kFp32) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -274,72 +360,44 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
           for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int e = 0; e < 4; ++e) of[nb][r][e] = 0.f;
-        const float* q = (const float*)p.q + cc.b * p.q_stride + (int64_t)head0 * p.dim;
-        // (the merge of the segment before ends with a barrier)
-        for (int i = tid * 4; i < ROWS * DP; i += kThreads * 4) {
-          const int r = i / DP, d = i % DP;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r < rows && d < p.dim) x = *reinterpret_cast<const float4*>(q + r * p.dim + d);
-          *reinterpret_cast<float4*>(s_q + i) = x;
+        // (the segment before ended with a barrier)
+#pragma unroll
+        for (int i = 0; i < QV; ++i) {
+          const int at = (tid + i * THREADS) * 4;
+          if (at < ROWS * DP) *reinterpret_cast<float4*>(s_q + at) = qv[i];
         }
         __syncthreads();
-        sc[0] = p.scale_log2;
       } else {
-        const __nv_bfloat16* q =
-            (const __nv_bfloat16*)p.q + cc.b * p.q_stride + (int64_t)head0 * p.dim;
-        if constexpr (KIND == kBf16) {
-          sc[0] = p.scale_log2;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const int r = nt * 8 + g;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int d = mt * 16 + i * 8 + quad * 2;
-                qf[mt][nt][i] = r < rows && d < p.dim
-                                    ? *reinterpret_cast<const uint32_t*>(q + r * p.dim + d)
-                                    : 0u;
-              }
-            }
-        } else {
-          // elements 16 mt + 4 quad .. + 3: the order in which ldmatrix hands out bytes
+        if constexpr (KIND == kE4m3) {
+          // (a negative key scale turns the queries round, so that a score's scale is
+          // positive; a zero one leaves it tiny)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + g;
-            uint2 x[MT];
             float top = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const int d = mt * 16 + quad * 4;
-              x[mt] = r < rows && d < p.dim
-                          ? *reinterpret_cast<const uint2*>(q + r * p.dim + d)
-                          : make_uint2(0u, 0u);
-              const uint32_t w[2] = {x[mt].x, x[mt].y};
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                top = fmaxf(top, fabsf(__uint_as_float(w[i] << 16)));
-                top = fmaxf(top, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+                top = fmaxf(top, fabsf(__uint_as_float(qf[mt][nt][i] << 16)));
+                top = fmaxf(top, fabsf(__uint_as_float(qf[mt][nt][i] & 0xFFFF0000u)));
               }
-            }
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
             // 2^e with top in [2^e, 2^(e+1)); its inverse stays a normal number
             const int e = min(max((int)((__float_as_uint(top) >> 23) & 255u) - 127, -120), 120);
             const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), ks);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const uint32_t w[2] = {x[mt].x, x[mt].y};
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * down,
-                                                    __uint_as_float(w[i] & 0xFFFF0000u) * down);
+                const uint32_t w = qf[mt][nt][i];
+                const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * down,
+                                                    __uint_as_float(w & 0xFFFF0000u) * down);
                 qf[mt][nt][i] = *reinterpret_cast<const uint32_t*>(&h);
               }
-            }
             // lanes of row r know 2^e of head r; a score's columns are heads 2 quad + {0, 1}
-            const float mine_sc = p.scale_log2 * ks * up;
+            const float mine_sc = fmaxf(p.scale_log2 * fabsf(ks) * up, 1e-37f);
             sc[2 * nt] = __shfl_sync(~0u, mine_sc, (2 * quad) * 4);
             sc[2 * nt + 1] = __shfl_sync(~0u, mine_sc, (2 * quad + 1) * 4);
           }
@@ -359,13 +417,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
     if (pos0 < cc.s.T) {
       if constexpr (KIND != kFp32) {
         constexpr int SUB = WP / 16;
-        float s[SUB][NT][4];
+        float s[SUB][NT][4], s2[SUB][NT][4];  // two chains of products per score
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[u][nt][e] = s2[u][nt][e] = 0.f;
         const int r8 = lane & 7, mi = lane >> 3;
         const int row_k = r8 + (mi & 1) * 8;  // matrices: rows 0-7, 8-15, then the next chunk
         const int swz_k = CH % 8 == 0 ? (row_k & 7) : ((row_k >> 1) & 3);
@@ -379,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
               ldmatrix4(at + (((2 * mt + (mi >> 1)) ^ swz_k) << 4), a);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_16816_bf16(s[u][nt], a, qf[mt][nt][0], qf[mt][nt][1]);
+                mma_16816_bf16(mt & 1 ? s2[u][nt] : s[u][nt], a, qf[mt][nt][0], qf[mt][nt][1]);
             }
           } else {
 #pragma unroll
@@ -388,38 +446,45 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
               ldmatrix4(at + (((c + (mi >> 1)) ^ swz_k) << 4), x);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t a[4] = {e4m3x2_to_half2(x[2 * h]), e4m3x2_to_half2(x[2 * h + 1]),
-                                       e4m3x2_to_half2(x[2 * h] >> 16),
-                                       e4m3x2_to_half2(x[2 * h + 1] >> 16)};
+                uint32_t a[4];
+                e4m3x4_to_half2(x[2 * h], a[0], a[2]);
+                e4m3x4_to_half2(x[2 * h + 1], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_16816_f16(s[u][nt], a, qf[c + h][nt][0], qf[c + h][nt][1]);
+                  mma_16816_f16(h ? s2[u][nt] : s[u][nt], a, qf[c + h][nt][0], qf[c + h][nt][1]);
               }
             }
           }
         }
-        // scores: rows are positions u 16 + g (+ 8), columns this lane's two heads
-        float top[2 * NT];
-        bool grew = false;
-#pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) top[i] = m[i];
-        const int live = cc.s.T - pos0;
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float& x = s[u][nt][e];
-              x *= KIND == kE4m3 ? sc[2 * nt + (e & 1)] : sc[0];
-              if (u * 16 + g + (e >> 1) * 8 >= live) x = -INFINITY;
-              top[2 * nt + (e & 1)] = fmaxf(top[2 * nt + (e & 1)], x);
-            }
+            for (int e = 0; e < 4; ++e) s[u][nt][e] += s2[u][nt][e];
+        // scores: rows are positions u 16 + g (+ 8), columns this lane's two heads
+        const int live = cc.s.T - pos0;
+        if (live < WP) {
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (u * 16 + g + (e >> 1) * 8 >= live) s[u][nt][e] = -INFINITY;
+        }
+        float top[2 * NT];
+        bool grew = false;
 #pragma unroll
         for (int i = 0; i < 2 * NT; ++i) {
-          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 4));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 8));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 16));
+          float x = s[0][i >> 1][i & 1];
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+            x = fmaxf(x, fmaxf(s[u][i >> 1][i & 1], s[u][i >> 1][2 + (i & 1)]));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+          top[i] = fmaxf(m[i], x * sc[KIND == kE4m3 ? i : 0]);  // (the scale is positive)
           grew = grew || top[i] > m[i];
         }
         if (__any_sync(~0u, grew)) {
@@ -435,6 +500,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
             }
           }
         }
+        float less[2 * NT];
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i)
+          less[i] = (KIND == kE4m3 ? kShift : 0.f) - (m[i] == -INFINITY ? 0.f : m[i]);
         uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
@@ -445,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
               float w[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float base = m[2 * nt + e] == -INFINITY ? 0.f : m[2 * nt + e];
-                w[e] = ex2(s[u][nt][2 * half + e] - base + (KIND == kE4m3 ? kShift : 0.f));
+                w[e] = ex2(fmaf(s[u][nt][2 * half + e], sc[KIND == kE4m3 ? 2 * nt + e : 0],
+                                less[2 * nt + e]));
                 l[2 * nt + e] += w[e];
               }
               if constexpr (KIND == kBf16) {
@@ -487,10 +556,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
               ldmatrix4_trans(at + (((c + (mi >> 1)) ^ swz_k) << 4), x);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t y0 = __byte_perm(x[2 * h], 0, 0x3120);
-                const uint32_t y1 = __byte_perm(x[2 * h + 1], 0, 0x3120);
-                const uint32_t a[4] = {e4m3x2_to_half2(y0), e4m3x2_to_half2(y0 >> 16),
-                                       e4m3x2_to_half2(y1), e4m3x2_to_half2(y1 >> 16)};
+                uint32_t a[4];
+                e4m3x4_to_half2(__byte_perm(x[2 * h], 0, 0x3120), a[0], a[1]);
+                e4m3x4_to_half2(__byte_perm(x[2 * h + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma_16816_f16(o[c + h][nt], a, hi[u][nt][0], hi[u][nt][1]);
@@ -570,7 +638,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
 
     // ---- the segment ends here, or this share does
     const bool ends = cc.j == cc.s.n - 1;
-    if (ends || t == t1 - 1) {
+    const Cursor<S::TILE> at = cc;
+    cc.next(p, t1);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    if (ends || cc.t >= t1) {
+      begin = true;
+      const float v_scale = vs;
+      if (cc.t < t1) load_queries(cc);
+      const int head0 = at.kvh * p.group + at.rt * ROWS;
+      const int rows = min(ROWS, p.group - at.rt * ROWS);
       // the warps' parts, joined over shared memory 32 columns at a time
       if constexpr (KIND == kFp32) {
 #pragma unroll
@@ -597,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
         const int r = KIND == kFp32 ? i : (i >> 1) * 8 + quad * 2 + (i & 1);
         float top = s_ml[r].x;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w * ROWS + r].x);
+        for (int w = 1; w < NW; ++w) top = fmaxf(top, s_ml[w * ROWS + r].x);
         f[i] = ex2(m[i] - (top == -INFINITY ? 0.f : top));
       }
       // the reducing threads' row: its maximum and sum
@@ -605,21 +681,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
       float M = -INFINITY, L = 0.f;
       if (rr < ROWS) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * ROWS + rr].x);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w * ROWS + rr].x);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
           const float2 x = s_ml[w * ROWS + rr];
           L += x.y * ex2(x.x - (M == -INFINITY ? 0.f : M));
         }
       }
       const bool cut = !(whole && ends);
       const int slot = whole ? 2 * cta + 1 : 2 * cta;
-      const float vs = KIND == kE4m3 && p.v_scale ? p.v_scale[kvh] : 1.f;
-      const float inv = L == 0.f ? 0.f : vs / L;
-      const int64_t head = (int64_t)cc.b * p.heads + head0 + rr;
+      const float inv = L == 0.f ? 0.f : v_scale / L;
+      const int64_t head = (int64_t)at.b * p.heads + head0 + rr;
 #pragma unroll
       for (int c0 = 0; c0 < DP; c0 += 32) {
-        float* mine_buf = s_merge + warp * ROWS * S::MSTRIDE;
+        float* buf = s_merge + (S::MBUFS == 2 && (c0 & 32) ? S::MBUF : 0);
+        float* mine_buf = buf + warp * ROWS * S::MSTRIDE;
         if constexpr (KIND == kFp32) {
           if ((lane >> 3) == (c0 >> 5) % 4) {
 #pragma unroll
@@ -644,9 +720,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
         if (rr < rows && c0 + c4 < p.dim) {
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
+          for (int w = 0; w < NW; ++w) {
             const float4 x = *reinterpret_cast<const float4*>(
-                s_merge + (w * ROWS + rr) * S::MSTRIDE + c4);
+                buf + (w * ROWS + rr) * S::MSTRIDE + c4);
             a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
           }
           if (cut) {
@@ -659,7 +735,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
                 make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
           }
         }
-        __syncthreads();
+        // (with two buffers the next round's barrier comes before this one is written again)
+        if (S::MBUFS == 1 || c0 + 32 >= DP) __syncthreads();
       }
       if (rr < rows && c4 == 0) {
         if (cut)
@@ -670,22 +747,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, KIND, NT>::OCC))
       }
       if (whole && !ends) {
         // the segment's last tile lies in CTA ((te + 1) ctas - 1) / total
-        const long long te = t + (cc.s.n - 1 - cc.j);
-        rec.b = cc.b;
-        rec.hr = cc.hr;
+        const long long te = at.t + (at.s.n - 1 - at.j);
+        rec.b = at.b;
+        rec.kvh = at.kvh;
+        rec.rt = at.rt;
         rec.parts = (int)(((te + 1) * ctas - 1) / total) - cta + 1;
       }
     }
-    if (t + 1 < t1) cc.next(p);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
   if (tid == 0 && p.rec) p.rec[cta] = rec;
+  zero_idle<S::TILE, KIND>(p);
 }
 
 template <int DP, int KIND, int NT>
 Kernel kernel_of() {
   using S = Shape<DP, KIND, NT>;
-  return {decode_attn_sm103<DP, KIND, NT>, S::SMEM, S::OCC, S::TILE, S::ROWS, DP};
+  return {decode_attn_sm103<DP, KIND, NT>, S::SMEM, S::THREADS, S::OCC, S::TILE, S::ROWS, DP};
 }
 
 template <int KIND>
