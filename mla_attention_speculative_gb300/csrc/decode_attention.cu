@@ -97,70 +97,100 @@ mla_status_t kv_cache_ok(const mla_kv_geometry_t* g, const mla_kv_cache_t* c) {
 namespace decode {
 namespace {
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinLoads = 8;  // parts a thread asks for at once
 
-// One CTA per (share, row): where a segment's first part ends a share, the
-// parts of this row, in this share and the next ones, are weighted by
-// exp(m - max m) and summed in order.  The parts are few and small (16 rows of
-// 512 bytes a share at most), so this is bound by latency: every weight is
-// made at once, then groups of threads walk over the parts side by side.
+// The parts of a row, in the share its segment begins in and the next ones,
+// are weighted by exp(m - max m) and summed in order.  They are few and small
+// (16 rows of 1 KB a share at most), so this is bound by the latency of its
+// loads: TPR threads take a row, groups of them walk over the parts side by
+// side with kJoinLoads parts on their way at once, the first of them while the
+// weights are made.  Few segments have many parts each: then a whole CTA
+// takes a row (T = 131072: 50.1 us a call against 51.5 with 64 threads);
+// many segments have few: 64 threads a row leave fewer CTAs with nothing to do.
+template <int TPR>
 __global__ void __launch_bounds__(kJoinThreads)
     decode_join_kernel(const Params p, const int rows_max, const int dp, const int kind) {
-  __shared__ float s_w[kMaxCtas];
-  __shared__ float s_red[kJoinThreads / 32];
+  constexpr int RPC = kJoinThreads / TPR, WPR = TPR / 32;
+  __shared__ float s_w[RPC][kMaxCtas], s_l[RPC][kMaxCtas];
+  __shared__ float s_red[RPC][WPR];
   __shared__ float4 s_acc[kJoinThreads];
   sm103::pdl_wait();
-  const int cta = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-  const Record rec = p.rec[cta];
+  const int tid = threadIdx.x, r = tid / TPR, i0 = tid % TPR, row = blockIdx.y * RPC + r;
+  const Record rec = p.rec[blockIdx.x];
   if (rec.parts == 0) return;
-  const int kvh = rec.kvh, rt = rec.rt;
-  if (row >= p.group - rt * rows_max) return;
-  // part k: the last segment of this share, then the first one of the shares behind it
-  auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
+  const int kvh = rec.hr / p.row_tiles, rt = rec.hr - kvh * p.row_tiles;
+  const bool live = row < min(rows_max, p.group - rt * rows_max);
+  const int parts = live ? rec.parts : 0;
+  // part k: the last segment of the first share, then the first one of those behind it
+  auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * rec.cta + 1 : 2 * (rec.cta + k)); };
   float M = -INFINITY;
-  for (int k = tid; k < rec.parts; k += kJoinThreads)
-    M = fmaxf(M, p.part_ml[slot(k) * rows_max + row].x);
+  for (int k = i0; k < parts; k += TPR) {
+    const float2 ml = p.part_ml[slot(k) * rows_max + row];
+    s_w[r][k] = ml.x;
+    s_l[r][k] = ml.y;
+    M = fmaxf(M, ml.x);
+  }
+  const int cols = dp / 4, groups = TPR / cols;
+  const int grp = i0 / cols, c = i0 - grp * cols;
+  const float* part = p.part_o + (int64_t)row * dp + c * 4;
+  const int64_t step = (int64_t)rows_max * dp;
+  float4 x[kJoinLoads];
+  auto ask = [&](int k0) {
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-  if ((tid & 31) == 0) s_red[tid >> 5] = M;
+    for (int i = 0; i < kJoinLoads; ++i) {
+      const int k = k0 + i * groups;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < parts) x[i] = *reinterpret_cast<const float4*>(part + slot(k) * step);
+    }
+  };
+  if (grp < groups) ask(grp);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+  if ((tid & 31) == 0) s_red[r][i0 >> 5] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+#pragma unroll
+  for (int w = 0; w < WPR; ++w) M = fmaxf(M, s_red[r][w]);
   const float base = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int k = tid; k < rec.parts; k += kJoinThreads) {
-    const float2 ml = p.part_ml[slot(k) * rows_max + row];
-    const float w = sm103::ex2(ml.x - base);
-    s_w[k] = w;
-    L += w * ml.y;
+  for (int k = i0; k < parts; k += TPR) {
+    const float w = sm103::ex2(s_w[r][k] - base);
+    s_w[r][k] = w;
+    L += w * s_l[r][k];
   }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
   __syncthreads();
-  if ((tid & 31) == 0) s_red[tid >> 5] = L;
+  if ((tid & 31) == 0) s_red[r][i0 >> 5] = L;
   __syncthreads();
-  L = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < WPR; ++w) L += s_red[r][w];
 
-  const int cols = dp / 4, groups = kJoinThreads / cols;
-  const int grp = tid / cols, c = tid - grp * cols;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (grp < groups) {
-#pragma unroll 4
-    for (int k = grp; k < rec.parts; k += groups) {
-      const float4 x = *reinterpret_cast<const float4*>(
-          p.part_o + (slot(k) * rows_max + row) * dp + c * 4);
-      const float w = s_w[k];
-      a.x = fmaf(w, x.x, a.x);
-      a.y = fmaf(w, x.y, a.y);
-      a.z = fmaf(w, x.z, a.z);
-      a.w = fmaf(w, x.w, a.w);
+    for (int k0 = grp; k0 < parts; k0 += groups * kJoinLoads) {
+      if (k0 > grp) ask(k0);
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {
+        const int k = k0 + i * groups;
+        if (k < parts) {
+          const float w = s_w[r][k];
+          a.x = fmaf(w, x[i].x, a.x);
+          a.y = fmaf(w, x[i].y, a.y);
+          a.z = fmaf(w, x[i].z, a.z);
+          a.w = fmaf(w, x[i].w, a.w);
+        }
+      }
     }
   }
   s_acc[tid] = a;
   __syncthreads();
+  if (!live) return;
   const int64_t head = (int64_t)rec.b * p.heads + kvh * p.group + rt * rows_max + row;
-  if (tid < cols && c * 4 < p.dim) {
-    for (int x = 1; x < groups; ++x) {
-      const float4 y = s_acc[x * cols + c];
+  if (i0 < cols && c * 4 < p.dim) {
+    for (int g = 1; g < groups; ++g) {
+      const float4 y = s_acc[r * TPR + g * cols + c];
       a.x += y.x;
       a.y += y.y;
       a.z += y.z;
@@ -175,7 +205,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c * 4) = make_uint2(
           sm103::pack_bf16(a.x * inv, a.y * inv), sm103::pack_bf16(a.z * inv, a.w * inv));
   }
-  if (tid == 0 && p.lse)
+  if (i0 == 0 && p.lse)
     p.lse[head] = L == 0.f ? -INFINITY
                            : (M + log2f(L) - (kind == kE4m3 ? kShift : 0.f)) * 0.6931471805599453f;
 }
@@ -184,7 +214,9 @@ __global__ void __launch_bounds__(kJoinThreads)
 struct Plan {
   Kernel k;
   int kind, row_tiles, ctas;
-  bool cut;  // a segment may fall into several shares
+  bool cut;         // a segment may fall into several shares
+  bool by_segment;  // records by segment: fewer than CTAs
+  int records;
   size_t off_ml, off_o, bytes;
 };
 
@@ -214,7 +246,9 @@ mla_status_t make_plan(const mla_kv_geometry_t* g, int32_t batch, int32_t page_s
   if (ctas > most) ctas = most;
   d.ctas = (int)ctas;
   d.cut = tiles > 1;
-  size_t off = align256(sizeof(Record) * ctas);
+  d.by_segment = batch * hrs <= ctas;
+  d.records = d.by_segment ? (int)(batch * hrs) : (int)ctas;
+  size_t off = align256(sizeof(Record) * d.records);
   d.off_ml = off;
   off = align256(off + sizeof(float2) * 2 * ctas * d.k.rows);
   d.off_o = off;
@@ -256,17 +290,28 @@ cudaError_t launch(const Plan& d, const Params& p, cudaStream_t stream) {
   cfg.dynamicSmemBytes = d.k.smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  // Equal shares need the CTAs spread evenly over the SMs.  Started while the
+  // kernel ahead still holds parts of them (as its dependent), they end up
+  // three on one SM and none on another: 452 us for 32 sequences of up to
+  // 32768 positions, against 327.  A call of single tiles has no such shares
+  // and saves 0.4 of its 4.2 us.
+  cfg.numAttrs = d.cut ? 0 : 1;
   {
     KernelTimer kt("decode_attn", stream);
     e = cudaLaunchKernelEx(&cfg, d.k.fn, p);
   }
   if (e != cudaSuccess || !d.cut) return e;
-  cfg.gridDim = dim3((unsigned)d.ctas, (unsigned)(p.group < d.k.rows ? p.group : d.k.rows));
+  cfg.numAttrs = 1;
+  const int rows = p.group < d.k.rows ? p.group : d.k.rows;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   KernelTimer kt("decode_join", stream);
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel, p, d.k.rows, d.k.dp, d.kind);
+  if (d.by_segment) {
+    cfg.gridDim = dim3((unsigned)d.records, (unsigned)rows);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<kJoinThreads>, p, d.k.rows, d.k.dp, d.kind);
+  }
+  cfg.gridDim = dim3((unsigned)d.records, (unsigned)((rows * 64 + kJoinThreads - 1) / kJoinThreads));
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<64>, p, d.k.rows, d.k.dp, d.kind);
 }
 
 }  // namespace
@@ -366,6 +411,7 @@ extern "C" mla_status_t mla_decode_attention(
   p.out = out;
   p.lse = lse;
   p.rec = d.cut ? (decode::Record*)workspace : nullptr;
+  p.by_segment = d.by_segment ? 1 : 0;
   p.part_ml = d.cut ? (float2*)((char*)workspace + d.off_ml) : nullptr;
   p.part_o = d.cut ? (float*)((char*)workspace + d.off_o) : nullptr;
   p.heads = g->num_heads;

@@ -51,7 +51,7 @@ struct Shape {
   static constexpr int RING = NW * STAGES * STAGE;
   static constexpr int MSTRIDE = 36;  // floats of a merge row: 32 columns, padded
   // two buffers, so that a round of the merge needs one barrier, where they fit
-  static constexpr int MBUFS = NW * ROWS <= 32 && OCC < 3 ? 2 : 1;
+  static constexpr int MBUFS = NW * ROWS <= 32 ? 2 : 1;
   static constexpr int MBUF = NW * ROWS * MSTRIDE;  // floats of one
   static constexpr int MERGE = MBUFS * MBUF * 4;
   static constexpr int STATS = NW * ROWS * 8;
@@ -64,10 +64,11 @@ struct Shape {
   static_assert(OCC * (SMEM + 1024 + 256) <= 228 * 1024, "OCC CTAs do not fit an SM");
 };
 
-// What a CTA leaves for the join: the segment whose first part it holds (as
-// its last one), and in how many parts, in this CTA and the next ones.
+// What is left for the join of a segment: the CTA whose share it begins in, as
+// its last segment, and how many shares hold a part of it, that one and the
+// next ones (0: nothing to join).
 struct Record {
-  int b, kvh, rt, parts;
+  int cta, parts, b, hr;
 };
 
 struct Params {
@@ -80,7 +81,8 @@ struct Params {
   const int32_t* table;
   void* out;
   float* lse;
-  Record* rec;     // [ctas]; NULL: no sequence is cut
+  Record* rec;     // by segment or by CTA; NULL: no sequence is cut
+  int by_segment;
   float2* part_ml; // [2 * ctas][ROWS] running maximum (base 2) and sum
   float* part_o;   // [2 * ctas][ROWS][DP] unnormalised
   int heads, kv_heads, group, row_tiles, dim, batch, page, width, num_pages, window;

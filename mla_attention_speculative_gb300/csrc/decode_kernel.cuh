@@ -104,7 +104,8 @@ struct Cursor {
   }
 };
 
-// Sequences with nothing to see have no tiles: their outputs, dealt over the CTAs.
+// Sequences with nothing to see have no tiles: their outputs (and records),
+// dealt over the CTAs.
 template <int TILE, int KIND>
 __device__ __forceinline__ void zero_idle(const Params& p) {
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -115,6 +116,11 @@ __device__ __forceinline__ void zero_idle(const Params& p) {
     if (p.lse)
       for (int h = threadIdx.x; h < p.heads; h += blockDim.x)
         p.lse[(int64_t)b * p.heads + h] = -INFINITY;
+    if (p.rec && p.by_segment) {
+      const int hrs = p.kv_heads * p.row_tiles;
+      for (int i = threadIdx.x; i < hrs; i += blockDim.x)
+        p.rec[(int64_t)b * hrs + i].parts = 0;
+    }
   }
 }
 
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   const int ctas = (int)min((long long)gridDim.x, total);
   const int cta = blockIdx.x;
   if (cta >= ctas) {
-    if (tid == 0 && p.rec) p.rec[cta].parts = 0;
+    if (tid == 0 && p.rec && !p.by_segment) p.rec[cta].parts = 0;
     zero_idle<S::TILE, KIND>(p);
     return;
   }
@@ -574,8 +580,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) s[r] = 0.f;
 #pragma unroll 4
-        for (int i = 0; i < CH / 4; ++i) {
-          const int c = part + 4 * i;
+        for (int c = part; c < chunks; c += 4) {
           const float4 x = *reinterpret_cast<const float4*>(kp + ((c ^ row) << 4));
 #pragma unroll
           for (int r = 0; r < ROWS; ++r) {
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             const int c = nb * 32 + lane;
-            if (c < CH) {
+            if (c < chunks) {
               const float4 x = *reinterpret_cast<const float4*>(vp + ((c ^ (t8 & 7)) << 4));
 #pragma unroll
               for (int r = 0; r < ROWS; ++r) {
@@ -748,14 +753,17 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
       if (whole && !ends) {
         // the segment's last tile lies in CTA ((te + 1) ctas - 1) / total
         const long long te = at.t + (at.s.n - 1 - at.j);
+        rec.cta = cta;
         rec.b = at.b;
-        rec.kvh = at.kvh;
-        rec.rt = at.rt;
+        rec.hr = at.kvh * p.row_tiles + at.rt;
         rec.parts = (int)(((te + 1) * ctas - 1) / total) - cta + 1;
       }
+      // (the CTA in which a segment begins writes its record)
+      if (tid == 0 && p.rec && p.by_segment && whole)
+        p.rec[(int64_t)at.b * hrs + at.kvh * p.row_tiles + at.rt] = rec;
     }
   }
-  if (tid == 0 && p.rec) p.rec[cta] = rec;
+  if (tid == 0 && p.rec && !p.by_segment) p.rec[cta] = rec;
   zero_idle<S::TILE, KIND>(p);
 }
 
