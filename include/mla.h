@@ -404,7 +404,7 @@ mla_status_t mla_indexer_select(const float* q, const float* pooled, int64_t poo
  * rejection) and appends new_tokens[b] >= 0 rows (0: an idle slot); its table
  * row holds held_pages[b] pages.  With P = page_size and W =
  * max_pages_per_seq:
- *   total  = min(kept + new, W * P)
+ *   total  = min(kept + new, W * P, INT32_MAX)
  *   grow   = max(0, ceil(total / P) - held)       pages it asks for
  *   got    = the first `grow` pages left on the free list after the sequences
  *            before it took theirs (fewer when the list runs out)
@@ -429,7 +429,7 @@ mla_status_t mla_indexer_select(const float* q, const float* pooled, int64_t poo
  *          Rows beyond max_rows are dropped.
  *  free_span_out  device [2]: {free_span[0] + pages taken, free_span[1]}
  *  missing_out  device [1]: pages asked for that the list did not have (0:
- *          every sequence got its pages; saturates at INT32_MAX)
+ *          every sequence got its pages)
  *
  * batch in [1, 65535]; batch * W at most 2^31 - 1.  max_rows and
  * free_capacity may be 0.  Outputs must not overlap inputs (page_table is

@@ -421,12 +421,7 @@ extern "C" mla_status_t mla_decode_attention(
   p.dim = g->head_dim;
   p.batch = batch;
   p.page = cache->page_size;
-  // with 2^(s-1) < page <= 2^s, m = ceil(2^(31+s) / page) < 2^32 overshoots by
-  // less than page, so pos m / 2^(31+s) is off by less than pos / 2^31 / 2^s < 1 / page
-  int s = 0;
-  while (((int64_t)1 << s) < p.page) ++s;
-  p.page_shift = 31 + s;
-  p.page_magic = (uint32_t)((((uint64_t)1 << (31 + s)) + (uint64_t)p.page - 1) / (uint64_t)p.page);
+  p.div = PageDiv(cache->page_size);
   p.width = max_pages_per_seq;
   p.num_pages = cache->num_pages;
   p.window = window;

@@ -86,9 +86,7 @@ struct Params {
   float2* part_ml; // [2 * ctas][ROWS] running maximum (base 2) and sum
   float* part_o;   // [2 * ctas][ROWS][DP] unnormalised
   int heads, kv_heads, group, row_tiles, dim, batch, page, width, num_pages, window;
-  // pos / page == (pos * page_magic) >> page_shift for 0 <= pos < 2^31
-  uint32_t page_magic;
-  int page_shift;
+  PageDiv div;  // by `page`
   float scale_log2;  // softmax scale * log2(e)
 };
 

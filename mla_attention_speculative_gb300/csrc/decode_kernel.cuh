@@ -293,7 +293,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     r.off = -1;
     r.id = 0;
     if (pos < lc.s.T) {
-      const int pg = (int)(((uint64_t)(uint32_t)pos * p.page_magic) >> p.page_shift);
+      const int pg = p.div(pos);
       r.id = p.table[(int64_t)lc.b * p.width + pg];
       r.off = (int64_t)(pos - pg * p.page) * p.row_stride + lc.kvh * p.head_stride;
     }

@@ -139,6 +139,25 @@ int indexer_device_status(bool clear);
 int paged_device_status(bool clear);
 int decode_device_status(bool clear);
 
+// Division by a page size of 1 .. 2^31 - 1, of positions below 2^31.  With
+// 2^(s-1) < page <= 2^s, m = ceil(2^(31+s) / page) < 2^32 overshoots by less
+// than one page in 2^(31+s), so pos m / 2^(31+s) is less than 1 / page above
+// pos / page: the floor is the same.
+struct PageDiv {
+  uint32_t magic = 0;
+  int shift = 31;
+  PageDiv() = default;
+  explicit PageDiv(int page) {
+    int s = 0;
+    while (((int64_t)1 << s) < page) ++s;
+    shift = 31 + s;
+    magic = (uint32_t)((((uint64_t)1 << shift) + (uint64_t)page - 1) / (uint64_t)page);
+  }
+  __host__ __device__ int operator()(int pos) const {
+    return (int)(((uint64_t)(uint32_t)pos * magic) >> shift);
+  }
+};
+
 // Argument checks shared by the entry points; false / a failing status means
 // set_error() has said why.
 bool geometry_ok(const mla_geometry_t* g);

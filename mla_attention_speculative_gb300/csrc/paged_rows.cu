@@ -35,18 +35,17 @@ namespace {
 // ---------------------------------------------------------------------------
 //
 // Two exclusive sums over the sequences (rows, pages asked for) place every
-// row and every new page; the rest is one lookup per row.  Each CTA computes
-// both sums itself, 2048 sequences at a time, so no CTA waits for another:
-// the counts (12 bytes a sequence) stay in L2, and a step has far more rows
-// than sequences or is bound by launch latency anyway.  The rows are split
-// over the CTAs evenly, whatever their sequences; a row finds its sequence by
-// a binary search over the sums in shared memory.  New pages are read from
-// the free list by position, never from the table that this launch writes.
+// row and every new page; the rest is one lookup each.  A CTA computes the
+// sums itself, a run of sequences per thread, so no CTA waits for another: the
+// counts (12 bytes a sequence) stay in L2, and a step has far more rows than
+// sequences or is bound by latency anyway.  The sums of up to 4096 sequences
+// (beyond: of groups of sequences) stay in shared memory, where each row, each
+// new page and each sequence, dealt out evenly over all threads, finds its
+// place by a binary search.  New pages are read from the free list by
+// position, never from the table that this launch writes.
 
-constexpr int kStepThreads = 512;
-constexpr int kSeqPerThread = 4;
-constexpr int kSeqPerPass = kStepThreads * kSeqPerThread;
 constexpr int kRowsPerThread = 4;
+constexpr int kEntries = 4096;  // sums kept in shared memory
 
 struct PageStepParams {
   const int32_t* kept;
@@ -63,181 +62,222 @@ struct PageStepParams {
   int32_t* span_out;
   int32_t* missing;
   int batch, width, page, num_pages, free_capacity, max_rows;
+  int capacity;  // rows of a table's pages, INT_MAX at most
   int rows_per_cta;
+  PageDiv div;
 };
 
-struct Pair64 {
-  long long rows, pages;
+struct Sums {
+  long long rows;
+  int pages;  // (batch * width < 2^31)
 };
 
 __device__ __forceinline__ int sat32(long long x) { return x > INT_MAX ? INT_MAX : (int)x; }
 
-// The pages sequence b asks for, and its (clamped) counts.
-__device__ __forceinline__ void sequence_counts(const PageStepParams& p, int b, int& kept,
-                                                int& fresh, int& held, int& grow) {
-  kept = max(p.kept[b], 0);
-  fresh = max(p.fresh[b], 0);
-  held = min(max(p.held[b], 0), p.width);
-  const long long total = min((long long)kept + fresh, (long long)p.width * p.page);
-  const int need = (int)((total + p.page - 1) / p.page);
-  grow = max(0, need - held);
+// One sequence: its clamped counts, the pages it asks for, and (once the sums
+// before it are known) what it gets.
+struct Sequence {
+  int kept, fresh, held, total, grow;
+  __device__ __forceinline__ void load(const PageStepParams& p, int b) {
+    set(p, p.kept[b], p.fresh[b], p.held[b]);
+  }
+  __device__ __forceinline__ void set(const PageStepParams& p, int k, int f, int h) {
+    kept = max(k, 0);
+    fresh = max(f, 0);
+    held = min(max(h, 0), p.width);
+    total = (int)min((uint32_t)kept + (uint32_t)fresh, (uint32_t)p.capacity);
+    grow = total > 0 ? max(0, p.div(total - 1) + 1 - held) : 0;
+  }
+  __device__ __forceinline__ int got(int have, int pages) const {
+    return min(grow, max(0, have - pages));
+  }
+};
+
+// The last of n ascending sums that is at or before x.
+__device__ __forceinline__ int find_entry(const int* sums, int n, int x) {
+  int a = 0, z = n;
+  while (z - a > 1) {
+    const int m = (a + z) >> 1;
+    if (sums[m] <= x) a = m; else z = m;
+  }
+  return a;
 }
 
-__global__ void __launch_bounds__(kStepThreads) page_step_kernel(PageStepParams p) {
-  __shared__ long long s_row[kSeqPerPass + 1];   // first row of each sequence
-  __shared__ int s_base[kSeqPerPass + 1];        // pages asked for before it
-  __shared__ int s_kept[kSeqPerPass];
-  __shared__ int s_held[kSeqPerPass];
-  __shared__ Pair64 s_warp[kStepThreads / 32];
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    page_step_kernel(const PageStepParams p) {
+  // before each entry's sequences (rows saturate: no row that is wanted lies there)
+  __shared__ int s_row[kEntries], s_page[kEntries];
+  __shared__ Sums s_warp[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = min(max(p.free_span[0], 0), p.free_capacity);
-  const int end = min(max(p.free_span[1], first), p.free_capacity);
+  const int span0 = p.free_span[0], span1 = p.free_span[1];
+
+  // ---- the sums; `per` consecutive sequences a thread, `size` an entry
+  const int size = (p.batch + kEntries - 1) / kEntries;
+  const int per = ((p.batch + THREADS - 1) / THREADS + size - 1) / size * size;
+  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  Sums mine = {0, 0};
+  Sequence q;
+  int b = b0;
+  if (per % 4 == 0) {
+    for (; b + 4 <= b1; b += 4) {
+      const int4 k4 = *reinterpret_cast<const int4*>(p.kept + b);
+      const int4 f4 = *reinterpret_cast<const int4*>(p.fresh + b);
+      const int4 h4 = *reinterpret_cast<const int4*>(p.held + b);
+      const int k[4] = {k4.x, k4.y, k4.z, k4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w},
+                h[4] = {h4.x, h4.y, h4.z, h4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q.set(p, k[i], f[i], h[i]);
+        mine.rows += q.fresh;
+        mine.pages += q.grow;
+      }
+    }
+  }
+  for (; b < b1; ++b) {
+    q.load(p, b);
+    mine.rows += q.fresh;
+    mine.pages += q.grow;
+  }
+  Sums sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long r = __shfl_up_sync(~0u, sum.rows, o);
+    const int g = __shfl_up_sync(~0u, sum.pages, o);
+    if (lane >= o) {
+      sum.rows += r;
+      sum.pages += g;
+    }
+  }
+  if (lane == 31) s_warp[warp] = sum;
+  __syncthreads();
+  Sums all = {0, 0};
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const Sums x = s_warp[w];
+    if (w < warp) {
+      sum.rows += x.rows;
+      sum.pages += x.pages;
+    }
+    all.rows += x.rows;
+    all.pages += x.pages;
+  }
+  {
+    Sums base = {sum.rows - mine.rows, sum.pages - mine.pages};
+    for (int b = b0; b < b1; b += size) {
+      s_row[b / size] = sat32(base.rows);
+      s_page[b / size] = base.pages;
+      for (int i = 0; i < size && b + i < b1; ++i) {
+        if (per == 1) break;
+        q.load(p, b + i);
+        base.rows += q.fresh;
+        base.pages += q.grow;
+      }
+    }
+  }
+  __syncthreads();
+  const int entries = (p.batch + size - 1) / size;
+  const int first = min(max(span0, 0), p.free_capacity);
+  const int end = min(max(span1, first), p.free_capacity);
   const int have = end - first;
+
+  // ---- this CTA's rows, four consecutive ones a thread
   const long long r0 = (long long)blockIdx.x * p.rows_per_cta;
   const long long r1 = min(r0 + p.rows_per_cta, (long long)p.max_rows);
-  Pair64 carry = {0, 0};
-
-  for (int b0 = 0; b0 < p.batch; b0 += kSeqPerPass) {
-    const int nb = min(kSeqPerPass, p.batch - b0);
-    int kept[kSeqPerThread], fresh[kSeqPerThread], held[kSeqPerThread], grow[kSeqPerThread];
-    Pair64 mine = {0, 0};
+  for (long long g = r0 + tid * kRowsPerThread; g < r1; g += THREADS * kRowsPerThread) {
+    int pos4[kRowsPerThread], id4[kRowsPerThread], off4[kRowsPerThread];
+    const int live = (int)max(0ll, min((long long)kRowsPerThread, all.rows - g));
+    int b = -1, owned = 0;
+    long long rows = 0;  // the sums before sequence b
+    int pages = 0;
 #pragma unroll
-    for (int i = 0; i < kSeqPerThread; ++i) {
-      const int s = tid * kSeqPerThread + i;
-      kept[i] = fresh[i] = held[i] = grow[i] = 0;
-      if (s < nb) sequence_counts(p, b0 + s, kept[i], fresh[i], held[i], grow[i]);
-      mine.rows += fresh[i];
-      mine.pages += grow[i];
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      pos4[i] = -1;
+      id4[i] = -1;
+      off4[i] = -1;  // no page
+      if (i >= live) continue;
+      if (b < 0) {
+        const int e = find_entry(s_row, entries, (int)g);
+        b = e * size;
+        rows = s_row[e];
+        pages = s_page[e];
+        q.load(p, b);
+        owned = q.held + q.got(have, pages);
+      }
+      while (g + i >= rows + q.fresh) {
+        rows += q.fresh;
+        pages += q.grow;
+        q.load(p, ++b);
+        owned = q.held + q.got(have, pages);
+      }
+      const long long pos = q.kept + (g + i - rows);
+      pos4[i] = sat32(pos);
+      if (pos >= q.total) continue;
+      const int page = p.div((int)pos);
+      if (page < owned) {
+        off4[i] = (int)pos - page * p.page;
+        id4[i] = page < q.held ? p.table[(long long)b * p.width + page]
+                               : p.free_pages[first + pages + (page - q.held)];
+      }
     }
-    Pair64 sum = mine;
+    long long slot4[kRowsPerThread];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long r = __shfl_up_sync(~0u, sum.rows, o);
-      const long long g = __shfl_up_sync(~0u, sum.pages, o);
-      if (lane >= o) {
-        sum.rows += r;
-        sum.pages += g;
-      }
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      slot4[i] = -1;
+      if (off4[i] < 0) continue;
+      if (id4[i] >= 0 && id4[i] < p.num_pages) slot4[i] = (long long)id4[i] * p.page + off4[i];
+      else atomicCAS(&g_paged_status, 0, kBadPageSite);
     }
-    __syncthreads();  // the previous pass has read the arrays
-    if (lane == 31) s_warp[warp] = sum;
-    __syncthreads();
-    Pair64 base = carry;
-    for (int w = 0; w < kStepThreads / 32; ++w) {
-      const Pair64 x = s_warp[w];
-      if (w < warp) {
-        base.rows += x.rows;
-        base.pages += x.pages;
-      }
-      carry.rows += x.rows;
-      carry.pages += x.pages;
-    }
-    base.rows += sum.rows - mine.rows;
-    base.pages += sum.pages - mine.pages;
-    // (batch * width < 2^31, so the pages asked for fit an int)
-#pragma unroll
-    for (int i = 0; i < kSeqPerThread; ++i) {
-      const int s = tid * kSeqPerThread + i;
-      if (s < nb) {
-        s_row[s] = base.rows;
-        s_base[s] = (int)base.pages;
-        s_kept[s] = kept[i];
-        s_held[s] = held[i];
-        if ((b0 / kSeqPerPass) % gridDim.x == blockIdx.x) {
-          const int got = min(grow[i], max(0, have - (int)base.pages));
-          const int b = b0 + s;
-          const long long total = min((long long)kept[i] + fresh[i], (long long)p.width * p.page);
-          p.held_out[b] = held[i] + got;
-          p.lens_out[b] = (int)min(min(total, (long long)(held[i] + got) * p.page),
-                                   (long long)INT_MAX);
-          p.row_start[b] = sat32(base.rows);
-        }
-      }
-      base.rows += fresh[i];
-      base.pages += grow[i];
-    }
-    if (tid == 0) {
-      s_row[nb] = carry.rows;
-      s_base[nb] = (int)carry.pages;
-    }
-    __syncthreads();
-
-    // new table entries: a warp per sequence, the sequences dealt over all warps
-    for (int s = blockIdx.x * (kStepThreads / 32) + warp; s < nb;
-         s += gridDim.x * (kStepThreads / 32)) {
-      const int got = min(s_base[s + 1] - s_base[s], max(0, have - s_base[s]));
-      const int32_t* src = p.free_pages + first + s_base[s];
-      int32_t* dst = p.table + (long long)(b0 + s) * p.width + s_held[s];
-      for (int j = lane; j < got; j += 32) dst[j] = src[j];
-    }
-
-    // this CTA's rows among the pass's sequences, four consecutive rows a thread
-    const long long lo = max(r0, s_row[0]), hi = min(r1, s_row[nb]);
-    const long long start = lo & ~(long long)(kRowsPerThread - 1);
-    for (long long g = start + tid * kRowsPerThread; g < hi;
-         g += kStepThreads * kRowsPerThread) {
-      const long long from = max(g, lo), to = min(g + kRowsPerThread, hi);
-      int a = 0, z = nb;  // the last sequence whose first row is at or before `from`
-      while (z - a > 1) {
-        const int m = (a + z) >> 1;
-        if (s_row[m] <= from) a = m; else z = m;
-      }
-      int pos4[kRowsPerThread];
-      long long slot4[kRowsPerThread];
+    if (g + kRowsPerThread <= r1) {
+      *reinterpret_cast<int4*>(p.positions + g) = make_int4(pos4[0], pos4[1], pos4[2], pos4[3]);
+      longlong2* d = reinterpret_cast<longlong2*>(p.slots + g);
+      d[0] = make_longlong2(slot4[0], slot4[1]);
+      d[1] = make_longlong2(slot4[2], slot4[3]);
+    } else {
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i) {
-        const long long row = g + i;
-        pos4[i] = -1;
-        slot4[i] = -1;
-        if (row < from || row >= to) continue;
-        while (row >= s_row[a + 1]) ++a;
-        const long long pos = s_kept[a] + (row - s_row[a]);
-        pos4[i] = sat32(pos);
-        const long long page_no = (pos >> 32) == 0
-                                      ? (long long)((uint32_t)pos / (uint32_t)p.page)
-                                      : pos / p.page;
-        const int off = (int)(pos - page_no * p.page);
-        const int have_pages =
-            s_held[a] + min(s_base[a + 1] - s_base[a], max(0, have - s_base[a]));
-        if (page_no < have_pages) {
-          const int j = (int)page_no;
-          const int id = j < s_held[a]
-                             ? p.table[(long long)(b0 + a) * p.width + j]
-                             : p.free_pages[first + s_base[a] + (j - s_held[a])];
-          if (id >= 0 && id < p.num_pages) {
-            slot4[i] = (long long)id * p.page + off;
-          } else {
-            atomicCAS(&g_paged_status, 0, kBadPageSite);
-          }
-        }
-      }
-      if (from == g && to == g + kRowsPerThread) {
-        *reinterpret_cast<int4*>(p.positions + g) = make_int4(pos4[0], pos4[1], pos4[2], pos4[3]);
-        longlong2* d = reinterpret_cast<longlong2*>(p.slots + g);
-        d[0] = make_longlong2(slot4[0], slot4[1]);
-        d[1] = make_longlong2(slot4[2], slot4[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-          if (g + i < from || g + i >= to) continue;
-          p.positions[g + i] = pos4[i];
-          p.slots[g + i] = slot4[i];
-        }
+        if (g + i >= r1) continue;
+        p.positions[g + i] = pos4[i];
+        p.slots[g + i] = slot4[i];
       }
     }
   }
 
-  // rows behind the last sequence
-  for (long long row = max(r0, carry.rows) + tid; row < r1; row += kStepThreads) {
-    p.positions[row] = -1;
-    p.slots[row] = -1;
+  // ---- new table entries
+  const int taken = min(all.pages, have);
+  for (int i = blockIdx.x * THREADS + tid; i < taken; i += gridDim.x * THREADS) {
+    const int e = find_entry(s_page, entries, i);
+    int b = e * size;
+    int at = s_page[e];
+    q.load(p, b);
+    while (i >= at + q.grow) {
+      at += q.grow;
+      q.load(p, ++b);
+    }
+    p.table[(long long)b * p.width + q.held + (i - at)] = p.free_pages[first + i];
+  }
+
+  // ---- per sequence
+  for (int b = blockIdx.x * THREADS + tid; b < p.batch; b += gridDim.x * THREADS) {
+    const int e = b / size;
+    long long rows = s_row[e];
+    int pages = s_page[e];
+    for (int x = e * size; x < b; ++x) {
+      q.load(p, x);
+      rows += q.fresh;
+      pages += q.grow;
+    }
+    q.load(p, b);
+    const int owned = q.held + q.got(have, pages);
+    p.held_out[b] = owned;
+    p.lens_out[b] = (int)min((long long)q.total, (long long)owned * p.page);
+    p.row_start[b] = sat32(rows);
   }
   if (blockIdx.x == 0 && tid == 0) {
-    p.row_start[p.batch] = sat32(carry.rows);
-    const int taken = (int)min(carry.pages, (long long)have);
+    p.row_start[p.batch] = sat32(all.rows);
     p.span_out[0] = first + taken;
     p.span_out[1] = end;
-    p.missing[0] = sat32(carry.pages - taken);
+    p.missing[0] = all.pages - taken;
   }
 }
 
@@ -651,10 +691,18 @@ extern "C" mla_status_t mla_page_step(
   p.num_pages = num_pages;
   p.free_capacity = free_capacity;
   p.max_rows = max_rows;
-  // one pass of every thread over its rows, or two CTAs per SM with longer walks
-  const int64_t per_pass = kStepThreads * kRowsPerThread;
+  p.div = PageDiv(page_size);
+  p.capacity = (int)((int64_t)max_pages_per_seq * page_size > INT_MAX
+                         ? INT_MAX
+                         : (int64_t)max_pages_per_seq * page_size);
+  // A small batch takes 256 threads, whose barriers are cheap (32 sequences: 4.2
+  // us in a graph, 6.4 with 1024), a larger one 1024, so that fewer CTAs make
+  // the sums of all sequences (4096: 12 us, 26 with 256).
+  const int threads = batch <= 256 ? 256 : 1024;
+  const int64_t per_pass = (int64_t)threads * kRowsPerThread;
   int64_t ctas = ((int64_t)max_rows + per_pass - 1) / per_pass;
-  const int64_t most = 2 * (int64_t)device_sm_count();
+  if (ctas < batch / threads) ctas = batch / threads;
+  const int64_t most = (int64_t)device_sm_count() * (1024 / threads);
   if (ctas > most) ctas = most;
   if (ctas < 1) ctas = 1;
   const int64_t share = ((int64_t)max_rows + ctas - 1) / ctas;
@@ -662,7 +710,8 @@ extern "C" mla_status_t mla_page_step(
   const cudaStream_t s = (cudaStream_t)stream;
   {
     KernelTimer kt("page_step", s);
-    page_step_kernel<<<(unsigned)ctas, kStepThreads, 0, s>>>(p);
+    if (threads == 256) page_step_kernel<256><<<(unsigned)ctas, 256, 0, s>>>(p);
+    else page_step_kernel<1024><<<(unsigned)ctas, 1024, 0, s>>>(p);
   }
   return launched(cudaGetLastError());
 }

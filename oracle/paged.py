@@ -30,7 +30,7 @@ def page_step(kept, new, held, table, free_pages, span, page, num_pages, max_row
     for b in range(B):
         k, n = max(int(kept[b]), 0), max(int(new[b]), 0)
         h = min(max(int(held[b]), 0), W)
-        total = min(k + n, W * page)
+        total = min(k + n, W * page, 2 ** 31 - 1)
         grow = max(0, math.ceil(total / page) - h)
         got = free[taken:taken + grow]
         taken += len(got)
