@@ -299,19 +299,6 @@ struct Vec {
   float v[N];
 };
 
-__device__ __forceinline__ void load_vec(const float* p, Vec<float>& x) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  x.v[0] = a.x; x.v[1] = a.y; x.v[2] = a.z; x.v[3] = a.w;
-}
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, Vec<__nv_bfloat16>& x) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x.v[2 * i] = __uint_as_float(w[i] << 16);
-    x.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
 __device__ __forceinline__ void store_vec(float* p, const Vec<float>& x) {
   *reinterpret_cast<float4*>(p) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
 }
@@ -336,6 +323,24 @@ __device__ __forceinline__ void store_vec(__nv_fp8_e4m3* p, const Vec<__nv_bfloa
     w[i] = lo | (hi << 16);
   }
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ uint4 load_raw(const void* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void unpack(const uint4& r, Vec<float>& x) {
+  x.v[0] = __uint_as_float(r.x);
+  x.v[1] = __uint_as_float(r.y);
+  x.v[2] = __uint_as_float(r.z);
+  x.v[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack(const uint4& r, Vec<__nv_bfloat16>& x) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.v[2 * i] = __uint_as_float(w[i] << 16);
+    x.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
 }
 
 // The cosines and sines of one item: Vec::N angles.
@@ -401,57 +406,70 @@ struct AppendKVParams {
   const float *k_scale, *v_scale;
   int page, table_rows, rope, interleaved;
   int q_heads, kv_heads, dim;  // q_heads 0: the cache only
-  int items, turned, heads_per_cta;
+  int items, turned;
+  PageDiv div;
 };
 
-template <typename T, typename CT>
-__global__ void __launch_bounds__(256) append_kv_kernel(AppendKVParams p) {
+template <typename T, typename CT, int K>
+__global__ void __launch_bounds__(256) append_kv_kernel(const AppendKVParams p) {
   constexpr int N = Vec<T>::N;
   const long long row = blockIdx.x;
   const int pos = p.positions[row];
-  if (pos < 0 || (p.rope > 0 && pos >= p.table_rows)) return;
   const int64_t slot = p.slots[row];
-  const bool cached = slot >= 0 && slot < p.cache_rows;
-  int64_t at = 0;
-  if (cached) {
-    const int64_t pg = (slot >> 32) == 0 ? (int64_t)((uint32_t)slot / (uint32_t)p.page)
-                                         : slot / p.page;
-    at = pg * p.page_stride + (slot - pg * p.page) * p.row_stride;
-  }
   const int item = threadIdx.x;
   int v0, v1;
   item_vectors(item, p.turned, 0, 2 * p.turned, p.dim / N - 2 * p.turned, p.interleaved != 0, v0,
                v1);
+  const int heads = p.q_heads + 2 * p.kv_heads;
+  const int h0 = blockIdx.y * (K * blockDim.y) + threadIdx.y;
+  uint4 xr[K], yr[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int h = h0 + i * blockDim.y;
+    xr[i] = yr[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (h >= heads) continue;
+    const int hk = h - p.q_heads;
+    const T* src = hk < 0             ? (const T*)p.q + row * p.q_stride + (int64_t)h * p.dim
+                   : hk < p.kv_heads ? (const T*)p.k + row * p.k_stride + (int64_t)hk * p.dim
+                                     : (const T*)p.v + row * p.v_stride +
+                                           (int64_t)(hk - p.kv_heads) * p.dim;
+    xr[i] = load_raw(src + v0 * N);
+    if (v1 >= 0) yr[i] = load_raw(src + v1 * N);
+  }
+  if (pos < 0 || (p.rope > 0 && pos >= p.table_rows)) return;
+  const bool cached = slot >= 0 && slot < p.cache_rows;
+  int64_t at = 0;
+  if (cached) {
+    const int64_t pg = (slot >> 31) == 0 ? (int64_t)p.div((int)slot) : slot / p.page;
+    at = pg * p.page_stride + (slot - pg * p.page) * p.row_stride;
+  }
   Angles<T> ang;
   if (item < p.turned) ang.load(p.cos_sin, pos, p.rope, item);
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  const int h1 = min(heads, (int)(blockIdx.y + 1) * p.heads_per_cta);
-#pragma unroll 2
-  for (int h = blockIdx.y * p.heads_per_cta + threadIdx.y; h < h1; h += blockDim.y) {
-    const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
-    const int hk = is_q ? 0 : is_k ? h - p.q_heads : h - p.q_heads - p.kv_heads;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int h = h0 + i * blockDim.y;
+    if (h >= heads) continue;
+    const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
     if (!is_q && !cached) continue;
-    const T* src = is_q ? (const T*)p.q + row * p.q_stride + (int64_t)h * p.dim
-                 : is_k ? (const T*)p.k + row * p.k_stride + (int64_t)hk * p.dim
-                        : (const T*)p.v + row * p.v_stride + (int64_t)hk * p.dim;
     Vec<T> x, y;
-    load_vec(src + v0 * N, x);
-    if (v1 >= 0) load_vec(src + v1 * N, y);
-    if (item < p.turned && (is_q || is_k)) ang.turn(x, y, p.interleaved != 0);
+    unpack(xr[i], x);
+    unpack(yr[i], y);
+    if (item < p.turned && !is_v) ang.turn(x, y, p.interleaved != 0);
     if (is_q) {
       T* dst = (T*)p.q_out + (row * p.q_heads + h) * p.dim;
       store_vec(dst + v0 * N, x);
       if (v1 >= 0) store_vec(dst + v1 * N, y);
     } else {
-      CT* dst = (CT*)(is_k ? p.k_cache : p.v_cache) + at + hk * p.head_stride;
+      const int hk = h - p.q_heads - (is_v ? p.kv_heads : 0);
+      CT* dst = (CT*)(is_v ? p.v_cache : p.k_cache) + at + hk * p.head_stride;
       if constexpr (sizeof(CT) == 1) {
-        const float* sc = is_k ? p.k_scale : p.v_scale;
+        const float* sc = is_v ? p.v_scale : p.k_scale;
         if (sc) {
           const float s = sc[hk];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            x.v[i] = __fdiv_rn(x.v[i], s);
-            if (v1 >= 0) y.v[i] = __fdiv_rn(y.v[i], s);
+          for (int e = 0; e < N; ++e) {
+            x.v[e] = __fdiv_rn(x.v[e], s);
+            y.v[e] = __fdiv_rn(y.v[e], s);
           }
         }
       }
@@ -472,100 +490,125 @@ struct AppendLatentParams {
   int64_t ckv_stride, kr_stride, cache_rows;
   int table_rows, interleaved;
   int heads, rank, nope, rope;
-  int items, turned, heads_per_cta;
+  int items, turned;
+  int rows, kv_ctas, head_ctas;  // head_ctas of one row
 };
 
-// CTAs (row, 0): the row's latent, normed, and its key, rotated, into the
-// cache.  CTAs (row, y > 0): a run of the row's query heads.
-template <typename T>
-__global__ void __launch_bounds__(256) append_latent_kernel(AppendLatentParams p) {
+// The first CTAs take the rows' latents and keys, a warp a row, so that the
+// sum of squares needs no barrier (with a CTA a row these, mostly waiting,
+// held half of the machine's places: 8191 rows took 62 us, now 47); the others
+// a run of one row's query heads each.
+template <typename T, int K>
+__global__ void __launch_bounds__(256) append_latent_kernel(const AppendLatentParams p) {
   constexpr int N = Vec<T>::N;
-  const long long row = blockIdx.x;
-  const int pos = p.positions[row];
-  if (pos < 0 || pos >= p.table_rows) return;
-  if (blockIdx.y > 0) {
+  if ((int)blockIdx.x >= p.kv_ctas) {
+    const int cta = blockIdx.x - p.kv_ctas, run = cta % p.head_ctas;
+    const long long row = cta / p.head_ctas;
+    const int pos = p.positions[row];
     const int item = threadIdx.x;
     int v0, v1;
     item_vectors(item, p.turned, p.nope / N, 0, p.nope / N, p.interleaved != 0, v0, v1);
+    const int h0 = run * (K * blockDim.y) + threadIdx.y;
+    uint4 xr[K], yr[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int h = h0 + i * blockDim.y;
+      xr[i] = yr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (h >= p.heads) continue;
+      const T* src = (const T*)p.q + row * p.q_stride + (int64_t)h * (p.nope + p.rope);
+      xr[i] = load_raw(src + v0 * N);
+      if (v1 >= 0) yr[i] = load_raw(src + v1 * N);
+    }
+    if (pos < 0 || pos >= p.table_rows) return;
     Angles<T> ang;
     if (item < p.turned) ang.load(p.cos_sin, pos, p.rope, item);
-    const int h1 = min(p.heads, (int)blockIdx.y * p.heads_per_cta);
-#pragma unroll 2
-    for (int h = (blockIdx.y - 1) * p.heads_per_cta + threadIdx.y; h < h1; h += blockDim.y) {
-      const T* src = (const T*)p.q + row * p.q_stride + (int64_t)h * (p.nope + p.rope);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int h = h0 + i * blockDim.y;
+      if (h >= p.heads) continue;
       const int64_t head = row * p.heads + h;
-      Vec<T> x, y;
-      load_vec(src + v0 * N, x);
-      if (v1 >= 0) load_vec(src + v1 * N, y);
-      T* dst = (T*)p.q_nope + head * p.nope;
       if (item < p.turned) {
+        Vec<T> x, y;
+        unpack(xr[i], x);
+        unpack(yr[i], y);
         ang.turn(x, y, p.interleaved != 0);
-        dst = (T*)p.q_rope + head * p.rope - p.nope;
+        T* dst = (T*)p.q_rope + head * p.rope - p.nope;
+        store_vec(dst + v0 * N, x);
+        store_vec(dst + v1 * N, y);
+      } else {
+        T* dst = (T*)p.q_nope + head * p.nope;
+        *reinterpret_cast<uint4*>(dst + v0 * N) = xr[i];
+        if (v1 >= 0) *reinterpret_cast<uint4*>(dst + v1 * N) = yr[i];
       }
-      store_vec(dst + v0 * N, x);
-      if (v1 >= 0) store_vec(dst + v1 * N, y);
     }
     return;
   }
+
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int warps = (blockDim.x * blockDim.y) >> 5;  // (whole ones)
+  const long long row = (long long)blockIdx.x * warps + warp;
+  if (warp >= warps || row >= p.rows) return;
+  const int pos = p.positions[row];
   const int64_t slot = p.slots[row];
-  if (slot < 0 || slot >= p.cache_rows) return;
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x, nt = blockDim.x * blockDim.y;
   const T* src = (const T*)p.kv + row * p.kv_stride;
-  T* c = (T*)p.c_kv + slot * p.ckv_stride;
-  T* kr = (T*)p.k_rope + slot * p.kr_stride;
   const int nv = p.rank / N;
-  // rank <= 1024 is at most 256 vectors; a CTA has 64 threads or more
-  constexpr int kMost = 4;
-  Vec<T> x[kMost];
-  float sum = 0.f;
+  // rank <= 1024 is at most 256 vectors, rope <= 128 at most 16 rotated items
+  constexpr int kMost = 256 / 32 * (int)sizeof(T) / 4;
+  uint4 x[kMost], w[kMost], ra, rb;
+  int v0 = 0, v1 = 0;
 #pragma unroll
   for (int m = 0; m < kMost; ++m) {
-    const int i = tid + m * nt;
-    if (i >= nv) break;
-    load_vec(src + i * N, x[m]);
-#pragma unroll
-    for (int e = 0; e < N; ++e) sum = fmaf(x[m].v[e], x[m].v[e], sum);
+    const int i = lane + m * 32;
+    x[m] = w[m] = make_uint4(0u, 0u, 0u, 0u);
+    if (i >= nv) continue;
+    x[m] = load_raw(src + i * N);
+    if (p.weight) w[m] = load_raw((const T*)p.weight + i * N);
   }
-  float scale = 1.f;
-  if (p.weight) {
-    __shared__ float part[8];
-    // the last warp may be partial: only its live lanes take part
-    const int left = nt - (tid & ~31);
-    const unsigned mask = left >= 32 ? ~0u : (1u << left) - 1u;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float other = __shfl_down_sync(mask, sum, o);
-      if ((tid & 31) + o < left) sum += other;
-    }
-    if ((tid & 31) == 0) part[tid >> 5] = sum;
-    __syncthreads();
-    float all = 0.f;
-    for (int w = 0; w < (nt + 31) / 32; ++w) all += part[w];
-    scale = __frsqrt_rn(all / p.rank + p.eps);
+  if (lane < p.turned) {
+    item_vectors(lane, p.turned, nv, 0, 0, p.interleaved != 0, v0, v1);
+    ra = load_raw(src + v0 * N);
+    rb = load_raw(src + v1 * N);
   }
-#pragma unroll
-  for (int m = 0; m < kMost; ++m) {
-    const int i = tid + m * nt;
-    if (i >= nv) break;
-    if (p.weight) {
-      Vec<T> w;
-      load_vec((const T*)p.weight + i * N, w);
-#pragma unroll
-      for (int e = 0; e < N; ++e) x[m].v[e] = x[m].v[e] * scale * w.v[e];
-    }
-    store_vec(c + i * N, x[m]);
-  }
-  for (int i = nt - 1 - tid; i < p.turned; i += nt) {
-    int v0, v1;
-    item_vectors(i, p.turned, nv, 0, 0, p.interleaved != 0, v0, v1);
+  if (pos < 0 || pos >= p.table_rows || slot < 0 || slot >= p.cache_rows) return;
+  T* c = (T*)p.c_kv + slot * p.ckv_stride;
+  if (lane < p.turned) {
+    T* kr = (T*)p.k_rope + slot * p.kr_stride;
     Angles<T> ang;
-    ang.load(p.cos_sin, pos, p.rope, i);
+    ang.load(p.cos_sin, pos, p.rope, lane);
     Vec<T> a, b;
-    load_vec(src + v0 * N, a);
-    load_vec(src + v1 * N, b);
+    unpack(ra, a);
+    unpack(rb, b);
     ang.turn(a, b, p.interleaved != 0);
     store_vec(kr + (v0 - nv) * N, a);
     store_vec(kr + (v1 - nv) * N, b);
+  }
+  __syncwarp();
+  if (p.weight == nullptr) {
+#pragma unroll
+    for (int m = 0; m < kMost; ++m)
+      if (lane + m * 32 < nv) *reinterpret_cast<uint4*>(c + (lane + m * 32) * N) = x[m];
+    return;
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int m = 0; m < kMost; ++m) {
+    Vec<T> a;
+    unpack(x[m], a);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum = fmaf(a.v[e], a.v[e], sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  const float scale = __frsqrt_rn(sum / p.rank + p.eps);
+#pragma unroll
+  for (int m = 0; m < kMost; ++m) {
+    if (lane + m * 32 >= nv) continue;
+    Vec<T> a, b;
+    unpack(x[m], a);
+    unpack(w[m], b);
+#pragma unroll
+    for (int e = 0; e < N; ++e) a.v[e] = a.v[e] * scale * b.v[e];
+    store_vec(c + (lane + m * 32) * N, a);
   }
 }
 
@@ -609,14 +652,28 @@ bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi
 // Threads of an append: blockDim.x items of a head, blockDim.y heads.
 dim3 item_block(int items) { return dim3((unsigned)items, (unsigned)(128 / items < 1 ? 1 : 128 / items)); }
 
-// Heads per CTA: one head per thread when the rows are few (the more CTAs the
-// better), up to four, which share one load of the cosines, when there are
-// enough rows to fill the machine anyway.
-int heads_per_cta(int heads, int by, int rows) {
+// Heads a thread takes: one when the rows are few (the more CTAs the better),
+// up to four, which share one load of the cosines and are on their way
+// together, when there are enough rows to fill the machine anyway.
+int heads_per_thread(int heads, int by, int rows) {
   const int64_t fill = (int64_t)device_sm_count() * 16;
   int k = 1;
   while (k < 4 && (int64_t)rows * ((heads + 2 * k * by - 1) / (2 * k * by)) >= fill) k *= 2;
-  return k * by;
+  return k;
+}
+
+template <typename T>
+void launch_latent(int k, dim3 grid, dim3 block, cudaStream_t s, const AppendLatentParams& p) {
+  if (k == 4) append_latent_kernel<T, 4><<<grid, block, 0, s>>>(p);
+  else if (k == 2) append_latent_kernel<T, 2><<<grid, block, 0, s>>>(p);
+  else append_latent_kernel<T, 1><<<grid, block, 0, s>>>(p);
+}
+
+template <typename T, typename CT>
+void launch_kv(int k, dim3 grid, dim3 block, cudaStream_t s, const AppendKVParams& p) {
+  if (k == 4) append_kv_kernel<T, CT, 4><<<grid, block, 0, s>>>(p);
+  else if (k == 2) append_kv_kernel<T, CT, 2><<<grid, block, 0, s>>>(p);
+  else append_kv_kernel<T, CT, 1><<<grid, block, 0, s>>>(p);
 }
 
 }  // namespace
@@ -785,18 +842,22 @@ extern "C" mla_status_t mla_append_latent(
   p.turned = d / 2 / N;
   p.items = p.turned + (n / N + 1) / 2;
   const dim3 block = item_block(p.items);
-  p.heads_per_cta = heads_per_cta(H, (int)block.y, rows);
-  const unsigned head_ctas = no_q ? 0u : (unsigned)((H + p.heads_per_cta - 1) / p.heads_per_cta);
-  const dim3 grid((unsigned)rows, 1 + head_ctas);
-  if (grid.y > 65535u) {
-    set_error("append latent: %d heads are too many", H);
+  const int k = heads_per_thread(H, (int)block.y, rows), hpc = k * (int)block.y;
+  const int warps = (int)(block.x * block.y) / 32;
+  p.rows = rows;
+  p.kv_ctas = (rows + warps - 1) / warps;
+  p.head_ctas = (H + hpc - 1) / hpc;
+  const int64_t ctas = p.kv_ctas + (no_q ? 0 : (int64_t)rows * p.head_ctas);
+  if (ctas > INT_MAX) {
+    set_error("append latent: %d rows of %d heads are too many for one call", rows, H);
     return MLA_ERR_UNSUPPORTED;
   }
+  const dim3 grid((unsigned)ctas);
   const cudaStream_t s = (cudaStream_t)stream;
   {
     KernelTimer kt("append_latent", s);
-    if (eb == 2) append_latent_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(p);
-    else append_latent_kernel<float><<<grid, block, 0, s>>>(p);
+    if (eb == 2) launch_latent<__nv_bfloat16>(k, grid, block, s, p);
+    else launch_latent<float>(k, grid, block, s, p);
   }
   return launched(cudaGetLastError());
 }
@@ -881,8 +942,9 @@ extern "C" mla_status_t mla_append_kv(
   p.items = p.turned + ((D / N - 2 * p.turned) + 1) / 2;
   const int heads = p.q_heads + 2 * Hk;
   const dim3 block = item_block(p.items);
-  p.heads_per_cta = heads_per_cta(heads, (int)block.y, rows);
-  const dim3 grid((unsigned)rows, (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
+  p.div = PageDiv(cache->page_size);
+  const int kk = heads_per_thread(heads, (int)block.y, rows), hpc = kk * (int)block.y;
+  const dim3 grid((unsigned)rows, (unsigned)((heads + hpc - 1) / hpc));
   if (grid.y > 65535u) {
     set_error("append kv: %d heads are too many", heads);
     return MLA_ERR_UNSUPPORTED;
@@ -891,11 +953,11 @@ extern "C" mla_status_t mla_append_kv(
   {
     KernelTimer kt("append_kv", s);
     if (eb == 4)
-      append_kv_kernel<float, float><<<grid, block, 0, s>>>(p);
+      launch_kv<float, float>(kk, grid, block, s, p);
     else if (g->cache_dtype == MLA_DTYPE_E4M3)
-      append_kv_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, block, 0, s>>>(p);
+      launch_kv<__nv_bfloat16, __nv_fp8_e4m3>(kk, grid, block, s, p);
     else
-      append_kv_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, block, 0, s>>>(p);
+      launch_kv<__nv_bfloat16, __nv_bfloat16>(kk, grid, block, s, p);
   }
   return launched(cudaGetLastError());
 }
