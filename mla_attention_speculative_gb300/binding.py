@@ -616,6 +616,7 @@ class _PreparedCall:
         self._args = [types[i](a) if isinstance(a, (int, float)) else a
                       for i, a in enumerate(args)]
         self._dev = dev.index if dev.index is not None else torch.cuda.current_device()
+        self._one_device = torch.cuda.device_count() == 1   # then it is the current one
         self._keep = keep
         self._made = [t for t in made if t is not None]
         self._home = _current_stream(torch.device("cuda", self._dev))
@@ -633,11 +634,11 @@ class _PreparedCall:
             for t in self._made:
                 t.record_stream(s)
             self._streams.add(stream)
-        if torch.cuda.current_device() != self._dev:
+        if self._one_device or torch.cuda.current_device() == self._dev:
+            st = self._fn(*self._args, stream)
+        else:
             with torch.cuda.device(self._dev):
                 st = self._fn(*self._args, stream)
-        else:
-            st = self._fn(*self._args, stream)
         if st != MLA_OK:
             _check(st, self._name)
 

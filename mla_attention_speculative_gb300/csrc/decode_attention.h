@@ -30,34 +30,40 @@ struct Shape {
   static constexpr int CB = KIND == kBf16 ? 2 : KIND == kE4m3 ? 1 : 4;  // bytes of an element
   static constexpr int ROWB = DP * CB;                                  // bytes of a tile row
   static constexpr int CH = ROWB / 16;                                  // its 16-byte chunks
-  // warps of a CTA, each with its own ring of tiles
-  static constexpr int NW = 4;
+  // warps of a CTA, each with its own ring of tiles: four, more for the wide
+  // heads whose CTA has an SM to itself and is short of warps, not of bytes on
+  // their way (16 sequences of 4000 to 16000, 256 wide: fp32 511 us against
+  // 622, bf16 with groups of 16 304 against 393)
+  static constexpr bool WIDE = DP >= 192 && (KIND == kFp32 || (KIND == kBf16 && NT == 2));
+  static constexpr int NW = !WIDE ? 4 : DP == 192 ? 8 : 6;
   static constexpr int THREADS = NW * 32;
-  // positions of a warp's tile: its K and V are about 8 KB
-  static constexpr int WP = KIND == kFp32 ? 8 : ROWB >= 192 ? 16 : 32;
+  // positions of a warp's tile: its K and V are 4 to 16 KB
+  static constexpr int WP = KIND == kFp32 ? (DP <= 64 ? 16 : 8) : ROWB >= 192 ? 16 : 32;
   static constexpr int TILE = NW * WP;  // positions of a CTA's tile
   static constexpr int ROWS = KIND == kFp32 ? 4 * NT : 8 * NT;  // query heads of a row tile
   static constexpr int STAGE = 2 * WP * ROWB;  // K, then V
   // Three CTAs per SM with rings of two tiles per warp where the registers of
-  // 168 a thread suffice (up to 128 elements, one row multiple): the third
-  // CTA's warps cover more latency than a third tile in each ring would (bf16,
-  // 32 sequences: 327 us against 340; e4m3, 64 sequences: 170 against 181).
-  // Else two CTAs, or one with the whole shared memory for wide heads.
-  static constexpr int OCC = KIND != kFp32 && DP <= 128 && NT == 1 ? 3
-                             : 98304 / (NW * STAGE) >= 3           ? 2
-                                                                   : 1;
+  // 168 a thread suffice (up to 128 elements; beside 16-bit products one row
+  // multiple): the third CTA's warps cover more latency than a third tile in
+  // each ring would (bf16, 32 sequences of up to 32768: 327 us against 340;
+  // e4m3, 64 sequences: 170 against 181; fp32, 16 sequences, groups of 8: 322
+  // against 383).  Else two CTAs, or one with the whole shared memory.
+  static constexpr int OCC = WIDE                                              ? 1
+                             : DP <= 128 && (NT == 1 || KIND == kFp32)         ? 3
+                             : 98304 / (NW * STAGE) >= 3                       ? 2
+                                                                               : 1;
   static constexpr int FIT = 196608 / OCC / (NW * STAGE);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int RING = NW * STAGES * STAGE;
   static constexpr int MSTRIDE = 36;  // floats of a merge row: 32 columns, padded
   // two buffers, so that a round of the merge needs one barrier, where they fit
-  static constexpr int MBUFS = NW * ROWS <= 32 ? 2 : 1;
+  static constexpr int MBUFS = NW * ROWS <= 32 && KIND != kFp32 ? 2 : 1;
   static constexpr int MBUF = NW * ROWS * MSTRIDE;  // floats of one
   static constexpr int MERGE = MBUFS * MBUF * 4;
   static constexpr int STATS = NW * ROWS * 8;
   // fp32: the row tile's queries, and each warp's weights
   static constexpr int QTILE = KIND == kFp32 ? ROWS * DP * 4 : 0;
-  static constexpr int WEIGHTS = KIND == kFp32 ? NW * WP * ROWS * 4 : 0;
+  static constexpr int WEIGHTS = KIND == kFp32 ? NW * 8 * ROWS * 4 : 0;
   static constexpr int SMEM = RING + MERGE + STATS + QTILE + WEIGHTS;
   static_assert(STAGES >= 2, "a warp's ring needs two tiles");
   // 228 KB of an SM, 1 KB of which each CTA costs besides (and a little static)
@@ -95,7 +101,7 @@ struct Kernel {
   int smem, threads, occupancy, tile, rows, dp;
 };
 
-// The kernel for padded width dp (64, 128, 192, 256) and row multiple nt (1, 2).
+// The kernel for a head width and row multiple nt (1, 2).
 Kernel kernel_bf16(int dp, int nt);
 Kernel kernel_e4m3(int dp, int nt);
 Kernel kernel_fp32(int dp, int nt);

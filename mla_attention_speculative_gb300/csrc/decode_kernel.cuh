@@ -124,6 +124,13 @@ __device__ __forceinline__ void zero_idle(const Params& p) {
   }
 }
 
+// A chunk's place in its row: XORed so that the same chunk of eight successive
+// rows lies in eight different 16-byte columns of the banks, whatever CH mod 8.
+template <int CH>
+__device__ __forceinline__ int swizzle(int row) {
+  return CH % 8 == 0 ? (row & 7) : CH % 4 == 0 ? ((row >> 1) & 3) : ((row >> 2) & 1);
+}
+
 // Where a lane's row of a tile lies: the page id is loaded, not yet used.
 struct RowAt {
   int64_t off;  // within the page, -1: beyond the sequence
@@ -311,8 +318,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
       const int idx = lane + 32 * i, row = idx / CH, c = idx % CH;
       const int64_t src = __shfl_sync(~0u, at, row);
       if (c < chunks) {
-        const int x = CH % 8 == 0 ? (row & 7) : ((row >> 1) & 3);
-        const uint32_t dst = base + row * S::ROWB + ((c ^ x) << 4);
+        const uint32_t dst = base + row * S::ROWB + ((c ^ swizzle<CH>(row)) << 4);
         const int64_t off = src < 0 ? 0 : src * S::CB + c * 16;
         const uint32_t bytes = src < 0 ? 0u : 16u;
         cp_async16(dst, (const char*)p.k + off, bytes);
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
             for (int e = 0; e < 4; ++e) s[u][nt][e] = s2[u][nt][e] = 0.f;
         const int r8 = lane & 7, mi = lane >> 3;
         const int row_k = r8 + (mi & 1) * 8;  // matrices: rows 0-7, 8-15, then the next chunk
-        const int swz_k = CH % 8 == 0 ? (row_k & 7) : ((row_k >> 1) & 3);
+        const int swz_k = swizzle<CH>(row_k);
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
           const uint32_t at = kb + (u * 16 + row_k) * S::ROWB;
@@ -539,7 +545,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
           if constexpr (KIND == kBf16) {
             // matrices: chunk 2 mt and 2 mt + 1 of rows 0-7, then of rows 8-15
             const int row_v = r8 + (mi >> 1) * 8;
-            const int swz_v = CH % 8 == 0 ? (row_v & 7) : ((row_v >> 1) & 3);
+            const int swz_v = swizzle<CH>(row_v);
             const uint32_t at = vb + (u * 16 + row_v) * S::ROWB;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -573,71 +579,76 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
           }
         }
       } else {
-        // lane: position lane % 8, every fourth chunk from lane / 8
+        // eight positions at a time; lane: position lane % 8, every fourth chunk from lane / 8
         const int row = lane & 7, part = lane >> 3;
-        const char* kp = smem + (kb - smem_u32(smem)) + row * S::ROWB;
-        float s[ROWS];
+        float* ws = s_w + warp * 8 * ROWS;
+#pragma unroll 1
+        for (int u = 0; u < WP && pos0 + u < cc.s.T; u += 8) {
+          const char* kp = smem + (kb - smem_u32(smem)) + (u + row) * S::ROWB;
+          float s[ROWS];
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) s[r] = 0.f;
+          for (int r = 0; r < ROWS; ++r) s[r] = 0.f;
 #pragma unroll 4
-        for (int c = part; c < chunks; c += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(kp + ((c ^ row) << 4));
+          for (int c = part; c < chunks; c += 4) {
+            const float4 x =
+                *reinterpret_cast<const float4*>(kp + ((c ^ swizzle<CH>(row)) << 4));
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+              const float4 q = *reinterpret_cast<const float4*>(s_q + r * DP + c * 4);
+              s[r] = fmaf(x.x, q.x, fmaf(x.y, q.y, fmaf(x.z, q.z, fmaf(x.w, q.w, s[r]))));
+            }
+          }
 #pragma unroll
           for (int r = 0; r < ROWS; ++r) {
-            const float4 q = *reinterpret_cast<const float4*>(s_q + r * DP + c * 4);
-            s[r] = fmaf(x.x, q.x, fmaf(x.y, q.y, fmaf(x.z, q.z, fmaf(x.w, q.w, s[r]))));
+            s[r] += __shfl_xor_sync(~0u, s[r], 8);
+            s[r] += __shfl_xor_sync(~0u, s[r], 16);
+            s[r] = pos0 + u + row < cc.s.T ? s[r] * sc[0] : -INFINITY;
+            float top = fmaxf(m[r], s[r]);
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+            const float base = top == -INFINITY ? 0.f : top;
+            if (__any_sync(~0u, top > m[r])) {
+              const float f = ex2(m[r] - base);
+              l[r] *= f;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) of[nb][r][e] *= f;
+            }
+            m[r] = top;
+            s[r] = ex2(s[r] - base);
+            l[r] += s[r];
+            if (r / (ROWS / 4) == part) ws[row * ROWS + r] = s[r];
           }
-        }
-        float* ws = s_w + warp * WP * ROWS;
+          __syncwarp();
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          s[r] += __shfl_xor_sync(~0u, s[r], 8);
-          s[r] += __shfl_xor_sync(~0u, s[r], 16);
-          s[r] = pos0 + row < cc.s.T ? s[r] * sc[0] : -INFINITY;
-          float top = fmaxf(m[r], s[r]);
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
-          const float base = top == -INFINITY ? 0.f : top;
-          if (__any_sync(~0u, top > m[r])) {
-            const float f = ex2(m[r] - base);
-            l[r] *= f;
+          for (int t = 0; t < 8; ++t) {
+            float w[ROWS];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int r = 0; r < ROWS; r += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(ws + t * ROWS + r);
+              w[r] = x.x; w[r + 1] = x.y; w[r + 2] = x.z; w[r + 3] = x.w;
+            }
+            const char* vp = smem + (vb - smem_u32(smem)) + (u + t) * S::ROWB;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) of[nb][r][e] *= f;
-          }
-          m[r] = top;
-          s[r] = ex2(s[r] - base);
-          l[r] += s[r];
-          if (r / (ROWS / 4) == part) ws[row * ROWS + r] = s[r];
-        }
-        __syncwarp();
+            for (int nb = 0; nb < NB; ++nb) {
+              const int c = nb * 32 + lane;
+              if (c < chunks) {
+                const float4 x =
+                    *reinterpret_cast<const float4*>(vp + ((c ^ swizzle<CH>(t)) << 4));
 #pragma unroll
-        for (int t8 = 0; t8 < WP; ++t8) {
-          float w[ROWS];
-#pragma unroll
-          for (int r = 0; r < ROWS; r += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(ws + t8 * ROWS + r);
-            w[r] = x.x; w[r + 1] = x.y; w[r + 2] = x.z; w[r + 3] = x.w;
-          }
-          const char* vp = smem + (vb - smem_u32(smem)) + t8 * S::ROWB;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const int c = nb * 32 + lane;
-            if (c < chunks) {
-              const float4 x = *reinterpret_cast<const float4*>(vp + ((c ^ (t8 & 7)) << 4));
-#pragma unroll
-              for (int r = 0; r < ROWS; ++r) {
-                of[nb][r][0] = fmaf(w[r], x.x, of[nb][r][0]);
-                of[nb][r][1] = fmaf(w[r], x.y, of[nb][r][1]);
-                of[nb][r][2] = fmaf(w[r], x.z, of[nb][r][2]);
-                of[nb][r][3] = fmaf(w[r], x.w, of[nb][r][3]);
+                for (int r = 0; r < ROWS; ++r) {
+                  of[nb][r][0] = fmaf(w[r], x.x, of[nb][r][0]);
+                  of[nb][r][1] = fmaf(w[r], x.y, of[nb][r][1]);
+                  of[nb][r][2] = fmaf(w[r], x.z, of[nb][r][2]);
+                  of[nb][r][3] = fmaf(w[r], x.w, of[nb][r][3]);
+                }
               }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
 
@@ -773,17 +784,18 @@ Kernel kernel_of() {
   return {decode_attn_sm103<DP, KIND, NT>, S::SMEM, S::THREADS, S::OCC, S::TILE, S::ROWS, DP};
 }
 
+template <int KIND, int NT>
+Kernel kernel_for(int dim) {
+  return dim <= 64    ? kernel_of<64, KIND, NT>()
+         : dim <= 96  ? kernel_of<96, KIND, NT>()
+         : dim <= 128 ? kernel_of<128, KIND, NT>()
+         : dim <= 192 ? kernel_of<192, KIND, NT>()
+                      : kernel_of<256, KIND, NT>();
+}
+
 template <int KIND>
-Kernel kernel_for(int dp, int nt) {
-  if (nt == 1)
-    return dp <= 64    ? kernel_of<64, KIND, 1>()
-           : dp <= 128 ? kernel_of<128, KIND, 1>()
-           : dp <= 192 ? kernel_of<192, KIND, 1>()
-                       : kernel_of<256, KIND, 1>();
-  return dp <= 64    ? kernel_of<64, KIND, 2>()
-         : dp <= 128 ? kernel_of<128, KIND, 2>()
-         : dp <= 192 ? kernel_of<192, KIND, 2>()
-                     : kernel_of<256, KIND, 2>();
+Kernel kernel_for(int dim, int nt) {
+  return nt == 1 ? kernel_for<KIND, 1>(dim) : kernel_for<KIND, 2>(dim);
 }
 
 }  // namespace decode

@@ -656,7 +656,7 @@ dim3 item_block(int items) { return dim3((unsigned)items, (unsigned)(128 / items
 // up to four, which share one load of the cosines and are on their way
 // together, when there are enough rows to fill the machine anyway.
 int heads_per_thread(int heads, int by, int rows) {
-  const int64_t fill = (int64_t)device_sm_count() * 16;
+  const int64_t fill = (int64_t)device_sm_count() * 8;
   int k = 1;
   while (k < 4 && (int64_t)rows * ((heads + 2 * k * by - 1) / (2 * k * by)) >= fill) k *= 2;
   return k;
