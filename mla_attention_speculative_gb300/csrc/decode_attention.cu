@@ -115,6 +115,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float s_w[RPC][kMaxCtas], s_l[RPC][kMaxCtas];
   __shared__ float s_red[RPC][WPR];
   __shared__ float4 s_acc[kJoinThreads];
+  // (No later kernel is let in early from here.  The attention's equal shares
+  // need its CTAs spread evenly; started while this kernel still held parts of
+  // the SMs, a next call's ended up three on one SM and none on another, and 32
+  // sequences of up to 32768 positions took 452 us instead of 327.)
   sm103::pdl_wait();
   const int tid = threadIdx.x, r = tid / TPR, i0 = tid % TPR, row = blockIdx.y * RPC + r;
   const Record rec = p.rec[blockIdx.x];
@@ -281,37 +285,21 @@ cudaError_t allow_smem(const Kernel& k) {
 cudaError_t launch(const Plan& d, const Params& p, cudaStream_t stream) {
   cudaError_t e = allow_smem(d.k);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)d.ctas);
-  cfg.blockDim = dim3(d.k.threads);
-  cfg.dynamicSmemBytes = d.k.smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  // Equal shares need the CTAs spread evenly over the SMs.  Started while the
-  // kernel ahead still holds parts of them (as its dependent), they end up
-  // three on one SM and none on another: 452 us for 32 sequences of up to
-  // 32768 positions, against 327.  A call of single tiles has no such shares
-  // and saves 0.4 of its 4.2 us.
-  cfg.numAttrs = d.cut ? 0 : 1;
   {
     KernelTimer kt("decode_attn", stream);
-    e = cudaLaunchKernelEx(&cfg, d.k.fn, p);
+    e = launch_dependent(d.k.fn, dim3((unsigned)d.ctas), dim3(d.k.threads), d.k.smem, stream, p);
   }
   if (e != cudaSuccess || !d.cut) return e;
-  cfg.numAttrs = 1;
   const int rows = p.group < d.k.rows ? p.group : d.k.rows;
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = 0;
   KernelTimer kt("decode_join", stream);
-  if (d.by_segment) {
-    cfg.gridDim = dim3((unsigned)d.records, (unsigned)rows);
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<kJoinThreads>, p, d.k.rows, d.k.dp, d.kind);
-  }
-  cfg.gridDim = dim3((unsigned)d.records, (unsigned)((rows * 64 + kJoinThreads - 1) / kJoinThreads));
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<64>, p, d.k.rows, d.k.dp, d.kind);
+  if (d.by_segment)
+    return launch_dependent(decode_join_kernel<kJoinThreads>,
+                            dim3((unsigned)d.records, (unsigned)rows), dim3(kJoinThreads), 0,
+                            stream, p, d.k.rows, d.k.dp, d.kind);
+  return launch_dependent(
+      decode_join_kernel<64>,
+      dim3((unsigned)d.records, (unsigned)((rows * 64 + kJoinThreads - 1) / kJoinThreads)),
+      dim3(kJoinThreads), 0, stream, p, d.k.rows, d.k.dp, d.kind);
 }
 
 }  // namespace

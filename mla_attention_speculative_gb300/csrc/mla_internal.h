@@ -164,6 +164,25 @@ bool geometry_ok(const mla_geometry_t* g);
 mla_status_t kv_geometry_ok(const mla_kv_geometry_t* g);
 mla_status_t kv_cache_ok(const mla_kv_geometry_t* g, const mla_kv_cache_t* c);
 
+// Launches a kernel as a programmatic dependent of the one ahead in the stream:
+// its launch overlaps that kernel's end (about 2.5 us of a call).  The kernel
+// itself waits (sm103::pdl_wait) before it reads or writes anything.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Records a one-line failure description for mla_last_error().
 void set_error(const char* fmt, ...);
 

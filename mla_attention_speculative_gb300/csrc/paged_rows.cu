@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "mla_internal.h"
+#include "sm103_ptx.cuh"
 
 namespace mla {
 
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   __shared__ int s_row[kEntries], s_page[kEntries];
   __shared__ Sums s_warp[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  sm103::pdl_wait();
   const int span0 = p.free_span[0], span1 = p.free_span[1];
 
   // ---- the sums; `per` consecutive sequences a thread, `size` an entry
@@ -413,6 +415,7 @@ struct AppendKVParams {
 template <typename T, typename CT, int K>
 __global__ void __launch_bounds__(256) append_kv_kernel(const AppendKVParams p) {
   constexpr int N = Vec<T>::N;
+  sm103::pdl_wait();
   const long long row = blockIdx.x;
   const int pos = p.positions[row];
   const int64_t slot = p.slots[row];
@@ -501,6 +504,7 @@ struct AppendLatentParams {
 template <typename T, int K>
 __global__ void __launch_bounds__(256) append_latent_kernel(const AppendLatentParams p) {
   constexpr int N = Vec<T>::N;
+  sm103::pdl_wait();
   if ((int)blockIdx.x >= p.kv_ctas) {
     const int cta = blockIdx.x - p.kv_ctas, run = cta % p.head_ctas;
     const long long row = cta / p.head_ctas;
@@ -663,17 +667,20 @@ int heads_per_thread(int heads, int by, int rows) {
 }
 
 template <typename T>
-void launch_latent(int k, dim3 grid, dim3 block, cudaStream_t s, const AppendLatentParams& p) {
-  if (k == 4) append_latent_kernel<T, 4><<<grid, block, 0, s>>>(p);
-  else if (k == 2) append_latent_kernel<T, 2><<<grid, block, 0, s>>>(p);
-  else append_latent_kernel<T, 1><<<grid, block, 0, s>>>(p);
+cudaError_t launch_latent(int k, dim3 grid, dim3 block, cudaStream_t s,
+                          const AppendLatentParams& p) {
+  auto* fn = k == 4   ? append_latent_kernel<T, 4>
+             : k == 2 ? append_latent_kernel<T, 2>
+                      : append_latent_kernel<T, 1>;
+  return launch_dependent(fn, grid, block, 0, s, p);
 }
 
 template <typename T, typename CT>
-void launch_kv(int k, dim3 grid, dim3 block, cudaStream_t s, const AppendKVParams& p) {
-  if (k == 4) append_kv_kernel<T, CT, 4><<<grid, block, 0, s>>>(p);
-  else if (k == 2) append_kv_kernel<T, CT, 2><<<grid, block, 0, s>>>(p);
-  else append_kv_kernel<T, CT, 1><<<grid, block, 0, s>>>(p);
+cudaError_t launch_kv(int k, dim3 grid, dim3 block, cudaStream_t s, const AppendKVParams& p) {
+  auto* fn = k == 4   ? append_kv_kernel<T, CT, 4>
+             : k == 2 ? append_kv_kernel<T, CT, 2>
+                      : append_kv_kernel<T, CT, 1>;
+  return launch_dependent(fn, grid, block, 0, s, p);
 }
 
 }  // namespace
@@ -765,12 +772,9 @@ extern "C" mla_status_t mla_page_step(
   const int64_t share = ((int64_t)max_rows + ctas - 1) / ctas;
   p.rows_per_cta = (int)((share + 3) / 4 * 4);
   const cudaStream_t s = (cudaStream_t)stream;
-  {
-    KernelTimer kt("page_step", s);
-    if (threads == 256) page_step_kernel<256><<<(unsigned)ctas, 256, 0, s>>>(p);
-    else page_step_kernel<1024><<<(unsigned)ctas, 1024, 0, s>>>(p);
-  }
-  return launched(cudaGetLastError());
+  KernelTimer kt("page_step", s);
+  return launched(launch_dependent(threads == 256 ? page_step_kernel<256> : page_step_kernel<1024>,
+                                   dim3((unsigned)ctas), dim3(threads), 0, s, p));
 }
 
 extern "C" mla_status_t mla_append_latent(
@@ -854,12 +858,9 @@ extern "C" mla_status_t mla_append_latent(
   }
   const dim3 grid((unsigned)ctas);
   const cudaStream_t s = (cudaStream_t)stream;
-  {
-    KernelTimer kt("append_latent", s);
-    if (eb == 2) launch_latent<__nv_bfloat16>(k, grid, block, s, p);
-    else launch_latent<float>(k, grid, block, s, p);
-  }
-  return launched(cudaGetLastError());
+  KernelTimer kt("append_latent", s);
+  return launched(eb == 2 ? launch_latent<__nv_bfloat16>(k, grid, block, s, p)
+                          : launch_latent<float>(k, grid, block, s, p));
 }
 
 extern "C" mla_status_t mla_append_kv(
@@ -950,14 +951,9 @@ extern "C" mla_status_t mla_append_kv(
     return MLA_ERR_UNSUPPORTED;
   }
   const cudaStream_t s = (cudaStream_t)stream;
-  {
-    KernelTimer kt("append_kv", s);
-    if (eb == 4)
-      launch_kv<float, float>(kk, grid, block, s, p);
-    else if (g->cache_dtype == MLA_DTYPE_E4M3)
-      launch_kv<__nv_bfloat16, __nv_fp8_e4m3>(kk, grid, block, s, p);
-    else
-      launch_kv<__nv_bfloat16, __nv_bfloat16>(kk, grid, block, s, p);
-  }
-  return launched(cudaGetLastError());
+  KernelTimer kt("append_kv", s);
+  if (eb == 4) return launched(launch_kv<float, float>(kk, grid, block, s, p));
+  if (g->cache_dtype == MLA_DTYPE_E4M3)
+    return launched(launch_kv<__nv_bfloat16, __nv_fp8_e4m3>(kk, grid, block, s, p));
+  return launched(launch_kv<__nv_bfloat16, __nv_bfloat16>(kk, grid, block, s, p));
 }
