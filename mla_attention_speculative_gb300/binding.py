@@ -565,6 +565,7 @@ def mla_indexer_select(q: torch.Tensor, pooled: torch.Tensor, cache_len: int, k_
 
 # ---------------------------------------------------------------------------
 # Paged serving steps: page tables, appends, the drafter's decode attention
+# (inference only: no gradients are recorded)
 # ---------------------------------------------------------------------------
 
 def _tensor(name: str, t: torch.Tensor, shape=None, dtype=None, dense: bool = True):
@@ -937,6 +938,8 @@ class PreparedDecodeAttention(_PreparedCall):
         dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, cache_lens=cache_lens,
                           page_table=page_table, k_scale=k_scale, v_scale=v_scale, out=out,
                           lse=lse, workspace=workspace)
+        if scale is not None and not float(scale) > 0.0:
+            raise ValueError("scale must be positive (None: 1/sqrt(head_dim))")
         geom = KVGeometry(H, Hk, D, float(scale) if scale is not None else 0.0, DTYPES[q.dtype],
                           CACHE_DTYPES[k_cache.dtype])
         made = []

@@ -110,7 +110,8 @@ constexpr int kJoinLoads = 8;  // parts a thread asks for at once
 // many segments have few: 64 threads a row leave fewer CTAs with nothing to do.
 template <int TPR>
 __global__ void __launch_bounds__(kJoinThreads)
-    decode_join_kernel(const Params p, const int rows_max, const int dp, const int kind) {
+    decode_join_kernel(const Params p, const int ctas, const int rows_max, const int dp,
+                       const int kind) {
   constexpr int RPC = kJoinThreads / TPR, WPR = TPR / 32;
   __shared__ float s_w[RPC][kMaxCtas], s_l[RPC][kMaxCtas];
   __shared__ float s_red[RPC][WPR];
@@ -122,7 +123,11 @@ __global__ void __launch_bounds__(kJoinThreads)
   sm103::pdl_wait();
   const int tid = threadIdx.x, r = tid / TPR, i0 = tid % TPR, row = blockIdx.y * RPC + r;
   const Record rec = p.rec[blockIdx.x];
-  if (rec.parts == 0) return;
+  // (a workspace that another call is writing at the same time gives wrong
+  // results, but no address outside this call's buffers)
+  if (rec.parts <= 0 || rec.cta < 0 || rec.cta >= ctas || rec.parts > ctas - rec.cta ||
+      rec.b < 0 || rec.b >= p.batch || rec.hr < 0 || rec.hr >= p.kv_heads * p.row_tiles)
+    return;
   const int kvh = rec.hr / p.row_tiles, rt = rec.hr - kvh * p.row_tiles;
   const bool live = row < min(rows_max, p.group - rt * rows_max);
   const int parts = live ? rec.parts : 0;
@@ -295,11 +300,11 @@ cudaError_t launch(const Plan& d, const Params& p, cudaStream_t stream) {
   if (d.by_segment)
     return launch_dependent(decode_join_kernel<kJoinThreads>,
                             dim3((unsigned)d.records, (unsigned)rows), dim3(kJoinThreads), 0,
-                            stream, p, d.k.rows, d.k.dp, d.kind);
+                            stream, p, d.ctas, d.k.rows, d.k.dp, d.kind);
   return launch_dependent(
       decode_join_kernel<64>,
       dim3((unsigned)d.records, (unsigned)((rows * 64 + kJoinThreads - 1) / kJoinThreads)),
-      dim3(kJoinThreads), 0, stream, p, d.k.rows, d.k.dp, d.kind);
+      dim3(kJoinThreads), 0, stream, p, d.ctas, d.k.rows, d.k.dp, d.kind);
 }
 
 }  // namespace

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   long long mine = 0;
+#pragma unroll 8
   for (int b = b0; b < b1; ++b) mine += cost_of(span_of<S::TILE>(p, b));
   mine *= hrs;
   long long upto = mine;

@@ -491,6 +491,95 @@ def test_decode_one_heavy_position_among_many_light_ones(cache):
     _check_decode(c, out, lse)
 
 
+@pytest.mark.parametrize("cache", [BF16, E4M3, FP32])
+def test_decode_reads_nothing_before_the_window(cache):
+    dtype = FP32 if cache == FP32 else BF16
+    c = _decode_case([300, 41, 16], 6, 2, 64, 16, dtype, cache, seed=14)
+    window = 37
+    table = c["page_table"]
+    for b, t in enumerate([300, 41, 16]):
+        lo = max(0, t - window)
+        for pos in range(lo):                       # rows before it hold NaN
+            pid = table[b, pos // 16].item()
+            for x in (c["k_cache"], c["v_cache"]):
+                if cache == E4M3:
+                    x.view(torch.uint8)[pid, pos % 16] = 0x7F
+                else:
+                    x[pid, pos % 16] = float("nan")
+        table[b, :lo // 16] = -1                    # and whole pages have no id
+    out, lse = B.mla_decode_attention(**c, window=window, return_lse=True)
+    torch.cuda.synchronize()
+    B.mla_device_status()
+    _check_decode(c, out, lse, window)
+
+
+def test_decode_odd_scales():
+    # a negative key scale, a zero one, and none at all
+    c = _decode_case([300, 41], 9, 3, 64, 16, BF16, E4M3, seed=15)
+    c["k_scale"].copy_(torch.tensor([-0.02, 0.0, 0.01], device=DEV))
+    c["v_scale"].copy_(torch.tensor([0.01, -0.5, 0.0], device=DEV))
+    out, lse = B.mla_decode_attention(**c, return_lse=True)
+    torch.cuda.synchronize()
+    _check_decode(c, out, lse)
+    with pytest.raises(ValueError, match="positive"):
+        B.mla_decode_attention(**c, scale=-1.0)
+    c["k_scale"] = c["v_scale"] = None
+    out, lse = B.mla_decode_attention(**c, scale=1e-4, return_lse=True)
+    torch.cuda.synchronize()
+    _check_decode(c, out, lse, scale=1e-4)
+
+
+def test_decode_many_sequences():
+    # more sequences than threads of a CTA, and than CTAs
+    g = np.random.default_rng(5)
+    lens = g.integers(0, 40, 3000)
+    lens[[7, 2999]] = [1500, 700]
+    c = _decode_case(lens.tolist(), 4, 2, 64, 16, BF16, BF16, seed=16)
+    out, lse = B.mla_decode_attention(**c, return_lse=True)
+    torch.cuda.synchronize()
+    _check_decode(c, out, lse)
+
+
+def test_decode_graphs_sharing_a_workspace():
+    a = _decode_case([3000, 200], 8, 2, 128, 16, BF16, BF16, seed=41)
+    b = _decode_case([50, 1000, 700], 4, 1, 64, 16, FP32, FP32, seed=42)
+    need = [B.mla_decode_workspace_bytes(8, 2, 128, 2, 16, a["page_table"].shape[1]),
+            B.mla_decode_workspace_bytes(4, 1, 64, 3, 16, b["page_table"].shape[1], FP32)]
+    assert min(need) > 0
+    ws = torch.full((max(need),), 0x7F, dtype=torch.uint8, device=DEV)   # (any contents will do)
+    calls = [B.PreparedDecodeAttention(**x, return_lse=True, workspace=ws) for x in (a, b)]
+    graphs = []
+    for call in calls:
+        call.run()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call.run()
+    for i in (0, 1, 1, 0, 1, 0):                                        # one after the other
+        calls[i].out.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        _check_decode((a, b)[i], calls[i].out, calls[i].lse)
+
+
+def test_steps_on_several_streams():
+    cases = [_page_case(60 + i, 40, 8, 60, 9) for i in range(3)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for c, s in zip(cases, streams):
+        args = [i32(c["kept"]), i32(c["new"]), i32(c["held"]), i32(c["table"]), i32(c["free"]),
+                i32(c["span"])]
+        torch.cuda.synchronize()
+        outs.append((args, B.mla_page_step(*args, c["page"], c["num_pages"], 300,
+                                           stream=s.cuda_stream)))
+    torch.cuda.synchronize()
+    for c, (args, out) in zip(cases, outs):
+        want = P.page_step(c["kept"], c["new"], c["held"], c["table"], c["free"], c["span"],
+                           c["page"], c["num_pages"], 300)
+        assert np.array_equal(args[3].cpu().numpy(), want[0])
+        assert np.array_equal(out.slots.cpu().numpy(), want[5])
+
+
 def test_decode_strided_inputs():
     c = _decode_case([100, 37], 8, 2, 128, 16, BF16, BF16, seed=8)
     pages = c["k_cache"].shape[0]

@@ -205,6 +205,7 @@ def test_append_kv_binding_rejects(kw, match):
     (dict(out=_z(2, 8, 64)), "out must be"),
     (dict(lse=_z(2, 8)), "lse must be torch.float32"),
     (dict(q=_z(2, 8, 64)), "k_cache must be"),
+    (dict(scale=0.0), "CUDA device|scale must be positive"),
 ])
 def test_decode_binding_rejects(kw, match):
     a = dict(q=_z(2, 8, 128), k_cache=_z(4, 16, 2, 128), v_cache=_z(4, 16, 2, 128),
