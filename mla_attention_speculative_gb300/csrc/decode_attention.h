@@ -34,11 +34,13 @@ struct Shape {
   // heads whose CTA has an SM to itself and is short of warps, not of bytes on
   // their way (16 sequences of 4000 to 16000, 256 wide: fp32 511 us against
   // 622, bf16 with groups of 16 304 against 393)
-  static constexpr bool WIDE = DP >= 192 && (KIND == kFp32 || (KIND == kBf16 && NT == 2));
+  static constexpr bool WIDE = DP >= 192 && (KIND == kFp32 || NT == 2);
   static constexpr int NW = !WIDE ? 4 : DP == 192 ? 8 : 6;
   static constexpr int THREADS = NW * 32;
   // positions of a warp's tile: its K and V are 4 to 16 KB
-  static constexpr int WP = KIND == kFp32 ? (DP <= 64 ? 16 : 8) : ROWB >= 192 ? 16 : 32;
+  static constexpr int WP = KIND == kFp32                            ? (DP <= 64 ? 16 : 8)
+                            : ROWB >= 192 && !(KIND == kE4m3 && NT == 2) ? 16
+                                                                      : 32;
   static constexpr int TILE = NW * WP;  // positions of a CTA's tile
   static constexpr int ROWS = KIND == kFp32 ? 4 * NT : 8 * NT;  // query heads of a row tile
   static constexpr int STAGE = 2 * WP * ROWB;  // K, then V
@@ -55,16 +57,12 @@ struct Shape {
   static constexpr int FIT = 196608 / OCC / (NW * STAGE);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int RING = NW * STAGES * STAGE;
-  static constexpr int MSTRIDE = 36;  // floats of a merge row: 32 columns, padded
-  // two buffers, so that a round of the merge needs one barrier, where they fit
-  static constexpr int MBUFS = NW * ROWS <= 32 && KIND != kFp32 ? 2 : 1;
-  static constexpr int MBUF = NW * ROWS * MSTRIDE;  // floats of one
-  static constexpr int MERGE = MBUFS * MBUF * 4;
   static constexpr int STATS = NW * ROWS * 8;
   // fp32: the row tile's queries, and each warp's weights
   static constexpr int QTILE = KIND == kFp32 ? ROWS * DP * 4 : 0;
   static constexpr int WEIGHTS = KIND == kFp32 ? NW * 8 * ROWS * 4 : 0;
-  static constexpr int SMEM = RING + MERGE + STATS + QTILE + WEIGHTS;
+  static constexpr int SMEM = RING + STATS + QTILE + WEIGHTS;
+  static_assert(ROWS * DP * 4 <= STAGE, "a segment's sums are merged in the tile just used");
   static_assert(STAGES >= 2, "a warp's ring needs two tiles");
   // 228 KB of an SM, 1 KB of which each CTA costs besides (and a little static)
   static_assert(OCC * (SMEM + 1024 + 256) <= 228 * 1024, "OCC CTAs do not fit an SM");

@@ -149,10 +149,9 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   constexpr int ROWS = S::ROWS, WP = S::WP, CH = S::CH, STAGES = S::STAGES, NW = S::NW;
   constexpr int THREADS = S::THREADS;
   extern __shared__ __align__(128) char smem[];
-  float* const s_merge = reinterpret_cast<float*>(smem + S::RING);
-  float2* const s_ml = reinterpret_cast<float2*>(smem + S::RING + S::MERGE);
-  float* const s_q = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::STATS);
-  float* const s_w = reinterpret_cast<float*>(smem + S::RING + S::MERGE + S::STATS + S::QTILE);
+  float2* const s_ml = reinterpret_cast<float2*>(smem + S::RING);
+  float* const s_q = reinterpret_cast<float*>(smem + S::RING + S::STATS);
+  float* const s_w = reinterpret_cast<float*>(smem + S::RING + S::STATS + S::QTILE);
   __shared__ long long s_sum[NW];
   __shared__ long long s_rem;
   __shared__ int s_b;
@@ -657,6 +656,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     const bool ends = cc.j == cc.s.n - 1;
     const Cursor<S::TILE> at = cc;
     cc.next(p, t1);
+    const int used = stage;
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     if (ends || cc.t >= t1) {
       begin = true;
@@ -664,7 +664,11 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
       if (cc.t < t1) load_queries(cc);
       const int head0 = at.kvh * p.group + at.rt * ROWS;
       const int rows = min(ROWS, p.group - at.rt * ROWS);
-      // the warps' parts, joined over shared memory 32 columns at a time
+      // The warps' parts are merged in the tiles just used (the next copy goes
+      // there after the barrier below).  Columns are XORed with 8 times the pair
+      // of the row, so that the lanes of a store lie in different banks.
+      float* const mine_o = reinterpret_cast<float*>(smem + (warp * STAGES + used) * S::STAGE);
+      __syncwarp();
       if constexpr (KIND == kFp32) {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
@@ -672,6 +676,13 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
           l[r] += __shfl_xor_sync(~0u, l[r], 2);
           l[r] += __shfl_xor_sync(~0u, l[r], 4);
           if (lane == 0) s_ml[warp * ROWS + r] = make_float2(m[r], l[r]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int c = (nb * 32 + lane) * 4;
+            if (c < DP)
+              *reinterpret_cast<float4*>(mine_o + r * DP + (c ^ (((r >> 1) & 3) << 3))) =
+                  make_float4(of[nb][r][0], of[nb][r][1], of[nb][r][2], of[nb][r][3]);
+          }
         }
       } else {
 #pragma unroll
@@ -679,88 +690,73 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
           l[i] += __shfl_xor_sync(~0u, l[i], 4);
           l[i] += __shfl_xor_sync(~0u, l[i], 8);
           l[i] += __shfl_xor_sync(~0u, l[i], 16);
-          if (g == 0)
-            s_ml[warp * ROWS + (i >> 1) * 8 + quad * 2 + (i & 1)] = make_float2(m[i], l[i]);
+          const int r = (i >> 1) * 8 + quad * 2 + (i & 1);
+          if (g == 0) s_ml[warp * ROWS + r] = make_float2(m[i], l[i]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int d = mt * 16 + (KIND == kBf16 ? g + h * 8 : 2 * g + h);
+              mine_o[r * DP + (d ^ (quad << 3))] = o[mt][i >> 1][2 * h + (i & 1)];
+            }
         }
       }
       __syncthreads();
-      float f[NSTAT];
-#pragma unroll
-      for (int i = 0; i < NSTAT; ++i) {
-        const int r = KIND == kFp32 ? i : (i >> 1) * 8 + quad * 2 + (i & 1);
-        float top = s_ml[r].x;
-#pragma unroll
-        for (int w = 1; w < NW; ++w) top = fmaxf(top, s_ml[w * ROWS + r].x);
-        f[i] = ex2(m[i] - (top == -INFINITY ? 0.f : top));
-      }
-      // the reducing threads' row: its maximum and sum
-      const int rr = tid >> 3, c4 = (tid & 7) * 4;
-      float M = -INFINITY, L = 0.f;
-      if (rr < ROWS) {
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w * ROWS + rr].x);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float2 x = s_ml[w * ROWS + rr];
-          L += x.y * ex2(x.x - (M == -INFINITY ? 0.f : M));
-        }
-      }
       const bool cut = !(whole && ends);
       const int slot = whole ? 2 * cta + 1 : 2 * cta;
-      const float inv = L == 0.f ? 0.f : v_scale / L;
-      const int64_t head = (int64_t)at.b * p.heads + head0 + rr;
+      constexpr int C4 = DP / 4;
 #pragma unroll
-      for (int c0 = 0; c0 < DP; c0 += 32) {
-        float* buf = s_merge + (S::MBUFS == 2 && (c0 & 32) ? S::MBUF : 0);
-        float* mine_buf = buf + warp * ROWS * S::MSTRIDE;
-        if constexpr (KIND == kFp32) {
-          if ((lane >> 3) == (c0 >> 5) % 4) {
+      for (int i = 0; i < (ROWS * C4 + THREADS - 1) / THREADS; ++i) {
+        const int unit = tid + i * THREADS, rr = unit / C4, c = (unit % C4) * 4;
+        if (rr >= rows || c >= p.dim) continue;
+        float2 ml[NW];
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-              *reinterpret_cast<float4*>(mine_buf + r * S::MSTRIDE + (lane & 7) * 4) =
-                  make_float4(of[c0 / 128][r][0] * f[r], of[c0 / 128][r][1] * f[r],
-                              of[c0 / 128][r][2] * f[r], of[c0 / 128][r][3] * f[r]);
-          }
+        for (int w = 0; w < NW; ++w) {
+          ml[w] = s_ml[w * ROWS + rr];
+          M = fmaxf(M, ml[w].x);
+        }
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float f = ex2(ml[w].x - (M == -INFINITY ? 0.f : M));
+          const float4 x = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + (w * STAGES + used) * S::STAGE) + rr * DP +
+              (c ^ (((rr >> 1) & 3) << 3)));
+          L = fmaf(f, ml[w].y, L);
+          a.x = fmaf(f, x.x, a.x);
+          a.y = fmaf(f, x.y, a.y);
+          a.z = fmaf(f, x.z, a.z);
+          a.w = fmaf(f, x.w, a.w);
+        }
+        const int64_t head = (int64_t)at.b * p.heads + head0 + rr;
+        if (cut) {
+          *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * ROWS + rr) * DP + c) = a;
+          if (c == 0) p.part_ml[(int64_t)slot * ROWS + rr] = make_float2(M, L);
         } else {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = nt * 8 + quad * 2 + (e & 1);
-                const int d = k * 16 + (KIND == kBf16 ? g + (e >> 1) * 8 : 2 * g + (e >> 1));
-                mine_buf[r * S::MSTRIDE + d] = o[c0 / 16 + k][nt][e] * f[2 * nt + (e & 1)];
-              }
-        }
-        __syncthreads();
-        if (rr < rows && c0 + c4 < p.dim) {
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(
-                buf + (w * ROWS + rr) * S::MSTRIDE + c4);
-            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-          }
-          if (cut) {
-            *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * ROWS + rr) * DP + c0 + c4) = a;
-          } else if constexpr (KIND == kFp32) {
-            *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c0 + c4) =
+          const float inv = L == 0.f ? 0.f : v_scale / L;
+          if constexpr (KIND == kFp32)
+            *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c) =
                 make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-          } else {
-            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c0 + c4) =
+          else
+            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c) =
                 make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-          }
+          if (c == 0 && p.lse)
+            p.lse[head] = L == 0.f ? -INFINITY
+                                   : (M + log2f(L) - (KIND == kE4m3 ? kShift : 0.f)) *
+                                         0.6931471805599453f;
         }
-        // (with two buffers the next round's barrier comes before this one is written again)
-        if (S::MBUFS == 1 || c0 + 32 >= DP) __syncthreads();
       }
-      if (rr < rows && c4 == 0) {
-        if (cut)
-          p.part_ml[(int64_t)slot * ROWS + rr] = make_float2(M, L);
-        else if (p.lse)
-          p.lse[head] = L == 0.f ? -INFINITY
-                                 : (M + log2f(L) - (KIND == kE4m3 ? kShift : 0.f)) * 0.6931471805599453f;
+      __syncthreads();
+      if (chunks < CH) {
+        // the rows' ends are zeros again (a zero query times anything but a number is none)
+        for (int i = lane; i < 2 * WP * CH; i += 32) {
+          const int row = i / CH, c = i % CH;
+          if ((c ^ swizzle<CH>(row)) >= chunks)
+            *reinterpret_cast<uint4*>(smem + (warp * STAGES + used) * S::STAGE + i * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
       }
       if (whole && !ends) {
         // the segment's last tile lies in CTA ((te + 1) ctas - 1) / total
