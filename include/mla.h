@@ -392,10 +392,10 @@ mla_status_t mla_indexer_select(const float* q, const float* pooled, int64_t poo
  * Rows beyond the last real one (padding of a fixed-size step) carry slot -1
  * and position -1.  None of these calls reads lengths, slots or tables on the
  * host, so each can be captured into a CUDA graph and replayed while they
- * change.  The kernels below start only when the kernel before them in the
- * stream has finished, and mla_page_step and the two appends let no later
- * kernel start early: a verify or decode call right behind an append reads
- * what it wrote.
+ * change.  The kernels below read and write nothing before the kernel ahead of
+ * them in the stream has finished, and mla_page_step and the two appends let
+ * no later kernel start early: a verify or decode call right behind an append
+ * reads what it wrote.
  * ------------------------------------------------------------------------ */
 
 /* Page tables, cache lengths, positions and slots of one step, on the GPU.

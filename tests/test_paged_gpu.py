@@ -562,6 +562,54 @@ def test_decode_graphs_sharing_a_workspace():
         _check_decode((a, b)[i], calls[i].out, calls[i].lse)
 
 
+def test_calls_on_the_default_stream_handle_and_a_second_stream():
+    c = _decode_case([700, 33], 8, 2, 64, 16, BF16, BF16, seed=70)
+    want = B.mla_decode_attention(**c, return_lse=True)
+    got = B.mla_decode_attention(**c, return_lse=True, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    call = B.PreparedDecodeAttention(**c, return_lse=True)
+    other = torch.cuda.Stream()
+    for stream in (None, other.cuda_stream, 0, other.cuda_stream):
+        call.out.zero_()
+        torch.cuda.synchronize()
+        call.run(stream)
+        torch.cuda.synchronize()
+        assert torch.equal(call.out, want[0])
+    with pytest.raises(B.MlaError, match="aligned"):
+        lens = i32([0, 700, 33])[1:]
+        B.mla_decode_attention(**{**c, "cache_lens": lens})
+
+
+def test_direct_calls_inside_a_capture():
+    c = _page_case(71, 6, 8, 30, 9)
+    args = [i32(c["kept"]), i32(c["new"]), i32(c["held"]), i32(c["table"]), i32(c["free"]),
+            i32(c["span"])]
+    rows = 64
+    g, gen = np.random.default_rng(3), torch.Generator(DEV).manual_seed(3)
+    cs = _table(64, 64, g)
+    kv, q = _randn(gen, rows, 576, dtype=BF16), _randn(gen, rows, 4, 192, dtype=BF16)
+    ckv, kr = (torch.zeros(c["num_pages"], 8, w, dtype=BF16, device=DEV) for w in (512, 64))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        st = B.mla_page_step(*args, c["page"], c["num_pages"], rows)
+        qn, qr = B.mla_append_latent(q, kv, cs, st.positions, st.slots, ckv, kr)
+    for _ in range(2):
+        ckv.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = P.page_step(c["kept"], c["new"], c["held"], c["table"], c["free"], c["span"],
+                           c["page"], c["num_pages"], rows)
+        assert np.array_equal(st.slots.cpu().numpy(), want[5])
+        live = [(i, s) for i, s in enumerate(want[5]) if s >= 0]
+        flat = ckv.view(-1, 512)
+        assert len(live) and all(torch.equal(flat[s], kv[i, :512]) for i, s in live)
+        assert flat.abs().sum(1).count_nonzero().item() == len(live)
+        n = int(want[3][-1])
+        assert torch.equal(qn[:n], q[:n, :, :128]) and not qn[n:].any()
+
+
 def test_steps_on_several_streams():
     cases = [_page_case(60 + i, 40, 8, 60, 9) for i in range(3)]
     streams = [torch.cuda.Stream() for _ in cases]
