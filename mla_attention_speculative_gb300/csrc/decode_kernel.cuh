@@ -605,26 +605,42 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
               s[r] = fmaf(x.x, q.x, fmaf(x.y, q.y, fmaf(x.z, q.z, fmaf(x.w, q.w, s[r]))));
             }
           }
+          // (one step of every row at a time: the rows' exchanges overlap)
+          float top[ROWS];
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) s[r] += __shfl_xor_sync(~0u, s[r], 8);
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) s[r] += __shfl_xor_sync(~0u, s[r], 16);
+          const bool live = pos0 + u + row < cc.s.T;
 #pragma unroll
           for (int r = 0; r < ROWS; ++r) {
-            s[r] += __shfl_xor_sync(~0u, s[r], 8);
-            s[r] += __shfl_xor_sync(~0u, s[r], 16);
-            s[r] = pos0 + u + row < cc.s.T ? s[r] * sc[0] : -INFINITY;
-            float top = fmaxf(m[r], s[r]);
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
-            const float base = top == -INFINITY ? 0.f : top;
-            if (__any_sync(~0u, top > m[r])) {
-              const float f = ex2(m[r] - base);
+            s[r] = live ? s[r] * sc[0] : -INFINITY;
+            top[r] = s[r];
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+              top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], o));
+          bool grew = false;
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) grew = grew || top[r] > m[r];
+          if (__any_sync(~0u, grew)) {
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+              top[r] = fmaxf(top[r], m[r]);
+              const float f = ex2(m[r] - (top[r] == -INFINITY ? 0.f : top[r]));
+              m[r] = top[r];
               l[r] *= f;
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) of[nb][r][e] *= f;
             }
-            m[r] = top;
-            s[r] = ex2(s[r] - base);
+          }
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            s[r] = ex2(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
             l[r] += s[r];
             if (r / (ROWS / 4) == part) ws[row * ROWS + r] = s[r];
           }
