@@ -110,8 +110,8 @@ constexpr int kJoinLoads = 8;  // parts a thread asks for at once
 // many segments have few: 64 threads a row leave fewer CTAs with nothing to do.
 template <int TPR>
 __global__ void __launch_bounds__(kJoinThreads)
-    decode_join_kernel(const Params p, const int ctas, const int rows_max, const int dp,
-                       const int kind) {
+    decode_join_kernel(const Params p, const int ctas, const int rows_max, const int rows_live,
+                       const int dp, const int kind) {
   constexpr int RPC = kJoinThreads / TPR, WPR = TPR / 32;
   __shared__ float s_w[RPC][kMaxCtas], s_l[RPC][kMaxCtas];
   __shared__ float s_red[RPC][WPR];
@@ -121,21 +121,25 @@ __global__ void __launch_bounds__(kJoinThreads)
   // the SMs, a next call's ended up three on one SM and none on another, and 32
   // sequences of up to 32768 positions took 452 us instead of 327.)
   sm103::pdl_wait();
-  const int tid = threadIdx.x, r = tid / TPR, i0 = tid % TPR, row = blockIdx.y * RPC + r;
+  const int tid = threadIdx.x, r = tid / TPR, i0 = tid % TPR, unit = blockIdx.y * RPC + r;
+  // this row of the segment's: head `sub` of its group, row `head_row` of the row tile
+  const int sub = unit / rows_live, head_row = unit - sub * rows_live;
+  const int row = sub * rows_max + head_row, stride = p.hg * rows_max;
   const Record rec = p.rec[blockIdx.x];
   // (a workspace that another call is writing at the same time gives wrong
   // results, but no address outside this call's buffers)
   if (rec.parts <= 0 || rec.cta < 0 || rec.cta >= ctas || rec.parts > ctas - rec.cta ||
-      rec.b < 0 || rec.b >= p.batch || rec.hr < 0 || rec.hr >= p.kv_heads * p.row_tiles)
+      rec.b < 0 || rec.b >= p.batch || rec.hr < 0 || rec.hr >= p.kv_groups * p.row_tiles)
     return;
-  const int kvh = rec.hr / p.row_tiles, rt = rec.hr - kvh * p.row_tiles;
-  const bool live = row < min(rows_max, p.group - rt * rows_max);
+  const int kvg = rec.hr / p.row_tiles, rt = rec.hr - kvg * p.row_tiles;
+  const int kvh = kvg * p.hg + sub;
+  const bool live = sub < p.hg && head_row < min(rows_max, p.group - rt * rows_max);
   const int parts = live ? rec.parts : 0;
   // part k: the last segment of the first share, then the first one of those behind it
   auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * rec.cta + 1 : 2 * (rec.cta + k)); };
   float M = -INFINITY;
   for (int k = i0; k < parts; k += TPR) {
-    const float2 ml = p.part_ml[slot(k) * rows_max + row];
+    const float2 ml = p.part_ml[slot(k) * stride + row];
     s_w[r][k] = ml.x;
     s_l[r][k] = ml.y;
     M = fmaxf(M, ml.x);
@@ -143,7 +147,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int cols = dp / 4, groups = TPR / cols;
   const int grp = i0 / cols, c = i0 - grp * cols;
   const float* part = p.part_o + (int64_t)row * dp + c * 4;
-  const int64_t step = (int64_t)rows_max * dp;
+  const int64_t step = (int64_t)stride * dp;
   float4 x[kJoinLoads];
   auto ask = [&](int k0) {
 #pragma unroll
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   s_acc[tid] = a;
   __syncthreads();
   if (!live) return;
-  const int64_t head = (int64_t)rec.b * p.heads + kvh * p.group + rt * rows_max + row;
+  const int64_t head = (int64_t)rec.b * p.heads + kvh * p.group + rt * rows_max + head_row;
   if (i0 < cols && c * 4 < p.dim) {
     for (int g = 1; g < groups; ++g) {
       const float4 y = s_acc[r * TPR + g * cols + c];
@@ -223,6 +227,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 struct Plan {
   Kernel k;
   int kind, row_tiles, ctas;
+  int hg, pw, tile, kv_groups;
   bool cut;         // a segment may fall into several shares
   bool by_segment;  // records by segment: fewer than CTAs
   int records;
@@ -231,19 +236,32 @@ struct Plan {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-mla_status_t make_plan(const mla_kv_geometry_t* g, int32_t batch, int32_t page_size,
-                       int32_t max_pages, Plan* out) {
-  Plan& d = *out;
-  d.kind = g->dtype == MLA_DTYPE_FP32 ? kFp32 : g->cache_dtype == MLA_DTYPE_E4M3 ? kE4m3 : kBf16;
-  const int group = g->num_heads / g->num_kv_heads;
+Kernel kernel_of(const mla_kv_geometry_t* g, int kind) {
   // one row multiple when the group fits it: half the products and registers
-  const int nt = group <= (d.kind == kFp32 ? 4 : 8) ? 1 : 2;
-  d.k = d.kind == kFp32   ? kernel_fp32(g->head_dim, nt)
-        : d.kind == kE4m3 ? kernel_e4m3(g->head_dim, nt)
-                          : kernel_bf16(g->head_dim, nt);
+  const int nt = g->num_heads / g->num_kv_heads <= (kind == kFp32 ? 4 : 8) ? 1 : 2;
+  return kind == kFp32   ? kernel_fp32(g->head_dim, nt)
+         : kind == kE4m3 ? kernel_e4m3(g->head_dim, nt)
+                         : kernel_bf16(g->head_dim, nt);
+}
+
+int kind_of(const mla_kv_geometry_t* g) {
+  return g->dtype == MLA_DTYPE_FP32 ? kFp32 : g->cache_dtype == MLA_DTYPE_E4M3 ? kE4m3 : kBf16;
+}
+
+// The plan with `hg` key/value heads to a tile.
+mla_status_t plan_for(const mla_kv_geometry_t* g, int32_t batch, int32_t page_size,
+                      int32_t max_pages, int hg, Plan* out) {
+  Plan& d = *out;
+  d.kind = kind_of(g);
+  const int group = g->num_heads / g->num_kv_heads;
+  d.k = kernel_of(g, d.kind);
   d.row_tiles = (group + d.k.rows - 1) / d.k.rows;
-  const int64_t hrs = (int64_t)g->num_kv_heads * d.row_tiles;
-  const int64_t tiles = ((int64_t)page_size * max_pages + d.k.tile - 1) / d.k.tile;
+  d.hg = hg;
+  d.pw = d.k.warps / hg;
+  d.tile = d.pw * d.k.wp;
+  d.kv_groups = g->num_kv_heads / hg;
+  const int64_t hrs = (int64_t)d.kv_groups * d.row_tiles;
+  const int64_t tiles = ((int64_t)page_size * max_pages + d.tile - 1) / d.tile;
   const int64_t most = (int64_t)batch * hrs * tiles;
   if (most > ((int64_t)1 << 48)) {
     set_error("decode: batch %d x %lld rows of a table is beyond what is planned for", batch,
@@ -257,17 +275,51 @@ mla_status_t make_plan(const mla_kv_geometry_t* g, int32_t batch, int32_t page_s
   d.cut = tiles > 1;
   d.by_segment = batch * hrs <= ctas;
   d.records = d.by_segment ? (int)(batch * hrs) : (int)ctas;
+  const size_t rows = (size_t)2 * ctas * hg * d.k.rows;
   size_t off = align256(sizeof(Record) * d.records);
   d.off_ml = off;
-  off = align256(off + sizeof(float2) * 2 * ctas * d.k.rows);
+  off = align256(off + sizeof(float2) * rows);
   d.off_o = off;
-  off = align256(off + sizeof(float) * 2 * ctas * d.k.rows * d.k.dp);
+  off = align256(off + sizeof(float) * rows * d.k.dp);
   d.bytes = d.cut ? off : 0;
   return MLA_OK;
 }
 
+// Whether a tile may hold `hg` heads: they share its warps evenly, and the
+// kernel keeps a head's queries per warp (fp32 keeps them per CTA).
+bool heads_fit(const mla_kv_geometry_t* g, int hg) {
+  const int kind = kind_of(g);
+  const Kernel k = kernel_of(g, kind);
+  return hg == 1 || (k.fn_heads != nullptr && g->num_kv_heads % hg == 0 && k.warps % hg == 0);
+}
+
+// Heads that lie side by side in a cache row and are no whole 128-byte lines
+// share lines with their neighbours, whose CTAs come by at another time: the
+// lines are fetched again (heads of 80 in bf16: 637 MB for 437).  Then a tile
+// takes as many neighbouring heads as make whole lines, a warp or two each (32
+// sequences of 1024 to 32768: 80 wide 315 -> 216 us, 96 wide 315 -> 248; e4m3,
+// 64 wide 146 -> 99), if the cache is beyond what L2 keeps between two heads:
+// the join has more to do, and below that the lines are found in L2 (16
+// sequences of up to 4099, 80 wide: 19.2 us with one head, 21.4 with four).
+mla_status_t make_plan(const mla_kv_geometry_t* g, const mla_kv_cache_t* cache, int32_t batch,
+                       int32_t max_pages, Plan* out) {
+  const mla_status_t st = plan_for(g, batch, cache->page_size, max_pages, 1, out);
+  constexpr int64_t kLine = 128;
+  constexpr double kLarge = 256.0 * 1024 * 1024;
+  const int64_t piece = (int64_t)g->head_dim * (g->cache_dtype == MLA_DTYPE_E4M3   ? 1
+                                                : g->cache_dtype == MLA_DTYPE_FP32 ? 4
+                                                                                   : 2);
+  const double bytes = 2.0 * piece * g->num_kv_heads * batch * cache->page_size * max_pages;
+  if (st != MLA_OK || !out->cut || piece % kLine == 0 || bytes < kLarge ||
+      cache->head_stride >= cache->row_stride)
+    return st;
+  int hg = 1;
+  while (hg < 4 && hg * piece % kLine != 0 && heads_fit(g, 2 * hg)) hg *= 2;
+  return hg == 1 ? st : plan_for(g, batch, cache->page_size, max_pages, hg, out);
+}
+
 // Allow a kernel its shared memory, once per kernel and device.
-cudaError_t allow_smem(const Kernel& k) {
+cudaError_t allow_smem(const Kernel& k, void (*fn)(Params)) {
   struct Done {
     int device;
     void (*fn)(Params);
@@ -281,30 +333,31 @@ cudaError_t allow_smem(const Kernel& k) {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
   for (int i = 0; i < count; ++i)
-    if (done[i].device == dev && done[i].fn == k.fn) return cudaSuccess;
-  e = cudaFuncSetAttribute((const void*)k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-  if (e == cudaSuccess && count < kMost) done[count++] = {dev, k.fn};
+    if (done[i].device == dev && done[i].fn == fn) return cudaSuccess;
+  e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+  if (e == cudaSuccess && count < kMost) done[count++] = {dev, fn};
   return e;
 }
 
 cudaError_t launch(const Plan& d, const Params& p, cudaStream_t stream) {
-  cudaError_t e = allow_smem(d.k);
+  void (*fn)(Params) = d.hg > 1 ? d.k.fn_heads : d.k.fn;
+  cudaError_t e = allow_smem(d.k, fn);
   if (e != cudaSuccess) return e;
   {
     KernelTimer kt("decode_attn", stream);
-    e = launch_dependent(d.k.fn, dim3((unsigned)d.ctas), dim3(d.k.threads), d.k.smem, stream, p);
+    e = launch_dependent(fn, dim3((unsigned)d.ctas), dim3(d.k.warps * 32), d.k.smem, stream, p);
   }
   if (e != cudaSuccess || !d.cut) return e;
-  const int rows = p.group < d.k.rows ? p.group : d.k.rows;
+  const int live = p.group < d.k.rows ? p.group : d.k.rows, rows = live * d.hg;
   KernelTimer kt("decode_join", stream);
   if (d.by_segment)
     return launch_dependent(decode_join_kernel<kJoinThreads>,
                             dim3((unsigned)d.records, (unsigned)rows), dim3(kJoinThreads), 0,
-                            stream, p, d.ctas, d.k.rows, d.k.dp, d.kind);
+                            stream, p, d.ctas, d.k.rows, live, d.k.dp, d.kind);
   return launch_dependent(
       decode_join_kernel<64>,
       dim3((unsigned)d.records, (unsigned)((rows * 64 + kJoinThreads - 1) / kJoinThreads)),
-      dim3(kJoinThreads), 0, stream, p, d.ctas, d.k.rows, d.k.dp, d.kind);
+      dim3(kJoinThreads), 0, stream, p, d.ctas, d.k.rows, live, d.k.dp, d.kind);
 }
 
 }  // namespace
@@ -337,10 +390,15 @@ extern "C" mla_status_t mla_decode_workspace_bytes(const mla_kv_geometry_t* g, i
   }
   const mla_status_t st = decode_sizes_ok(g, batch, page_size, max_pages_per_seq);
   if (st != MLA_OK) return st;
-  decode::Plan d;
-  const mla_status_t pst = decode::make_plan(g, batch, page_size, max_pages_per_seq, &d);
-  if (pst != MLA_OK) return pst;
-  *bytes = d.bytes;
+  // the cache's layout decides how many heads a tile holds: room for each
+  *bytes = 0;
+  for (int hg = 1; hg <= 4; hg *= 2) {
+    if (!decode::heads_fit(g, hg)) continue;
+    decode::Plan d;
+    const mla_status_t pst = decode::plan_for(g, batch, page_size, max_pages_per_seq, hg, &d);
+    if (pst != MLA_OK) return pst;
+    if (d.bytes > *bytes) *bytes = d.bytes;
+  }
   return MLA_OK;
 }
 
@@ -378,11 +436,14 @@ extern "C" mla_status_t mla_decode_attention(
     return MLA_ERR_INVALID_ARG;
   }
   decode::Plan d;
-  st = decode::make_plan(g, batch, cache->page_size, max_pages_per_seq, &d);
+  st = decode::make_plan(g, cache, batch, max_pages_per_seq, &d);
   if (st != MLA_OK) return st;
-  if (workspace_bytes < d.bytes || (d.bytes > 0 && workspace == nullptr)) {
+  size_t need = 0;
+  st = mla_decode_workspace_bytes(g, batch, cache->page_size, max_pages_per_seq, &need);
+  if (st != MLA_OK) return st;
+  if (workspace_bytes < need || (need > 0 && workspace == nullptr)) {
     set_error("workspace of %zu bytes is smaller than the %zu this call needs", workspace_bytes,
-              d.bytes);
+              need);
     return MLA_ERR_WORKSPACE;
   }
   if ((uintptr_t)workspace & 255u) {
@@ -408,7 +469,11 @@ extern "C" mla_status_t mla_decode_attention(
   p.part_ml = d.cut ? (float2*)((char*)workspace + d.off_ml) : nullptr;
   p.part_o = d.cut ? (float*)((char*)workspace + d.off_o) : nullptr;
   p.heads = g->num_heads;
-  p.kv_heads = g->num_kv_heads;
+  p.kv_groups = d.kv_groups;
+  p.hg = d.hg;
+  p.pw = d.pw;
+  p.tile = d.tile;
+  p.tile_div = PageDiv(d.tile);
   p.group = g->num_heads / g->num_kv_heads;
   p.row_tiles = d.row_tiles;
   p.dim = g->head_dim;

@@ -41,7 +41,6 @@ struct Shape {
   static constexpr int WP = KIND == kFp32                            ? (DP <= 64 ? 16 : 8)
                             : ROWB >= 192 && !(KIND == kE4m3 && NT == 2) ? 16
                                                                       : 32;
-  static constexpr int TILE = NW * WP;  // positions of a CTA's tile
   static constexpr int ROWS = KIND == kFp32 ? 4 * NT : 8 * NT;  // query heads of a row tile
   static constexpr int STAGE = 2 * WP * ROWB;  // K, then V
   // Three CTAs per SM with rings of two tiles per warp where the registers of
@@ -87,16 +86,21 @@ struct Params {
   float* lse;
   Record* rec;     // by segment or by CTA; NULL: no sequence is cut
   int by_segment;
-  float2* part_ml; // [2 * ctas][ROWS] running maximum (base 2) and sum
-  float* part_o;   // [2 * ctas][ROWS][DP] unnormalised
-  int heads, kv_heads, group, row_tiles, dim, batch, page, width, num_pages, window;
+  float2* part_ml; // [2 * ctas][hg][ROWS] running maximum (base 2) and sum
+  float* part_o;   // [2 * ctas][hg][ROWS][DP] unnormalised
+  int heads, group, row_tiles, dim, batch, page, width, num_pages, window;
+  // a tile: `hg` neighbouring key/value heads, each taken by `pw` warps side by
+  // side, `tile` positions in all; kv_groups such groups of heads
+  int kv_groups, hg, pw, tile;
+  PageDiv tile_div;
   PageDiv div;  // by `page`
   float scale_log2;  // softmax scale * log2(e)
 };
 
 struct Kernel {
-  void (*fn)(Params);
-  int smem, threads, occupancy, tile, rows, dp;
+  void (*fn)(Params);        // one key/value head to a tile
+  void (*fn_heads)(Params);  // several (NULL: none)
+  int smem, warps, occupancy, wp, rows, dp;
 };
 
 // The kernel for a head width and row multiple nt (1, 2).

@@ -75,23 +75,25 @@ struct Span {  // the positions a sequence sees, and its tiles
   int lo, T, n;
 };
 
+// TILE: positions of a tile, 0: as the call says.
 template <int TILE>
 __device__ __forceinline__ Span span_of(const Params& p, int b) {
   Span s;
   s.T = (int)min((long long)max(p.lens[b], 0), (long long)p.width * p.page);
   s.lo = p.window > 0 ? max(0, s.T - p.window) : 0;
-  s.n = (s.T - s.lo + TILE - 1) / TILE;
+  s.n = TILE > 0 ? (s.T - s.lo + TILE - 1) / (TILE > 0 ? TILE : 1)
+                 : p.tile_div(s.T - s.lo + p.tile - 1);
   return s;
 }
 
 // What a sequence's segments count for, each, when the work is dealt out.
 __device__ __forceinline__ int cost_of(const Span& s) { return s.n > 0 ? s.n + kSegmentCost : 0; }
 
-// A place in the work: tile j of segment (b, kvh, rt), and its place t in the
+// A place in the work: tile j of segment (b, kvg, rt), and its place t in the
 // list in which a segment's tiles come behind kSegmentCost places without one.
 template <int TILE>
 struct Cursor {
-  int b, kvh, rt, j;
+  int b, kvg, rt, j;
   long long t;
   Span s;
   // To the next tile; beyond `end` the place alone is right.
@@ -103,8 +105,8 @@ struct Cursor {
     j = 0;
     if (++rt < p.row_tiles) return;
     rt = 0;
-    if (++kvh < p.kv_heads) return;
-    kvh = 0;
+    if (++kvg < p.kv_groups) return;
+    kvg = 0;
     do {
       s = span_of<TILE>(p, ++b);
     } while (s.n == 0);
@@ -124,7 +126,7 @@ __device__ __forceinline__ void zero_idle(const Params& p) {
       for (int h = threadIdx.x; h < p.heads; h += blockDim.x)
         p.lse[(int64_t)b * p.heads + h] = -INFINITY;
     if (p.rec && p.by_segment) {
-      const int hrs = p.kv_heads * p.row_tiles;
+      const int hrs = p.kv_groups * p.row_tiles;
       for (int i = threadIdx.x; i < hrs; i += blockDim.x)
         p.rec[(int64_t)b * hrs + i].parts = 0;
     }
@@ -149,12 +151,14 @@ __device__ __forceinline__ long long div_small(long long a, int b) {
   return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-template <int DP, int KIND, int NT>
+// HEADS: a tile may hold several key/value heads (p.hg of them).
+template <int DP, int KIND, int NT, bool HEADS>
 __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIND, NT>::OCC))
     decode_attn_sm103(const Params p) {
   using S = Shape<DP, KIND, NT>;
   constexpr int ROWS = S::ROWS, WP = S::WP, CH = S::CH, STAGES = S::STAGES, NW = S::NW;
-  constexpr int THREADS = S::THREADS;
+  constexpr int THREADS = S::THREADS, TILE = HEADS ? 0 : NW * WP;
+  const int hg = HEADS ? p.hg : 1, pw = HEADS ? p.pw : NW, tile = HEADS ? p.tile : TILE;
   extern __shared__ __align__(128) char smem[];
   float2* const s_ml = reinterpret_cast<float2*>(smem + S::RING);
   float* const s_q = reinterpret_cast<float*>(smem + S::RING + S::STATS);
@@ -164,6 +168,8 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   __shared__ int s_b;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // this warp's head of the tile's, and its positions' place in the tile
+  const int sub = HEADS ? warp / pw : 0, pos_in_tile = (warp - sub * pw) * WP;
   const uint32_t ring = smem_u32(smem) + warp * STAGES * S::STAGE;
   const int chunks = p.dim * S::CB / 16;  // of a row; the rest of a tile row stays zero
   if (chunks < CH) {
@@ -176,12 +182,12 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   pdl_launch_dependents();
 
   // ---- this CTA's share of the tiles
-  const int hrs = p.kv_heads * p.row_tiles;
+  const int hrs = p.kv_groups * p.row_tiles;
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   long long mine = 0;
 #pragma unroll 8
-  for (int b = b0; b < b1; ++b) mine += cost_of(span_of<S::TILE>(p, b));
+  for (int b = b0; b < b1; ++b) mine += cost_of(span_of<TILE>(p, b));
   mine *= hrs;
   long long upto = mine;
 #pragma unroll
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   const int cta = blockIdx.x;
   if (cta >= ctas) {
     if (tid == 0 && p.rec && !p.by_segment) p.rec[cta].parts = 0;
-    zero_idle<S::TILE, KIND>(p);
+    zero_idle<TILE, KIND>(p);
     return;
   }
   // share i is places floor(total i / ctas) up to the next one's first
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     int b = b0;
     if (per > 1) {
       for (; b < b1 - 1; ++b) {
-        const long long n = (long long)cost_of(span_of<S::TILE>(p, b)) * hrs;
+        const long long n = (long long)cost_of(span_of<TILE>(p, b)) * hrs;
         if (t0 < at + n) break;
         at += n;
       }
@@ -223,15 +229,15 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     s_rem = t0 - at;
   }
   __syncthreads();
-  Cursor<S::TILE> cc;  // the tile being computed
+  Cursor<TILE> cc;  // the tile being computed
   cc.b = s_b;
-  cc.s = span_of<S::TILE>(p, cc.b);
+  cc.s = span_of<TILE>(p, cc.b);
   const int hr = (int)div_small(s_rem, cost_of(cc.s));
   const int place = (int)(s_rem - (long long)hr * cost_of(cc.s)) - kSegmentCost;
   cc.j = max(place, 0);
   cc.t = t0 + max(-place, 0);
-  cc.kvh = hr / p.row_tiles;
-  cc.rt = hr - cc.kvh * p.row_tiles;
+  cc.kvg = hr / p.row_tiles;
+  cc.rt = hr - cc.kvg * p.row_tiles;
 
   // ---- state of a segment, per lane
   // matrix kinds: heads 8 nt + 2 (lane % 4) + {0, 1}; fp32: all ROWS heads
@@ -254,10 +260,11 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   // begins; fp32 stages them in shared memory.
   constexpr int QV = KIND == kFp32 ? (ROWS * DP / 4 + THREADS - 1) / THREADS : 1;
   float4 qv[QV];
-  float ks = 1.f, vs = 1.f;  // e4m3: the head's scales
-  auto load_queries = [&](const Cursor<S::TILE>& c) {
+  float ks = 1.f;  // e4m3: the keys' scale
+  auto load_queries = [&](const Cursor<TILE>& c) {
     const int rows = min(ROWS, p.group - c.rt * ROWS);
-    const int64_t base = c.b * p.q_stride + (int64_t)(c.kvh * p.group + c.rt * ROWS) * p.dim;
+    const int kvh = c.kvg * hg + sub;
+    const int64_t base = c.b * p.q_stride + (int64_t)(kvh * p.group + c.rt * ROWS) * p.dim;
     if constexpr (KIND == kFp32) {
 #pragma unroll
       for (int i = 0; i < QV; ++i) {
@@ -269,8 +276,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     } else {
       const __nv_bfloat16* q = (const __nv_bfloat16*)p.q + base;
       if constexpr (KIND == kE4m3) {
-        ks = p.k_scale ? p.k_scale[c.kvh] : 1.f;
-        vs = p.v_scale ? p.v_scale[c.kvh] : 1.f;
+        ks = p.k_scale ? p.k_scale[kvh] : 1.f;
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -300,16 +306,17 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   load_queries(cc);
 
   // ---- copies
-  Cursor<S::TILE> lc = cc;  // the tile whose page ids were last asked for
+  Cursor<TILE> lc = cc;  // the tile whose page ids were last asked for
   auto locate = [&]() {
     RowAt r;
-    const int pos = lc.s.lo + lc.j * S::TILE + warp * WP + (lane & (WP - 1));
+    const int pos = lc.s.lo + lc.j * tile + pos_in_tile + (lane & (WP - 1));
     r.off = -1;
     r.id = 0;
     if (pos < lc.s.T) {
       const int pg = p.div(pos);
       r.id = p.table[(int64_t)lc.b * p.width + pg];
-      r.off = (int64_t)(pos - pg * p.page) * p.row_stride + lc.kvh * p.head_stride;
+      r.off = (int64_t)(pos - pg * p.page) * p.row_stride +
+              (int64_t)(lc.kvg * hg + sub) * p.head_stride;
     }
     return r;
   };
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     }
 
     // ---- one tile: positions pos0 .. pos0 + WP - 1
-    const int pos0 = cc.s.lo + cc.j * S::TILE + warp * WP;
+    const int pos0 = cc.s.lo + cc.j * tile + pos_in_tile;
     const uint32_t kb = ring + stage * S::STAGE, vb = kb + WP * S::ROWB;
     if (pos0 < cc.s.T) {
       if constexpr (KIND != kFp32) {
@@ -677,15 +684,13 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
 
     // ---- the segment ends here, or this share does
     const bool ends = cc.j == cc.s.n - 1;
-    const Cursor<S::TILE> at = cc;
+    const Cursor<TILE> at = cc;
     cc.next(p, t1);
     const int used = stage;
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     if (ends || cc.t >= t1) {
       begin = true;
-      const float v_scale = vs;
       if (cc.t < t1) load_queries(cc);
-      const int head0 = at.kvh * p.group + at.rt * ROWS;
       const int rows = min(ROWS, p.group - at.rt * ROWS);
       // The warps' parts are merged in the tiles just used (the next copy goes
       // there after the barrier below).  Columns are XORed with 8 times the pair
@@ -728,46 +733,55 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
       const bool cut = !(whole && ends);
       const int slot = whole ? 2 * cta + 1 : 2 * cta;
       constexpr int C4 = DP / 4;
+      for (int x = 0; x < hg; ++x) {  // the tile's heads
+        const int kvh = at.kvg * hg + x;
+        const float v_scale = KIND == kE4m3 && p.v_scale ? p.v_scale[kvh] : 1.f;
+        const int64_t head0 = (int64_t)at.b * p.heads + kvh * p.group + at.rt * ROWS;
+        const int64_t row0 = (int64_t)(slot * hg + x) * ROWS;
 #pragma unroll
-      for (int i = 0; i < (ROWS * C4 + THREADS - 1) / THREADS; ++i) {
-        const int unit = tid + i * THREADS, rr = unit / C4, c = (unit % C4) * 4;
-        if (rr >= rows || c >= p.dim) continue;
-        float2 ml[NW];
-        float M = -INFINITY, L = 0.f;
+        for (int i = 0; i < (ROWS * C4 + THREADS - 1) / THREADS; ++i) {
+          const int unit = tid + i * THREADS, rr = unit / C4, c = (unit % C4) * 4;
+          if (rr >= rows || c >= p.dim) continue;
+          float2 ml[NW];
+          float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          ml[w] = s_ml[w * ROWS + rr];
-          M = fmaxf(M, ml[w].x);
-        }
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int w = 0; w < NW; ++w) {
+            ml[w] = make_float2(-INFINITY, 0.f);
+            if (w < pw) ml[w] = s_ml[(x * pw + w) * ROWS + rr];
+            M = fmaxf(M, ml[w].x);
+          }
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float f = ex2(ml[w].x - (M == -INFINITY ? 0.f : M));
-          const float4 x = *reinterpret_cast<const float4*>(
-              reinterpret_cast<const float*>(smem + (w * STAGES + used) * S::STAGE) + rr * DP +
-              (c ^ (((rr >> 1) & 3) << 3)));
-          L = fmaf(f, ml[w].y, L);
-          a.x = fmaf(f, x.x, a.x);
-          a.y = fmaf(f, x.y, a.y);
-          a.z = fmaf(f, x.z, a.z);
-          a.w = fmaf(f, x.w, a.w);
-        }
-        const int64_t head = (int64_t)at.b * p.heads + head0 + rr;
-        if (cut) {
-          *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * ROWS + rr) * DP + c) = a;
-          if (c == 0) p.part_ml[(int64_t)slot * ROWS + rr] = make_float2(M, L);
-        } else {
-          const float inv = L == 0.f ? 0.f : v_scale / L;
-          if constexpr (KIND == kFp32)
-            *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c) =
-                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-          else
-            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c) =
-                make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-          if (c == 0 && p.lse)
-            p.lse[head] = L == 0.f ? -INFINITY
-                                   : (M + log2f(L) - (KIND == kE4m3 ? kShift : 0.f)) *
-                                         0.6931471805599453f;
+          for (int w = 0; w < NW; ++w) {
+            if (w >= pw) continue;
+            const float f = ex2(ml[w].x - (M == -INFINITY ? 0.f : M));
+            const float4 y = *reinterpret_cast<const float4*>(
+                reinterpret_cast<const float*>(
+                    smem + ((x * pw + w) * STAGES + used) * S::STAGE) +
+                rr * DP + (c ^ (((rr >> 1) & 3) << 3)));
+            L = fmaf(f, ml[w].y, L);
+            a.x = fmaf(f, y.x, a.x);
+            a.y = fmaf(f, y.y, a.y);
+            a.z = fmaf(f, y.z, a.z);
+            a.w = fmaf(f, y.w, a.w);
+          }
+          if (cut) {
+            *reinterpret_cast<float4*>(p.part_o + (row0 + rr) * DP + c) = a;
+            if (c == 0) p.part_ml[row0 + rr] = make_float2(M, L);
+          } else {
+            const int64_t head = head0 + rr;
+            const float inv = L == 0.f ? 0.f : v_scale / L;
+            if constexpr (KIND == kFp32)
+              *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c) =
+                  make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+            else
+              *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c) =
+                  make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+            if (c == 0 && p.lse)
+              p.lse[head] = L == 0.f ? -INFINITY
+                                     : (M + log2f(L) - (KIND == kE4m3 ? kShift : 0.f)) *
+                                           0.6931471805599453f;
+          }
         }
       }
       __syncthreads();
@@ -786,22 +800,26 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
         const long long te = at.t + (at.s.n - 1 - at.j);
         rec.cta = cta;
         rec.b = at.b;
-        rec.hr = at.kvh * p.row_tiles + at.rt;
+        rec.hr = at.kvg * p.row_tiles + at.rt;
         rec.parts = (int)(((te + 1) * ctas - 1) / total) - cta + 1;
       }
       // (the CTA in which a segment begins writes its record)
       if (tid == 0 && p.rec && p.by_segment && whole)
-        p.rec[(int64_t)at.b * hrs + at.kvh * p.row_tiles + at.rt] = rec;
+        p.rec[(int64_t)at.b * hrs + at.kvg * p.row_tiles + at.rt] = rec;
     }
   }
   if (tid == 0 && p.rec && !p.by_segment) p.rec[cta] = rec;
-  zero_idle<S::TILE, KIND>(p);
+  zero_idle<TILE, KIND>(p);
 }
 
 template <int DP, int KIND, int NT>
 Kernel kernel_of() {
   using S = Shape<DP, KIND, NT>;
-  return {decode_attn_sm103<DP, KIND, NT>, S::SMEM, S::THREADS, S::OCC, S::TILE, S::ROWS, DP};
+  // (fp32 keeps a segment's queries per CTA, for one head)
+  void (*heads)(Params) = nullptr;
+  if constexpr (KIND != kFp32) heads = decode_attn_sm103<DP, KIND, NT, true>;
+  return {decode_attn_sm103<DP, KIND, NT, false>, heads, S::SMEM, S::NW, S::OCC, S::WP, S::ROWS,
+          DP};
 }
 
 template <int KIND, int NT>

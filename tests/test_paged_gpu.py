@@ -461,6 +461,29 @@ def test_decode_matches_oracle(lens, H, Hk, D, page, dtype, cache, by_head, wind
     assert torch.equal(out, again) and torch.equal(lse, lse2)    # the same bits each time
 
 
+@pytest.mark.parametrize("lens,H,Hk,D,page,cache,window", [
+    (EDGES, 8, 4, 80, 16, BF16, 0), (EDGES, 8, 8, 40, 16, BF16, 0), (EDGES, 4, 2, 96, 7, BF16, 33),
+    (EDGES, 12, 4, 112, 64, BF16, 0), (EDGES, 6, 2, 80, 16, BF16, 0), (EDGES, 3, 3, 80, 16, BF16, 0),
+    (EDGES, 8, 4, 64, 16, E4M3, 0), (EDGES, 36, 4, 96, 24, E4M3, 0), (EDGES, 4, 4, 16, 16, E4M3, 20),
+    ([700, 5, 2000, 0], 36, 4, 200, 16, BF16, 0), ([700, 5, 2000, 0], 36, 4, 168, 16, BF16, 0),
+    ([700, 5, 2000, 0], 8, 4, 192, 16, E4M3, 0), ([700, 5, 2000, 0], 72, 4, 208, 16, E4M3, 0),
+    ([9000, 1, 4000], 8, 4, 8, 16, BF16, 0), ([30, 0, 64, 7] * 90, 8, 4, 80, 16, BF16, 0),
+])
+def test_decode_several_heads_to_a_tile(lens, H, Hk, D, page, cache, window):
+    # heads side by side that are no whole lines, and a table of a cache beyond 256 MB
+    size = 1 if cache == E4M3 else 2
+    width = -(-(256 << 20) // (2 * D * size * Hk * len(lens) * page)) + 1
+    c = _decode_case(lens, H, Hk, D, page, BF16, cache, seed=len(lens) + D, width=width)
+    out, lse = B.mla_decode_attention(**c, window=window, return_lse=True)
+    torch.cuda.synchronize()
+    B.mla_device_status()
+    narrow = dict(c, page_table=c["page_table"][:, :max(-(-max(lens) // page), 1)].contiguous())
+    _check_decode(narrow, out, lse, window)
+    one, one_lse = B.mla_decode_attention(**narrow, window=window, return_lse=True)
+    torch.cuda.synchronize()
+    _check_decode(narrow, one, one_lse, window)
+
+
 @pytest.mark.parametrize("cache", [BF16, E4M3, FP32])
 def test_decode_sharp_scores_and_scale(cache):
     dtype = FP32 if cache == FP32 else BF16
