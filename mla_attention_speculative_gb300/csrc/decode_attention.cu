@@ -295,26 +295,30 @@ bool heads_fit(const mla_kv_geometry_t* g, int hg) {
 
 // Heads that lie side by side in a cache row and are no whole 128-byte lines
 // share lines with their neighbours, whose CTAs come by at another time: the
-// lines are fetched again (heads of 80 in bf16: 637 MB for 437).  Then a tile
-// takes as many neighbouring heads as make whole lines, a warp or two each (32
-// sequences of 1024 to 32768: 80 wide 315 -> 216 us, 96 wide 315 -> 248; e4m3,
-// 64 wide 146 -> 99), if the cache is beyond what L2 keeps between two heads:
-// the join has more to do, and below that the lines are found in L2 (16
-// sequences of up to 4099, 80 wide: 19.2 us with one head, 21.4 with four).
+// lines are fetched again (heads of 80 in bf16: 637 MB for 437).  And single
+// lines a row apart come from DRAM slower than two at a time.  So a tile takes
+// as many neighbouring heads as make whole lines, two at least, a warp or two
+// each (32 sequences of 1024 to 32768: 80 wide 315 -> 216 us, 96 wide 315 ->
+// 248, 64 wide 189 -> 173; e4m3, 64 sequences: 64 wide 146 -> 102, 128 wide in
+// groups of 4 169 -> 159), if the cache is beyond what L2 keeps between two
+// heads: the merge and the join have more to do, and below that the lines are
+// found in L2 (16 sequences of up to 4099, 80 wide: 19.2 us with one head to a
+// tile, 21.4 with four).
 mla_status_t make_plan(const mla_kv_geometry_t* g, const mla_kv_cache_t* cache, int32_t batch,
                        int32_t max_pages, Plan* out) {
   const mla_status_t st = plan_for(g, batch, cache->page_size, max_pages, 1, out);
-  constexpr int64_t kLine = 128;
+  constexpr int64_t kLine = 128, kRun = 256;
   constexpr double kLarge = 256.0 * 1024 * 1024;
   const int64_t piece = (int64_t)g->head_dim * (g->cache_dtype == MLA_DTYPE_E4M3   ? 1
                                                 : g->cache_dtype == MLA_DTYPE_FP32 ? 4
                                                                                    : 2);
   const double bytes = 2.0 * piece * g->num_kv_heads * batch * cache->page_size * max_pages;
-  if (st != MLA_OK || !out->cut || piece % kLine == 0 || bytes < kLarge ||
+  auto whole = [&](int64_t run) { return run % kLine == 0 && run >= kRun; };
+  if (st != MLA_OK || !out->cut || whole(piece) || bytes < kLarge ||
       cache->head_stride >= cache->row_stride)
     return st;
   int hg = 1;
-  while (hg < 4 && hg * piece % kLine != 0 && heads_fit(g, 2 * hg)) hg *= 2;
+  while (hg < 4 && !whole(hg * piece) && heads_fit(g, 2 * hg)) hg *= 2;
   return hg == 1 ? st : plan_for(g, batch, cache->page_size, max_pages, hg, out);
 }
 

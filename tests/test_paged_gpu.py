@@ -464,7 +464,8 @@ def test_decode_matches_oracle(lens, H, Hk, D, page, dtype, cache, by_head, wind
 @pytest.mark.parametrize("lens,H,Hk,D,page,cache,window", [
     (EDGES, 8, 4, 80, 16, BF16, 0), (EDGES, 8, 8, 40, 16, BF16, 0), (EDGES, 4, 2, 96, 7, BF16, 33),
     (EDGES, 12, 4, 112, 64, BF16, 0), (EDGES, 6, 2, 80, 16, BF16, 0), (EDGES, 3, 3, 80, 16, BF16, 0),
-    (EDGES, 8, 4, 64, 16, E4M3, 0), (EDGES, 36, 4, 96, 24, E4M3, 0), (EDGES, 4, 4, 16, 16, E4M3, 20),
+    (EDGES, 8, 4, 64, 16, E4M3, 0), (EDGES, 16, 2, 128, 16, E4M3, 0), (EDGES, 8, 2, 64, 8, BF16, 9),
+    (EDGES, 36, 4, 96, 24, E4M3, 0), (EDGES, 4, 4, 16, 16, E4M3, 20),
     ([700, 5, 2000, 0], 36, 4, 200, 16, BF16, 0), ([700, 5, 2000, 0], 36, 4, 168, 16, BF16, 0),
     ([700, 5, 2000, 0], 8, 4, 192, 16, E4M3, 0), ([700, 5, 2000, 0], 72, 4, 208, 16, E4M3, 0),
     ([9000, 1, 4000], 8, 4, 8, 16, BF16, 0), ([30, 0, 64, 7] * 90, 8, 4, 80, 16, BF16, 0),
