@@ -14,8 +14,9 @@
 // are three trips to memory in a row), the merge and the join; T = 131072 49 us,
 // 5.5 TB/s; e4m3, 64 sequences with groups of 8 168 us, 5.8 TB/s.
 //
-// Work.  The cache rows a call reads form segments (sequence, key/value head,
-// row tile of up to ROWS query heads), each a run of tiles of TILE positions.
+// Work.  The cache rows a call reads form segments (sequence, key/value head or
+// a few neighbouring ones, row tile of up to ROWS query heads of each), each a
+// run of tiles of positions.
 // All tiles, in that order, are dealt out in equal contiguous shares to as
 // many CTAs as are resident at once, whatever the lengths, so a batch of
 // ragged sequences and one long sequence load the machine alike.  The lengths
@@ -23,8 +24,8 @@
 // several shares leaves its parts (unnormalised sums, m, sum of weights) in
 // the workspace, at most two per CTA, and a second kernel joins them in order.
 //
-// Loads.  Each warp owns a quarter of every tile and a ring of STAGES of its
-// quarters in shared memory, filled by 16-byte asynchronous copies (any page
+// Loads.  Each warp owns a part of every tile and a ring of STAGES of its
+// parts in shared memory, filled by 16-byte asynchronous copies (any page
 // size, any strides; rows beyond the sequence are zero-filled without being
 // read).  The warps share nothing until a segment ends, so there is no
 // barrier in the loop, and the copies run on across segments.  The page ids
