@@ -426,7 +426,8 @@ mla_status_t mla_indexer_select(const float* q, const float* pooled, int64_t poo
  *          table) and for a row whose page id is outside [0, num_pages)
  *          (recorded as code 300 in the status word); both -1 for rows at or
  *          beyond row_start[batch].
- *          Rows beyond max_rows are dropped.
+ *          Rows beyond max_rows are dropped (cache_lens_out counts them all the
+ *          same, so max_rows must cover the step).
  *  free_span_out  device [2]: {free_span[0] + pages taken, free_span[1]}
  *  missing_out  device [1]: pages asked for that the list did not have (0:
  *          every sequence got its pages)
