@@ -45,7 +45,6 @@ namespace {
 // place by a binary search.  New pages are read from the free list by
 // position, never from the table that this launch writes.
 
-constexpr int kRowsPerThread = 4;
 constexpr int kEntries = 4096;  // sums kept in shared memory
 
 struct PageStepParams {
@@ -94,6 +93,11 @@ struct Sequence {
   }
 };
 
+__device__ __forceinline__ void load4(const int32_t* p, int (&x)[4]) {
+  const int4 v = *reinterpret_cast<const int4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+
 // The last of n ascending sums that is at or before x.
 __device__ __forceinline__ int find_entry(const int* sums, int n, int x) {
   int a = 0, z = n;
@@ -104,7 +108,8 @@ __device__ __forceinline__ int find_entry(const int* sums, int n, int x) {
   return a;
 }
 
-template <int THREADS>
+// ROWS: consecutive rows a thread places at a time.
+template <int THREADS, int ROWS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     page_step_kernel(const PageStepParams p) {
   // before each entry's sequences (rows saturate: no row that is wanted lies there)
@@ -123,11 +128,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   int b = b0;
   if (per % 4 == 0) {
     for (; b + 4 <= b1; b += 4) {
-      const int4 k4 = *reinterpret_cast<const int4*>(p.kept + b);
-      const int4 f4 = *reinterpret_cast<const int4*>(p.fresh + b);
-      const int4 h4 = *reinterpret_cast<const int4*>(p.held + b);
-      const int k[4] = {k4.x, k4.y, k4.z, k4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w},
-                h[4] = {h4.x, h4.y, h4.z, h4.w};
+      int k[4], f[4], h[4];
+      load4(p.kept + b, k);
+      load4(p.fresh + b, f);
+      load4(p.held + b, h);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         q.set(p, k[i], f[i], h[i]);
@@ -166,11 +170,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   }
   {
     Sums base = {sum.rows - mine.rows, sum.pages - mine.pages};
-    for (int b = b0; b < b1; b += size) {
-      s_row[b / size] = sat32(base.rows);
-      s_page[b / size] = base.pages;
+    int e = b0 / size, b = b0;
+    if (size == 1 && per % 4 == 0) {
+      for (; b + 4 <= b1; b += 4) {
+        int k[4], f[4], h[4];
+        load4(p.kept + b, k);
+        load4(p.fresh + b, f);
+        load4(p.held + b, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i, ++e) {
+          s_row[e] = sat32(base.rows);
+          s_page[e] = base.pages;
+          q.set(p, k[i], f[i], h[i]);
+          base.rows += q.fresh;
+          base.pages += q.grow;
+        }
+      }
+    }
+    for (; b < b1; b += size, ++e) {
+      s_row[e] = sat32(base.rows);
+      s_page[e] = base.pages;
+      if (per == 1) break;
       for (int i = 0; i < size && b + i < b1; ++i) {
-        if (per == 1) break;
         q.load(p, b + i);
         base.rows += q.fresh;
         base.pages += q.grow;
@@ -183,20 +204,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int end = min(max(span1, first), p.free_capacity);
   const int have = end - first;
 
-  // ---- this CTA's rows, four consecutive ones a thread
+  // ---- this CTA's rows
   const long long r0 = (long long)blockIdx.x * p.rows_per_cta;
   const long long r1 = min(r0 + p.rows_per_cta, (long long)p.max_rows);
-  for (long long g = r0 + tid * kRowsPerThread; g < r1; g += THREADS * kRowsPerThread) {
-    int pos4[kRowsPerThread], id4[kRowsPerThread], off4[kRowsPerThread];
-    const int live = (int)max(0ll, min((long long)kRowsPerThread, all.rows - g));
+  for (long long g = r0 + tid * ROWS; g < r1; g += THREADS * ROWS) {
+    int pos_of[ROWS], id_of[ROWS], off_of[ROWS];
+    const int live = (int)max(0ll, min((long long)ROWS, all.rows - g));
     int b = -1, owned = 0;
     long long rows = 0;  // the sums before sequence b
     int pages = 0;
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      pos4[i] = -1;
-      id4[i] = -1;
-      off4[i] = -1;  // no page
+    for (int i = 0; i < ROWS; ++i) {
+      pos_of[i] = -1;
+      id_of[i] = -1;
+      off_of[i] = -1;  // no page
       if (i >= live) continue;
       if (b < 0) {
         const int e = find_entry(s_row, entries, (int)g);
@@ -213,35 +234,37 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         owned = q.held + q.got(have, pages);
       }
       const long long pos = q.kept + (g + i - rows);
-      pos4[i] = sat32(pos);
+      pos_of[i] = sat32(pos);
       if (pos >= q.total) continue;
       const int page = p.div((int)pos);
       if (page < owned) {
-        off4[i] = (int)pos - page * p.page;
-        id4[i] = page < q.held ? p.table[(long long)b * p.width + page]
+        off_of[i] = (int)pos - page * p.page;
+        id_of[i] = page < q.held ? p.table[(long long)b * p.width + page]
                                : p.free_pages[first + pages + (page - q.held)];
       }
     }
-    long long slot4[kRowsPerThread];
+    long long slot_of[ROWS];
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      slot4[i] = -1;
-      if (off4[i] < 0) continue;
-      if (id4[i] >= 0 && id4[i] < p.num_pages) slot4[i] = (long long)id4[i] * p.page + off4[i];
+    for (int i = 0; i < ROWS; ++i) {
+      slot_of[i] = -1;
+      if (off_of[i] < 0) continue;
+      if (id_of[i] >= 0 && id_of[i] < p.num_pages) slot_of[i] = (long long)id_of[i] * p.page + off_of[i];
       else atomicCAS(&g_paged_status, 0, kBadPageSite);
     }
-    if (g + kRowsPerThread <= r1) {
-      *reinterpret_cast<int4*>(p.positions + g) = make_int4(pos4[0], pos4[1], pos4[2], pos4[3]);
-      longlong2* d = reinterpret_cast<longlong2*>(p.slots + g);
-      d[0] = make_longlong2(slot4[0], slot4[1]);
-      d[1] = make_longlong2(slot4[2], slot4[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i) {
-        if (g + i >= r1) continue;
-        p.positions[g + i] = pos4[i];
-        p.slots[g + i] = slot4[i];
+    if constexpr (ROWS == 4) {
+      if (g + ROWS <= r1) {
+        *reinterpret_cast<int4*>(p.positions + g) = make_int4(pos_of[0], pos_of[1], pos_of[2], pos_of[3]);
+        longlong2* d = reinterpret_cast<longlong2*>(p.slots + g);
+        d[0] = make_longlong2(slot_of[0], slot_of[1]);
+        d[1] = make_longlong2(slot_of[2], slot_of[3]);
+        continue;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (g + i >= r1) continue;
+      p.positions[g + i] = pos_of[i];
+      p.slots[g + i] = slot_of[i];
     }
   }
 
@@ -761,11 +784,14 @@ extern "C" mla_status_t mla_page_step(
   p.capacity = (int)((int64_t)max_pages_per_seq * page_size > INT_MAX
                          ? INT_MAX
                          : (int64_t)max_pages_per_seq * page_size);
-  // A small batch takes 256 threads, whose barriers are cheap (32 sequences: 4.2
-  // us in a graph, 6.4 with 1024), a larger one 1024, so that fewer CTAs make
-  // the sums of all sequences (4096: 13 us, 26 with 256).
-  const int threads = batch <= 256 ? 256 : 1024;
-  const int64_t per_pass = (int64_t)threads * kRowsPerThread;
+  // A small batch takes 256 threads, whose barriers are cheap, and a row a
+  // thread (32 sequences: 3.1 us in a graph, 4.1 with four rows a thread, 6.4
+  // with 1024 threads); a larger one 1024 threads, so that fewer CTAs make the
+  // sums of all sequences, and four rows (4096 sequences, 1.07 M rows: 12.2 us,
+  // 16.5 with one row a thread, 26 with 256 threads).
+  const bool small = batch <= 256;
+  const int threads = small ? 256 : 1024;
+  const int64_t per_pass = (int64_t)threads * (small ? 1 : 4);
   int64_t ctas = ((int64_t)max_rows + per_pass - 1) / per_pass;
   if (ctas < batch / threads) ctas = batch / threads;
   const int64_t most = (int64_t)device_sm_count() * (1024 / threads);
@@ -775,7 +801,7 @@ extern "C" mla_status_t mla_page_step(
   p.rows_per_cta = (int)((share + 3) / 4 * 4);
   const cudaStream_t s = (cudaStream_t)stream;
   KernelTimer kt("page_step", s);
-  return launched(launch_dependent(threads == 256 ? page_step_kernel<256> : page_step_kernel<1024>,
+  return launched(launch_dependent(small ? page_step_kernel<256, 1> : page_step_kernel<1024, 4>,
                                    dim3((unsigned)ctas), dim3(threads), 0, s, p));
 }
 
