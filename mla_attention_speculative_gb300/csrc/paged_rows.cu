@@ -270,8 +270,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 
   // ---- new table entries
   const int taken = min(all.pages, have);
-  for (int i = blockIdx.x * THREADS + tid; i < taken; i += gridDim.x * THREADS) {
-    const int e = find_entry(s_page, entries, i);
+  // (unsigned: a grid's stride beyond `taken`, which may be close to 2^31)
+  for (uint32_t at_free = blockIdx.x * THREADS + tid; at_free < (uint32_t)taken;
+       at_free += gridDim.x * THREADS) {
+    const int i = (int)at_free, e = find_entry(s_page, entries, i);
     int b = e * size;
     int at = s_page[e];
     q.load(p, b);

@@ -1,0 +1,44 @@
+"""The paged-step kernels at the ends of what their documentation allows: the
+largest tables, values and scales that are not numbers, scores beyond what the
+weights' type holds, long runs of idle slots, streams, and a draft loop whose
+slots are not all in use.  Tolerances as in test_paged_gpu."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as P
+from mla_attention_speculative_gb300 import binding as B
+from mla_attention_speculative_gb300 import build_lib
+from test_paged_gpu import BF16, DEV, E4M3, FP32, i32, npy  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build_lib.build()
+    B.lib()
+    yield
+    torch.cuda.synchronize()
+    B.mla_device_status()
+
+
+# ------------------------------------------------------------------------------ page step
+
+def test_page_step_largest_table():
+    """A table of 2^31 - 2^15 pages, all taken in one step: the list position of the last
+    pages plus a grid's stride passes 2^31."""
+    batch, width = 65535, 32768
+    if torch.cuda.mem_get_info()[0] < 28 << 30:
+        pytest.skip("needs 28 GB")
+    full = torch.full((batch,), width, dtype=torch.int32, device=DEV)
+    none = torch.zeros(batch, dtype=torch.int32, device=DEV)
+    table = torch.full((batch, width), -1, dtype=torch.int32, device=DEV)
+    free = torch.arange(batch * width, dtype=torch.int32, device=DEV)
+    out = B.mla_page_step(none, full, none, table, free, i32([0, batch * width]), 1, 2 ** 31 - 1, 0)
+    torch.cuda.synchronize()
+    assert out.missing.item() == 0 and out.free_span.tolist() == [batch * width] * 2
+    assert torch.equal(table.view(-1), free)
+    assert torch.equal(out.cache_lens, full) and torch.equal(out.held_pages, full)
+    assert out.row_start[-1].item() == batch * width
