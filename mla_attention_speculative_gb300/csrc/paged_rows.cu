@@ -879,7 +879,7 @@ extern "C" mla_status_t mla_append_latent(
   const int k = heads_per_thread(H, (int)block.y, rows), hpc = k * (int)block.y;
   const int warps = (int)(block.x * block.y) / 32;
   p.rows = rows;
-  p.kv_ctas = (rows + warps - 1) / warps;
+  p.kv_ctas = (int)(((int64_t)rows + warps - 1) / warps);
   p.head_ctas = (H + hpc - 1) / hpc;
   const int64_t ctas = p.kv_ctas + (no_q ? 0 : (int64_t)rows * p.head_ctas);
   if (ctas > INT_MAX) {

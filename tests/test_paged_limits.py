@@ -1,0 +1,29 @@
+"""Refusals of the paged-step entry points at the largest sizes (no GPU): like
+the other refusals they are turned down before any CUDA call is made, so the
+device pointers are fake and never dereferenced."""
+
+import ctypes
+
+import pytest
+import torch
+
+from mla_attention_speculative_gb300 import binding as B
+from mla_attention_speculative_gb300 import build_lib
+
+F = 0x100000
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build_lib.build()
+    yield
+
+
+def test_append_latent_counts_the_largest_rows():
+    # 2^31 - 1 rows of four heads take more thread blocks than a grid has
+    geom = B.make_geometry(H=4, r=512, n=128, v=128, rope=64, dtype=torch.bfloat16)
+    st = B.lib().mla_append_latent(
+        ctypes.byref(geom), F, 4 * 192, F, 576, F, ctypes.c_float(1e-6), F, 100, 1, F, F,
+        2 ** 31 - 1, F, F, F, F, 512, 64, 100, None)
+    assert st == B.MLA_ERR_UNSUPPORTED
+    assert "too many" in B.mla_last_error()
