@@ -598,12 +598,19 @@ def _one_device(**tensors) -> torch.device:
     return dev
 
 
+def _stream_object(handle: int, dev: torch.device):
+    """The PyTorch stream of a raw handle.  (ExternalStream would take 0 for no handle
+    and give some other stream.)"""
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else \
+        torch.cuda.default_stream(dev)
+
+
 def _allocating_on(stream, dev: torch.device):
     """Allocate for kernels of `stream` (a raw handle; None: the current one), so
     that freed memory is only reused behind them."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev))
+    return torch.cuda.stream(_stream_object(int(stream), dev))
 
 
 class _PreparedCall:
@@ -631,7 +638,7 @@ class _PreparedCall:
                       torch.cuda.current_stream(self._dev).cuda_stream)
         if stream not in self._streams:
             # the buffers made here must not be reused before this stream is done with them
-            s = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", self._dev))
+            s = _stream_object(int(stream), torch.device("cuda", self._dev))
             for t in self._made:
                 t.record_stream(s)
             self._streams.add(stream)

@@ -42,3 +42,21 @@ def test_page_step_largest_table():
     assert torch.equal(table.view(-1), free)
     assert torch.equal(out.cache_lens, full) and torch.equal(out.held_pages, full)
     assert out.row_start[-1].item() == batch * width
+
+
+# -------------------------------------------------------------------------------- streams
+
+def test_handle_zero_is_the_default_stream():
+    # a call on handle 0 allocates (and zeroes) on the stream that its kernel runs on
+    assert B._stream_object(0, torch.device(DEV, 0)).cuda_stream == 0
+    gen = torch.Generator(DEV).manual_seed(2)
+    k = torch.randn(3, 2, 64, generator=gen, device=DEV).to(BF16)
+    q = torch.randn(3, 4, 64, generator=gen, device=DEV).to(BF16)
+    kc, vc = (torch.zeros(2, 4, 2, 64, dtype=BF16, device=DEV) for _ in "kv")
+    pos, slots = i32([0, 4, 8]), torch.tensor([5, 1, 0], device=DEV)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        out = B.mla_append_kv(q, k, k, None, pos, slots, kc, vc, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, q)
