@@ -637,10 +637,7 @@ class _PreparedCall:
             stream = (_raw_stream(self._dev) if _raw_stream is not None else
                       torch.cuda.current_stream(self._dev).cuda_stream)
         if stream not in self._streams:
-            # the buffers made here must not be reused before this stream is done with them
-            s = _stream_object(int(stream), torch.device("cuda", self._dev))
-            for t in self._made:
-                t.record_stream(s)
+            self._made_for(int(stream))
             self._streams.add(stream)
         if self._one_device or torch.cuda.current_device() == self._dev:
             st = self._fn(*self._args, stream)
@@ -649,6 +646,23 @@ class _PreparedCall:
                 st = self._fn(*self._args, stream)
         if st != MLA_OK:
             _check(st, self._name)
+
+
+    def _made_for(self, stream: int) -> None:
+        """Before the first run on another stream than the one the buffers made here
+        belong to: what that one still does with them (zeros, or earlier work on the
+        same memory) comes first, and they are not reused before this stream is done
+        with them.  (A capture cannot wait for work outside it; it begins behind a
+        synchronisation.)"""
+        if not self._made:
+            return
+        dev = torch.device("cuda", self._dev)
+        s = _stream_object(stream, dev)
+        with torch.cuda.stream(s):
+            if not torch.cuda.is_current_stream_capturing():
+                s.wait_stream(_stream_object(self._home, dev))
+        for t in self._made:
+            t.record_stream(s)
 
 
 class PageStep(NamedTuple):

@@ -46,6 +46,36 @@ def test_page_step_largest_table():
 
 # -------------------------------------------------------------------------------- streams
 
+def _busy():
+    """Tens of milliseconds of copies on the current stream."""
+    a = torch.empty(1 << 30, dtype=torch.uint8, device=DEV)
+    b = torch.empty_like(a)
+    torch.cuda.synchronize()
+    for _ in range(100):
+        b.copy_(a)
+
+
+def test_outputs_made_on_one_stream_and_run_on_another():
+    # what the constructor's stream still does with the buffers comes before the run
+    gen = torch.Generator(DEV).manual_seed(1)
+    q = torch.randn(3, 4, 192, generator=gen, device=DEV).to(BF16)
+    kv = torch.randn(3, 576, generator=gen, device=DEV).to(BF16)
+    cs = torch.cat([torch.ones(9, 32, device=DEV), torch.zeros(9, 32, device=DEV)], 1)
+    pos, slots = i32([0, 4, 8]), torch.tensor([5, 1, 0], device=DEV)
+    ckv, kr = (torch.zeros(8, w, dtype=BF16, device=DEV) for w in (512, 64))
+    kc, vc = (torch.zeros(2, 4, 2, 192, dtype=BF16, device=DEV) for _ in "kv")
+    other = torch.cuda.Stream()
+    for _ in range(2):
+        _busy()
+        lat = B.PreparedAppendLatent(q, kv, cs, pos, slots, ckv, kr)
+        put = B.PreparedAppendKV(q, q[:, :2], q[:, 2:], None, pos, slots, kc, vc)
+        lat.run(other.cuda_stream)
+        put.run(other.cuda_stream)
+        torch.cuda.synchronize()
+        assert torch.equal(lat.q_nope, q[..., :128]) and torch.equal(lat.q_rope, q[..., 128:])
+        assert torch.equal(put.q_out, q)
+
+
 def test_handle_zero_is_the_default_stream():
     # a call on handle 0 allocates (and zeroes) on the stream that its kernel runs on
     assert B._stream_object(0, torch.device(DEV, 0)).cuda_stream == 0
