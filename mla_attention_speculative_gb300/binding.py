@@ -620,6 +620,9 @@ class _PreparedCall:
         self._name = name
         self._fn = getattr(lib(), name)
         types = _SIGS[name][1]
+        for t, a in zip(types, args):   # (ctypes would keep the low 32 bits)
+            if t is _I32 and not -2 ** 31 <= a < 2 ** 31:
+                raise ValueError(f"{name}: {a} does not fit a 32-bit integer")
         # plain numbers become ctypes values now, so a run converts nothing
         self._args = [types[i](a) if isinstance(a, (int, float)) else a
                       for i, a in enumerate(args)]

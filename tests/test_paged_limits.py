@@ -27,3 +27,12 @@ def test_append_latent_counts_the_largest_rows():
         2 ** 31 - 1, F, F, F, F, 512, 64, 100, None)
     assert st == B.MLA_ERR_UNSUPPORTED
     assert "too many" in B.mla_last_error()
+
+
+@pytest.mark.parametrize("at,value", [(8, 2 ** 32 + 5), (8, 2 ** 31), (7, -2 ** 31 - 1)])
+def test_numbers_beyond_32_bits_are_refused(at, value):
+    # (a window of 2^32 + 5 is not one of 5)
+    args = [F, F, 64, F, F, 3, F, 8, 0, F, F, F, 0]
+    args[at] = value
+    with pytest.raises(ValueError, match="32-bit"):
+        B._PreparedCall()._prepare("mla_decode_attention", args, torch.device("cuda", 0), ())
