@@ -397,7 +397,8 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
       } else {
         if constexpr (KIND == kE4m3) {
           // (a negative key scale turns the queries round, so that a score's scale is
-          // positive; a zero one leaves it tiny)
+          // positive; a zero one leaves it tiny; one that is no finite number makes
+          // every score NaN)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float top = 0.f;
@@ -424,7 +425,8 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
                 qf[mt][nt][i] = *reinterpret_cast<const uint32_t*>(&h);
               }
             // lanes of row r know 2^e of head r; a score's columns are heads 2 quad + {0, 1}
-            const float mine_sc = fmaxf(p.scale_log2 * fabsf(ks) * up, 1e-37f);
+            const float score = p.scale_log2 * fabsf(ks) * up + (ks - ks);
+            const float mine_sc = score < 1e-37f ? 1e-37f : score;
             sc[2 * nt] = __shfl_sync(~0u, mine_sc, (2 * quad) * 4);
             sc[2 * nt + 1] = __shfl_sync(~0u, mine_sc, (2 * quad + 1) * 4);
           }

@@ -10,7 +10,7 @@ import torch
 from oracle import paged as P
 from mla_attention_speculative_gb300 import binding as B
 from mla_attention_speculative_gb300 import build_lib
-from test_paged_gpu import BF16, DEV, E4M3, FP32, i32, npy  # noqa: F401
+from test_paged_gpu import BF16, DEV, E4M3, FP32, _decode_case, i32, npy  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,23 @@ def test_handle_zero_is_the_default_stream():
         out = B.mla_append_kv(q, k, k, None, pos, slots, kc, vc, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out, q)
+
+
+# ----------------------------------------------------------------------- decode attention
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("lens", [[300, 41, 1, 0], [9000]])
+def test_decode_key_scale_that_is_no_number(lens, scale):
+    c = _decode_case(lens, 9, 3, 64, 16, BF16, E4M3, seed=15)
+    want, want_lse = B.mla_decode_attention(**c, return_lse=True)
+    c["k_scale"][1] = scale
+    out, lse = B.mla_decode_attention(**c, return_lse=True)
+    torch.cuda.synchronize()
+    others = [0, 1, 2, 6, 7, 8]
+    assert torch.equal(out[:, others], want[:, others])
+    assert torch.equal(lse[:, others], want_lse[:, others])
+    for b, t in enumerate(lens):
+        if t:
+            assert torch.isnan(out[b, 3:6]).all() and torch.isnan(lse[b, 3:6]).all()
+        else:
+            assert not out[b].any() and (lse[b] == float("-inf")).all()
