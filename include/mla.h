@@ -550,7 +550,8 @@ mla_status_t mla_decode_workspace_bytes(const mla_kv_geometry_t* geom, int32_t b
  * A sequence with T_b <= 0 (an idle slot) gets zeros and lse = -inf, and so
  * does a head whose scores are all -inf.  T_b beyond the table's
  * max_pages_per_seq * page_size rows (2^31 - 1024 at most) counts as that
- * many.  An infinite value among the v rows seen may give NaN.
+ * many.  An infinite value among the v rows seen gives that infinity (NaN beside
+ * its opposite, or under a weight below 2^-100 of the largest).
  *
  *  q       device [batch, num_heads, head_dim], q_row_stride elements between
  *          sequences, heads dense

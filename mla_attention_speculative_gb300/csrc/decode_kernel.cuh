@@ -41,9 +41,11 @@
 // it waits for DRAM.
 //
 // Roundings.  bf16: the products are exact in fp32, and the weights enter the
-// second product as two bf16 parts, hi + lo (2^-16 relative), so that the
-// output's own rounding is the only one that shows (an infinite v therefore
-// gives NaN).  e4m3: keys and values become fp16 (exact), queries fp16 scaled
+// second product as two bf16 parts, hi + lo (2^-15 relative), so that the
+// output's own rounding is the only one that shows.  Both parts are above zero:
+// an infinite v gives infinity and not the difference of two (hi rounded to
+// nearest would halve the error and leave lo zero or negative half the time).
+// e4m3: keys and values become fp16 (exact), queries fp16 scaled
 // by a power of two per head (exact down to 2^-24 of the head's largest
 // element), weights fp16 scaled by 2^15, so that even many weights far below
 // the largest keep their sum.
@@ -548,10 +550,15 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
                 l[2 * nt + e] += w[e];
               }
               if constexpr (KIND == kBf16) {
-                const uint32_t h = pack_bf16(w[0], w[1]);
+                // (cut, not rounded, so that no second part is below zero; and none of a
+                // weight is zero)
+                const uint32_t h =
+                    __byte_perm(__float_as_uint(w[0]), __float_as_uint(w[1]), 0x7632);
+                const float low[2] = {
+                    fmaxf(w[0] - __uint_as_float(h << 16), w[0] * 0x1p-20f),
+                    fmaxf(w[1] - __uint_as_float(h & 0xFFFF0000u), w[1] * 0x1p-20f)};
                 hi[u][nt][half] = movmatrix_trans(h);
-                lo[u][nt][half] = movmatrix_trans(pack_bf16(
-                    w[0] - __uint_as_float(h << 16), w[1] - __uint_as_float(h & 0xFFFF0000u)));
+                lo[u][nt][half] = movmatrix_trans(pack_bf16(low[0], low[1]));
               } else {
                 const __half2 h = __floats2half2_rn(w[0], w[1]);
                 hi[u][nt][half] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h));

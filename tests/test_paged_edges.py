@@ -110,3 +110,30 @@ def test_decode_key_scale_that_is_no_number(lens, scale):
             assert torch.isnan(out[b, 3:6]).all() and torch.isnan(lse[b, 3:6]).all()
         else:
             assert not out[b].any() and (lse[b] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("dtype,lens,H,Hk,D", [
+    (BF16, [300, 41], 4, 1, 64), (FP32, [300, 41], 4, 1, 64), (BF16, [700, 20000], 32, 2, 128),
+    (BF16, [300, 41], 12, 1, 256)])
+def test_decode_infinite_values(dtype, lens, H, Hk, D):
+    c = _decode_case(lens, H, Hk, D, 16, dtype, dtype, seed=15)
+    want = B.mla_decode_attention(**c)
+    inf, group = float("inf"), H // Hk
+    put = {0: {3: [(5, inf)], 9: [(7, -inf)], 33: [(2, inf), (8, inf)], 20: [(8, inf), (9, -inf)]},
+           1: {0: [(40, inf)], 1: [(0, -inf)], 2: [(31, inf)], 3: [(32, -inf)]}}
+    for b, cols in put.items():
+        for d, values in cols.items():
+            for t, x in values:
+                c["v_cache"][c["page_table"][b, t // 16], t % 16, 0, d] = x
+    out = B.mla_decode_attention(**c)
+    torch.cuda.synchronize()
+    for b, cols in put.items():
+        for d in range(D):
+            got = out[b, :group, d]
+            if d not in cols:
+                assert torch.equal(got, want[b, :group, d])
+            elif len({x for _, x in cols[d]}) == 2:
+                assert torch.isnan(got).all()
+            else:
+                assert (got == cols[d][0][1]).all(), (b, d, got)
+    assert torch.equal(out[:, group:], want[:, group:])
