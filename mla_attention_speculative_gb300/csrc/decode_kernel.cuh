@@ -531,10 +531,9 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
             }
           }
         }
-        float less[2 * NT];
+        float base[2 * NT];
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i)
-          less[i] = (KIND == kE4m3 ? kShift : 0.f) - (m[i] == -INFINITY ? 0.f : m[i]);
+        for (int i = 0; i < 2 * NT; ++i) base[i] = m[i] == -INFINITY ? 0.f : m[i];
         uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
@@ -545,8 +544,12 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
               float w[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                w[e] = ex2(fmaf(s[u][nt][2 * half + e], sc[KIND == kE4m3 ? 2 * nt + e : 0],
-                                less[2 * nt + e]));
+                // (the product rounded as the maximum was, so that no difference is above
+                // zero: from 2^23 on an exact one would be, by enough to leave fp16)
+                const float x = __fadd_rn(
+                    __fmul_rn(s[u][nt][2 * half + e], sc[KIND == kE4m3 ? 2 * nt + e : 0]),
+                    -base[2 * nt + e]);
+                w[e] = ex2(KIND == kE4m3 ? x + kShift : x);
                 l[2 * nt + e] += w[e];
               }
               if constexpr (KIND == kBf16) {

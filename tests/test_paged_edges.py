@@ -10,7 +10,7 @@ import torch
 from oracle import paged as P
 from mla_attention_speculative_gb300 import binding as B
 from mla_attention_speculative_gb300 import build_lib
-from test_paged_gpu import BF16, DEV, E4M3, FP32, _decode_case, i32, npy  # noqa: F401
+from test_paged_gpu import BF16, DEV, E4M3, FP32, _check_decode, _decode_case, i32, near, npy
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +137,37 @@ def test_decode_infinite_values(dtype, lens, H, Hk, D):
             else:
                 assert (got == cols[d][0][1]).all(), (b, d, got)
     assert torch.equal(out[:, group:], want[:, group:])
+
+
+@pytest.mark.parametrize("power", [0, 12, 17, 18, 20, 22, 24, 28, 33, 60])
+@pytest.mark.parametrize("cache", [BF16, E4M3, FP32])
+def test_decode_scores_of_any_size(cache, power):
+    # finite scores give finite results, and a key above all others its value
+    dtype = FP32 if cache == FP32 else BF16
+    lens, D = [300, 41, 3000], 64
+    c = _decode_case(lens, 8, 2, D, 16, dtype, cache, seed=15)
+    scale = 2.0 ** power
+    out, lse = B.mla_decode_attention(**c, scale=scale, return_lse=True)
+    torch.cuda.synchronize()
+    _check_decode(c, out, lse, scale=scale)
+    # every other score is at most half of this key's
+    c["q"].fill_(1.0)
+    k = torch.nan_to_num(c["k_cache"].float(), nan=0.0).clamp(-2.0, 2.0)
+    at = [17, 40, 2999]
+    for b, t in enumerate(at):
+        k[c["page_table"][b, t // 16], t % 16] = 4.0
+    c["k_cache"] = k.to(cache)
+    if cache == E4M3:
+        c["k_scale"].fill_(0.5)
+    out, lse = B.mla_decode_attention(**c, scale=scale, return_lse=True)
+    torch.cuda.synchronize()
+    for b, t in enumerate(at):
+        v = npy(c["v_cache"][c["page_table"][b, t // 16], t % 16])
+        top = 4.0 * D * scale
+        if cache == E4M3:
+            v, top = v * npy(c["v_scale"])[:, None], top * 0.5
+        # (the others weigh less than 3000 e^-64 of it; fp32: two roundings of the result)
+        u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -22
+        v = np.repeat(v, 4, 0)
+        near(out[b], v, np.abs(v) * (u + 2.0 ** -20) + 1e-20, f"{power} {b}")
+        assert (np.abs(npy(lse[b]) - top) <= top * 2.0 ** -21).all()
