@@ -78,7 +78,7 @@ struct Span {  // the positions a sequence sees, and its tiles
   int lo, T, n;
 };
 
-// TILE: positions of a tile, 0: as the call says.
+// TILE: positions of a tile, 0: as the call says.  (A length above 0 has tiles.)
 template <int TILE>
 __device__ __forceinline__ Span span_of(const Params& p, int b) {
   Span s;
@@ -92,6 +92,39 @@ __device__ __forceinline__ Span span_of(const Params& p, int b) {
 // What a sequence's segments count for, each, when the work is dealt out.
 __device__ __forceinline__ int cost_of(const Span& s) { return s.n > 0 ? s.n + kSegmentCost : 0; }
 
+// Which blocks of `per` sequences have one with tiles, a bit each.
+struct LiveBlocks {
+  const uint32_t* words;
+  int count, per;
+};
+
+// The first sequence behind b with tiles (p.batch: none).  The whole warp calls
+// it.  Blocks without one are passed over by their bits, the sequences of a block
+// 32 at a time: one by one, a run of 4094 idle slots between two sequences of
+// 20064 and 25000 positions cost the CTA whose share spans it 450 us, and the
+// call with it (481 us, now 27).
+__device__ __forceinline__ int next_live(const Params& p, int b, const LiveBlocks& blocks) {
+  const int lane = threadIdx.x & 31;
+  int block = b / blocks.per;
+  for (int from = b + 1;;) {
+    const int to = min(p.batch, (block + 1) * blocks.per);
+    for (; from < to; from += 32) {
+      const uint32_t live =
+          __ballot_sync(~0u, from + lane < to && p.lens[from + lane] > 0);
+      if (live != 0) return from + __ffs(live) - 1;
+    }
+    int w = (block + 1) >> 5;
+    if (w >= blocks.count) return p.batch;
+    uint32_t bits = blocks.words[w] & (~0u << ((block + 1) & 31));
+    while (bits == 0) {
+      if (++w == blocks.count) return p.batch;
+      bits = blocks.words[w];
+    }
+    block = w * 32 + __ffs(bits) - 1;
+    from = block * blocks.per;
+  }
+}
+
 // A place in the work: tile j of segment (b, kvg, rt), and its place t in the
 // list in which a segment's tiles come behind kSegmentCost places without one.
 template <int TILE>
@@ -100,7 +133,7 @@ struct Cursor {
   long long t;
   Span s;
   // To the next tile; beyond `end` the place alone is right.
-  __device__ __forceinline__ void next(const Params& p, long long end) {
+  __device__ __forceinline__ void next(const Params& p, long long end, const LiveBlocks& blocks) {
     ++t;
     if (++j < s.n) return;
     t += kSegmentCost;
@@ -110,9 +143,16 @@ struct Cursor {
     rt = 0;
     if (++kvg < p.kv_groups) return;
     kvg = 0;
-    do {
-      s = span_of<TILE>(p, ++b);
-    } while (s.n == 0);
+    if (++b < p.batch) {
+      s = span_of<TILE>(p, b);
+      if (s.n > 0) return;
+      b = next_live(p, b, blocks);
+    }
+    if (b >= p.batch) {  // (lengths that another kernel changes meanwhile)
+      t = end;
+      return;
+    }
+    s = span_of<TILE>(p, b);
   }
 };
 
@@ -167,6 +207,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
   float* const s_q = reinterpret_cast<float*>(smem + S::RING + S::STATS);
   float* const s_w = reinterpret_cast<float*>(smem + S::RING + S::STATS + S::QTILE);
   __shared__ long long s_sum[NW];
+  __shared__ uint32_t s_live[NW];
   __shared__ long long s_rem;
   __shared__ int s_b;
 
@@ -199,6 +240,9 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     if (lane >= o) upto += x;
   }
   if (lane == 31) s_sum[warp] = upto;
+  const uint32_t live_here = __ballot_sync(~0u, mine > 0);
+  if (lane == 0) s_live[warp] = live_here;
+  const LiveBlocks blocks = {s_live, NW, per};
   __syncthreads();
   long long total = 0;
 #pragma unroll
@@ -350,7 +394,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     for (int s = 0; s < STAGES; ++s) {
       first[s].off = -1;
       first[s].id = 0;
-      if (s > 0 && lc.t < t1) lc.next(p, t1);
+      if (s > 0 && lc.t < t1) lc.next(p, t1, blocks);
       if (lc.t < t1) first[s] = locate();
     }
 #pragma unroll
@@ -368,7 +412,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     __syncwarp();
     if (lc.t < t1) {
       copy(ahead, stage == 0 ? STAGES - 1 : stage - 1);
-      lc.next(p, t1);
+      lc.next(p, t1, blocks);
       if (lc.t < t1) ahead = locate();
     }
     cp_async_commit();
@@ -698,7 +742,7 @@ __global__ void __launch_bounds__((Shape<DP, KIND, NT>::THREADS), (Shape<DP, KIN
     // ---- the segment ends here, or this share does
     const bool ends = cc.j == cc.s.n - 1;
     const Cursor<TILE> at = cc;
-    cc.next(p, t1);
+    cc.next(p, t1, blocks);
     const int used = stage;
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     if (ends || cc.t >= t1) {

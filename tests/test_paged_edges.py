@@ -171,3 +171,23 @@ def test_decode_scores_of_any_size(cache, power):
         v = np.repeat(v, 4, 0)
         near(out[b], v, np.abs(v) * (u + 2.0 ** -20) + 1e-20, f"{power} {b}")
         assert (np.abs(npy(lse[b]) - top) <= top * 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("batch,lens", [
+    (1024, {0: 700, 1023: 500}), (4096, {0: 40, 4095: 3}), (65535, {0: 100, 65534: 70}),
+    (2048, {0: 20064, 2047: 25000}), (4500, {31: 5, 32: 9, 64: 1, 97: 33, 4480: 2}), (300, {299: 1}), (300, {0: 1})])
+@pytest.mark.parametrize("cache,H,Hk,D", [(BF16, 4, 2, 128), (FP32, 2, 1, 16)])
+def test_decode_long_runs_of_idle_slots(batch, lens, cache, H, Hk, D):
+    all_lens = [0] * batch
+    for b, t in lens.items():
+        all_lens[b] = t
+    c = _decode_case(all_lens, H, Hk, D, 16, cache, cache, seed=batch)
+    out, lse = B.mla_decode_attention(**c, return_lse=True)
+    torch.cuda.synchronize()
+    rows = sorted(lens)
+    live = dict(c, q=c["q"][rows], cache_lens=c["cache_lens"][rows],
+                page_table=c["page_table"][rows].contiguous())
+    _check_decode(live, out[rows], lse[rows])
+    rest = torch.ones(batch, dtype=torch.bool, device=DEV)
+    rest[rows] = False
+    assert not out[rest].any() and (lse[rest] == float("-inf")).all()
