@@ -191,3 +191,33 @@ def test_decode_long_runs_of_idle_slots(batch, lens, cache, H, Hk, D):
     rest = torch.ones(batch, dtype=torch.bool, device=DEV)
     rest[rows] = False
     assert not out[rest].any() and (lse[rest] == float("-inf")).all()
+
+
+def _graph_us(call, reps=20):
+    """Device time of one run among others in a captured graph, the least of ten replays."""
+    call.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(reps):
+            call.run()
+    best = float("inf")
+    for _ in range(10):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / reps)
+    return best
+
+
+def test_decode_idle_slots_between_live_ones_cost_little():
+    # (one by one they cost the thread block whose share spans them 0.1 us each)
+    def us(last):
+        lens = [0] * 4096
+        lens[0], lens[last] = 20064, 25000
+        c = _decode_case(lens, 8, 2, 128, 16, BF16, BF16, seed=1)
+        return _graph_us(B.PreparedDecodeAttention(**c))
+    apart, together = us(4095), us(1)
+    assert apart < 3 * together + 20, (apart, together)
