@@ -10,7 +10,8 @@ import torch
 from oracle import paged as P
 from mla_attention_speculative_gb300 import binding as B
 from mla_attention_speculative_gb300 import build_lib
-from test_paged_gpu import BF16, DEV, E4M3, FP32, _check_decode, _decode_case, i32, near, npy
+from test_paged_gpu import (BF16, DEV, E4M3, FP32, _check_decode, _check_page_step, _decode_case,
+                            _page_case, i32, near, npy)
 
 pytestmark = pytest.mark.gpu
 
@@ -22,6 +23,25 @@ def built():
     yield
     torch.cuda.synchronize()
     B.mla_device_status()
+
+
+def _graph_us(call, reps=20):
+    """Device time of one run among others in a captured graph, the least of ten replays."""
+    call.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(reps):
+            call.run()
+    best = float("inf")
+    for _ in range(10):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / reps)
+    return best
 
 
 # ------------------------------------------------------------------------------ page step
@@ -42,6 +62,33 @@ def test_page_step_largest_table():
     assert torch.equal(table.view(-1), free)
     assert torch.equal(out.cache_lens, full) and torch.equal(out.held_pages, full)
     assert out.row_start[-1].item() == batch * width
+
+
+@pytest.mark.parametrize("batch", [300, 1024, 4096, 5000, 65535])
+@pytest.mark.parametrize("live", [{0: 3, -1: 3}, {0: 1, 1: 1, -2: 5, -1: 2}, {-1: 7}, {5: 2, 40: 3}])
+def test_page_step_long_runs_of_idle_slots(batch, live):
+    c = _page_case(batch, batch, 4, 9, 0)
+    for b, n in live.items():
+        c["new"][b] = n
+    c["table"] = np.concatenate([c["table"], np.full((batch, 3), -1)], 1)
+    top = c["num_pages"]
+    c["free"], c["span"], c["num_pages"] = np.arange(top, top + 20), [1, 19], top + 20
+    _check_page_step(c, sum(live.values()) + 2)
+
+
+def test_page_step_idle_slots_between_live_ones_cost_little():
+    # (one by one they cost the thread whose rows span them 0.06 us each)
+    def us(last):
+        batch = 65535
+        kept = torch.full((batch,), 10, dtype=torch.int32, device=DEV)
+        new = torch.zeros(batch, dtype=torch.int32, device=DEV)
+        new[[0, last]] = 3
+        held = torch.ones(batch, dtype=torch.int32, device=DEV)
+        table = torch.arange(batch, dtype=torch.int32, device=DEV).view(batch, 1)
+        return _graph_us(B.PreparedPageStep(kept, new, held, table, i32([7]), i32([0, 1]), 16,
+                                            batch, 6), 5)
+    apart, together = us(65534), us(1)
+    assert apart < 3 * together + 20, (apart, together)
 
 
 # -------------------------------------------------------------------------------- streams
@@ -191,25 +238,6 @@ def test_decode_long_runs_of_idle_slots(batch, lens, cache, H, Hk, D):
     rest = torch.ones(batch, dtype=torch.bool, device=DEV)
     rest[rows] = False
     assert not out[rest].any() and (lse[rest] == float("-inf")).all()
-
-
-def _graph_us(call, reps=20):
-    """Device time of one run among others in a captured graph, the least of ten replays."""
-    call.run()
-    torch.cuda.synchronize()
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        for _ in range(reps):
-            call.run()
-    best = float("inf")
-    for _ in range(10):
-        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        a.record()
-        graph.replay()
-        b.record()
-        torch.cuda.synchronize()
-        best = min(best, a.elapsed_time(b) * 1e3 / reps)
-    return best
 
 
 def test_decode_idle_slots_between_live_ones_cost_little():
