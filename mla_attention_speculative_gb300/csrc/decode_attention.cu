@@ -312,7 +312,10 @@ mla_status_t make_plan(const mla_kv_geometry_t* g, const mla_kv_cache_t* cache, 
   const int64_t piece = (int64_t)g->head_dim * (g->cache_dtype == MLA_DTYPE_E4M3   ? 1
                                                 : g->cache_dtype == MLA_DTYPE_FP32 ? 4
                                                                                    : 2);
-  const double bytes = 2.0 * piece * g->num_kv_heads * batch * cache->page_size * max_pages;
+  // what the call can read: the tables' pages, and no more than the pool has
+  int64_t pages = (int64_t)batch * max_pages;
+  if (pages > cache->num_pages) pages = cache->num_pages;
+  const double bytes = 2.0 * piece * g->num_kv_heads * cache->page_size * pages;
   auto whole = [&](int64_t run) { return run % kLine == 0 && run >= kRun; };
   if (st != MLA_OK || !out->cut || whole(piece) || bytes < kLarge ||
       cache->head_stride >= cache->row_stride)

@@ -7,10 +7,9 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import paged as P
 from mla_attention_speculative_gb300 import binding as B
 from mla_attention_speculative_gb300 import build_lib
-from test_paged_gpu import (BF16, DEV, E4M3, FP32, _check_decode, _check_page_step, _decode_case,
+from test_paged_gpu import (BF16, DEV, E4M3, EDGES, FP32, _check_decode, _check_page_step, _decode_case,
                             _page_case, i32, near, npy)
 
 pytestmark = pytest.mark.gpu
@@ -249,3 +248,46 @@ def test_decode_idle_slots_between_live_ones_cost_little():
         return _graph_us(B.PreparedDecodeAttention(**c))
     apart, together = us(4095), us(1)
     assert apart < 3 * together + 20, (apart, together)
+
+
+@pytest.mark.parametrize("lens,H,Hk,D,page,cache,window", [
+    (EDGES, 8, 4, 80, 16, BF16, 0), (EDGES, 8, 8, 40, 16, BF16, 0), (EDGES, 4, 2, 96, 7, BF16, 33),
+    (EDGES, 12, 4, 112, 64, BF16, 0), (EDGES, 6, 2, 80, 16, BF16, 0), (EDGES, 3, 3, 80, 16, BF16, 0),
+    (EDGES, 8, 4, 64, 16, E4M3, 0), (EDGES, 16, 2, 128, 16, E4M3, 0), (EDGES, 8, 2, 64, 8, BF16, 9),
+    (EDGES, 36, 4, 96, 24, E4M3, 0), (EDGES, 4, 4, 16, 16, E4M3, 20),
+    ([700, 5, 2000, 0], 36, 4, 200, 16, BF16, 0), ([700, 5, 2000, 0], 36, 4, 168, 16, BF16, 0),
+    ([700, 5, 2000, 0], 8, 4, 192, 16, E4M3, 0), ([700, 5, 2000, 0], 72, 4, 208, 16, E4M3, 0),
+    ([9000, 1, 4000], 8, 4, 8, 16, BF16, 0), ([30, 0, 64, 7] * 90, 8, 4, 80, 16, BF16, 0),
+])
+def test_decode_several_heads_to_a_tile_of_a_large_pool(lens, H, Hk, D, page, cache, window):
+    # heads side by side that are no whole lines, in a pool and tables beyond 256 MB
+    size = 1 if cache == E4M3 else 2
+    pages = -(-(256 << 20) // (2 * D * size * Hk * page)) + 1
+    c = _decode_case(lens, H, Hk, D, page, BF16, cache, seed=len(lens) + D,
+                     width=-(-pages // len(lens)))
+    large = dict(c)
+    for name in ("k_cache", "v_cache"):
+        small = c[name].view(torch.uint8)
+        pool = torch.full((pages, *small.shape[1:]), 0x7F, dtype=torch.uint8, device=DEV)
+        if cache == BF16:
+            pool.view(BF16).fill_(float("nan"))
+        pool[:small.shape[0]] = small
+        large[name] = pool.view(cache)
+    out, lse = B.mla_decode_attention(**large, window=window, return_lse=True)
+    torch.cuda.synchronize()
+    B.mla_device_status()
+    narrow = dict(c, page_table=c["page_table"][:, :max(-(-max(lens) // page), 1)].contiguous())
+    _check_decode(narrow, out, lse, window)
+
+
+@pytest.mark.parametrize("D,cache", [(80, BF16), (64, BF16), (64, E4M3)])
+def test_decode_goes_by_the_pool_where_the_tables_are_wider(D, cache):
+    # a table for the longest context over a small pool: the same bits as one that fits
+    lens = np.random.default_rng(3).integers(1500, 2100, 16).tolist()
+    c = _decode_case(lens, 16, 8, D, 16, BF16, cache, seed=1, width=16384)
+    wide = B.mla_decode_attention(**c, return_lse=True)
+    c["page_table"] = c["page_table"][:, :2100 // 16 + 1].contiguous()
+    fit = B.mla_decode_attention(**c, return_lse=True)
+    torch.cuda.synchronize()
+    _check_decode(c, *fit)
+    assert torch.equal(wide[0], fit[0]) and torch.equal(wide[1], fit[1])
