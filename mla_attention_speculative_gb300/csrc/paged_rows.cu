@@ -796,12 +796,14 @@ extern "C" mla_status_t mla_page_step(
   p.capacity = (int)((int64_t)max_pages_per_seq * page_size > INT_MAX
                          ? INT_MAX
                          : (int64_t)max_pages_per_seq * page_size);
-  // A small batch takes 256 threads, whose barriers are cheap, and a row a
-  // thread (32 sequences: 3.1 us in a graph, 4.1 with four rows a thread, 6.4
-  // with 1024 threads); a larger one 1024 threads, so that fewer CTAs make the
-  // sums of all sequences, and four rows (4096 sequences, 1.07 M rows: 12.2 us,
-  // 16.5 with one row a thread, 26 with 256 threads).
-  const bool small = batch <= 256;
+  // 256 threads, whose barriers are cheap, and a row a thread: up to 1024 sequences
+  // whatever their rows, up to 4096 with four rows each.  (us in a graph, against 1024
+  // threads and four rows a thread: 257 sequences of 1 and of 261 rows 3.9 and 4.1
+  // against 6.9 and 8.2, 1024 3.9 and 6.7 against 7.7 and 8.9, 4096 of 4 rows 7.6
+  // against 10.6.)  Beyond, 1024 threads, so that fewer CTAs make the sums of all
+  // sequences, and four rows (4096 of 32 rows 10.2 against 17.7, of 261 rows 12.3
+  // against 26.5; 2048 of 261 rows 9.7 against 11.4, but of 32 rows 9.8 against 5.6).
+  const bool small = batch <= 1024 || (batch <= kEntries && max_rows <= 4 * (int64_t)batch);
   const int threads = small ? 256 : 1024;
   const int64_t per_pass = (int64_t)threads * (small ? 1 : 4);
   int64_t ctas = ((int64_t)max_rows + per_pass - 1) / per_pass;

@@ -63,6 +63,17 @@ def test_page_step_largest_table():
     assert out.row_start[-1].item() == batch * width
 
 
+@pytest.mark.parametrize("batch,page,tmax,newmax,short", [
+    (257, 16, 90, 30, True), (1024, 8, 40, 40, False), (1025, 8, 40, 40, True),
+    (1025, 16, 300, 3, False), (2047, 16, 300, 1, True), (4095, 16, 60, 3, False),
+    (4096, 7, 60, 4, True), (4097, 16, 60, 2, False)])
+def test_page_step_forms(batch, page, tmax, newmax, short):
+    c = _page_case(batch, batch, page, tmax, newmax, short)
+    total = int(c["new"].sum())
+    for rows in (total, 4 * batch + 1, 4 * batch, total // 2):
+        _check_page_step(c, rows)
+
+
 @pytest.mark.parametrize("batch", [300, 1024, 4096, 5000, 65535])
 @pytest.mark.parametrize("live", [{0: 3, -1: 3}, {0: 1, 1: 1, -2: 5, -1: 2}, {-1: 7}, {5: 2, 40: 3}])
 def test_page_step_long_runs_of_idle_slots(batch, live):
