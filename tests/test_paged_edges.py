@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import paged as P
 from mla_attention_speculative_gb300 import binding as B
 from mla_attention_speculative_gb300 import build_lib
 from test_paged_gpu import (BF16, DEV, E4M3, EDGES, FP32, _check_decode, _check_page_step, _decode_case,
@@ -302,3 +303,83 @@ def test_decode_goes_by_the_pool_where_the_tables_are_wider(D, cache):
     torch.cuda.synchronize()
     _check_decode(c, *fit)
     assert torch.equal(wide[0], fit[0]) and torch.equal(wide[1], fit[1])
+
+
+# ------------------------------------------------------------------- a draft loop, idle slots
+
+@pytest.mark.parametrize("cache", [BF16, E4M3, FP32])
+def test_draft_loop_with_idle_slots_in_a_graph(cache):
+    """page step -> K/V append -> queries by sequence -> decode attention, captured once; at
+    every step the rows that the page table names are the ones appended so far, and the
+    attention is theirs."""
+    H, Hk, D, page, Bn, W = 8, 2, 64, 8, 5, 4
+    pages, dtype = Bn * W, FP32 if cache == FP32 else BF16
+    g, gen = np.random.default_rng(51), torch.Generator(DEV).manual_seed(51)
+    a = g.uniform(-3, 3, (W * page, D // 2))
+    cs = torch.tensor(np.concatenate([np.cos(a), np.sin(a)], 1), dtype=FP32, device=DEV)
+    ks = vs = None
+    if cache == E4M3:
+        ks, vs = (torch.tensor([0.02, 0.03], device=DEV) for _ in "kv")
+    kc, vc = (torch.zeros(pages, page, Hk, D, dtype=FP32, device=DEV).to(cache) for _ in "kv")
+    table = i32(np.full((Bn, W), -1))
+    kept, new, held = (i32([0] * Bn) for _ in range(3))
+    free, span = i32(g.permutation(pages)), i32([0, pages])
+    qkv = torch.zeros(Bn, H + 2 * Hk, D, dtype=dtype, device=DEV)
+    step = B.PreparedPageStep(kept, new, held, table, free, span, page, pages, Bn)
+    put = B.PreparedAppendKV(qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:], cs, step.out.positions,
+                             step.out.slots, kc, vc, k_scale=ks, v_scale=vs)
+    q = torch.zeros(Bn, H, D, dtype=dtype, device=DEV)
+    att = B.PreparedDecodeAttention(q, kc, vc, step.out.cache_lens, table, k_scale=ks, v_scale=vs,
+                                    return_lse=True)
+
+    def one():
+        step.run()
+        put.run()
+        # the step's rows are packed: sequence b's is row_start[b]
+        rows = step.out.row_start[:Bn].clamp_max(Bn - 1).long()
+        torch.index_select(put.q_out, 0, rows, out=q)
+        att.run()
+        kept.copy_(step.out.cache_lens)
+        held.copy_(step.out.held_pages)
+        span.copy_(step.out.free_span)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        one()
+    hist = [[] for _ in range(Bn)]                     # (rotated k, v), [Hk, D] in 64 bits
+    u = {BF16: 2.0 ** -8, FP32: 2.0 ** -24, E4M3: 2.0 ** -4}[cache]
+    for i in range(24):
+        live = [b for b in range(Bn) if (i + 2 * b) % 5 != 0 and not (b == 2 and i < 9) and b != 4]
+        new.copy_(i32([int(b in live) for b in range(Bn)]))
+        qkv.copy_(torch.randn(qkv.shape, generator=gen, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert step.out.missing.item() == 0
+        x = npy(qkv)
+        for row, b in enumerate(live):
+            turn = npy(cs)[len(hist[b])]
+            want_q = P.rotate(x[row, :H], turn, False)
+            near(q[b], want_q, np.abs(want_q) * {BF16: 2.0 ** -8, FP32: 2.0 ** -23}[dtype]
+                 + 2.0 ** -20, f"q of {b} at step {i}")
+            hist[b].append((P.rotate(x[row, H:H + Hk], turn, False), x[row, H + Hk:]))
+        lens = step.out.cache_lens.tolist()
+        assert lens == [len(h) for h in hist]
+        tab = table.cpu().numpy()
+        for b in range(Bn):
+            pos = np.arange(lens[b])
+            for c, scale, part in ((kc, ks, 0), (vc, vs, 1)):
+                got = npy(c)[tab[b, pos // page], pos % page]
+                want = np.array([h[part] for h in hist[b]]).reshape(-1, Hk, D)
+                sc = 1.0 if scale is None else npy(scale)[:, None]
+                # (half a step of the cache's type, e4m3's smallest, and the rotation in fp32)
+                tol = np.abs(want) * (u + 2.0 ** -20) + 2.0 ** -20
+                if cache == E4M3:
+                    tol = np.maximum(tol, 2.0 ** -10 * sc) + 2.0 ** -20
+                    assert (np.abs(want) < 448 * sc).all()
+                assert (np.abs(got * sc - want) <= tol).all(), (i, b, part)
+        _check_decode(dict(q=q, k_cache=kc, v_cache=vc, cache_lens=step.out.cache_lens,
+                           page_table=table, k_scale=ks, v_scale=vs), att.out, att.lse,
+                      what=f"step {i}")
+    assert lens[4] == 0 and 0 < lens[2] < lens[0]
+    B.mla_device_status()
