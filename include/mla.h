@@ -523,7 +523,7 @@ typedef struct {
  *          elements between rows (views of one projection's rows will do);
  *          q NULL: only the cache is written
  *  q_out   device [rows, num_heads, head_dim], dense; may be q itself when q
- *          is dense
+ *          is dense.  No output may overlap another buffer otherwise.
  *
  * Skipped rows, distinct slots and rows == 0: as for mla_append_latent (with
  * rope_dim 0 only a negative position counts as outside). */

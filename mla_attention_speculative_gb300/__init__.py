@@ -12,6 +12,8 @@ __all__ = [
     "mla_max_absorbed_queries", "mla_max_absorbed_queries_batch", "mla_select_branch",
     "mla_workspace_bytes", "mla_verify_attention", "make_geometry", "MlaError",
     "mla_page_step", "mla_append_latent", "mla_append_kv", "mla_decode_attention",
+    "mla_decode_workspace_bytes", "PageStep", "PreparedPageStep", "PreparedAppendLatent",
+    "PreparedAppendKV", "PreparedDecodeAttention",
 ]
 
 

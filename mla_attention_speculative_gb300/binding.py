@@ -566,6 +566,11 @@ def mla_indexer_select(q: torch.Tensor, pooled: torch.Tensor, cache_len: int, k_
 # ---------------------------------------------------------------------------
 # Paged serving steps: page tables, appends, the drafter's decode attention
 # (inference only: no gradients are recorded)
+#
+# Every tensor starts on a 16-byte boundary (lengths and tables too: a slice of a
+# larger array may not).  The functions check, marshal and allocate at each call,
+# about 40 us of host time; a Prepared* object does so once, for fixed buffers,
+# and its run() takes 3 to 4 us.
 # ---------------------------------------------------------------------------
 
 def _tensor(name: str, t: torch.Tensor, shape=None, dtype=None, dense: bool = True):
@@ -614,7 +619,10 @@ def _allocating_on(stream, dev: torch.device):
 
 
 class _PreparedCall:
-    """A C call whose arguments are marshalled once and issued by run()."""
+    """A C call whose arguments are marshalled once and issued by run().
+
+    Runs share the object's buffers (outputs, and the workspace of the decode
+    attention): on several streams each must wait for the one before."""
 
     def _prepare(self, name: str, args, dev: torch.device, keep, made=()):
         self._name = name
@@ -918,7 +926,12 @@ def mla_append_kv(q, k, v, cos_sin, positions, slots, k_cache, v_cache, interlea
     caches [num_pages, page_size, Hkv, D] in any stride order (a cache laid
     out [pages, Hkv, page, D] is passed as ``cache.transpose(1, 2)``), of q's
     type or float8_e4m3fn with fp32 ``k_scale`` / ``v_scale`` [Hkv].  Rows
-    with position -1 are skipped.  ``q_out`` may be ``q``."""
+    with position -1 are skipped.  ``q_out`` may be ``q``; otherwise no output
+    may overlap an input.
+
+    The rows are a step's, packed: with an idle slot among the sequences the
+    query that mla_decode_attention wants for sequence b is row
+    ``row_start[b]`` (of mla_page_step), not b."""
     with _allocating_on(stream, k.device):
         call = PreparedAppendKV(q, k, v, cos_sin, positions, slots, k_cache, v_cache, interleaved,
                                 k_scale, v_scale, q_out)
@@ -942,7 +955,9 @@ class PreparedDecodeAttention(_PreparedCall):
     over fixed buffers (lengths and tables are read on the device, so they may
     change between runs and under a captured graph); ``run()`` issues it,
     ``out`` and ``lse`` are its outputs.  The tensors must outlive the
-    object."""
+    object.  It has one workspace: runs on several streams, and graphs that
+    hold them, must not overlap (an object, or a ``workspace``, for each
+    otherwise)."""
 
     def __init__(self, q, k_cache, v_cache, cache_lens, page_table, window: int = 0,
                  scale: Optional[float] = None, k_scale=None, v_scale=None, out=None, lse=None,

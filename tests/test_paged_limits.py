@@ -36,3 +36,11 @@ def test_numbers_beyond_32_bits_are_refused(at, value):
     args[at] = value
     with pytest.raises(ValueError, match="32-bit"):
         B._PreparedCall()._prepare("mla_decode_attention", args, torch.device("cuda", 0), ())
+
+
+def test_the_package_exports_the_paged_steps():
+    import mla_attention_speculative_gb300 as mla
+    for name in ("mla_page_step", "mla_append_latent", "mla_append_kv", "mla_decode_attention",
+                 "mla_decode_workspace_bytes", "PageStep", "PreparedPageStep",
+                 "PreparedAppendLatent", "PreparedAppendKV", "PreparedDecodeAttention"):
+        assert name in mla.__all__ and getattr(mla, name) is getattr(B, name)
