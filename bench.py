@@ -12,9 +12,9 @@ call streams its operands from HBM.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
 
-Prints one JSON line on rank 0.  Under torchrun every rank runs the same
-replica (no data exchange); value is the calls of all ranks over the slowest
-rank's time.
+Prints one JSON line on rank 0 (the secondary shapes go to stderr).  Under
+torchrun every rank runs the same replica (no data exchange); value is the
+calls of all ranks over the slowest rank's time.
 """
 
 from __future__ import annotations
@@ -206,7 +206,7 @@ def kernel_rates(kernel: str, geom, L: int, lens, us: float, peaks, topk_k: int 
 
 
 # Secondary measurements beside the headline (each its own workload, its own
-# line in the "shapes" object):
+# entry of the "shapes" object on stderr):
 # - the GLM-4.7-Flash-like crossover sweep at cache 8192 with each branch
 #   forced (the pages time both branches across L to validate the formula);
 # - the batched paged serving verify (32 sequences, T ~ U{1024..32768}, L = 8,
@@ -1000,15 +1000,23 @@ def run_ours(args):
                                  us, peaks) for L, us in per_L.items()},
             "roofline": roof,
             "kernel_ms_per_step": {k: v[1] / args.steps for k, v in ktimes.items()},
-            "shapes": shapes,
             "cpu_baseline": cpu,
             "clocks": clocks,
             "e2e": e2e,
             "gpu_launches": int(round(launches_per_step * args.steps)),
         }
-        print(json.dumps(line), flush=True)
+        _emit(line, shapes)
     if dist is not None:
         dist.destroy_process_group()
+
+
+def _emit(line, shapes):
+    """The headline as one JSON line on stdout.  The secondary shapes, tens of
+    kilobytes (a reader that keeps the last few of them lost the headline), are a
+    JSON line of their own on stderr, before it."""
+    if shapes is not None:
+        print(json.dumps({"shapes": shapes}), file=sys.stderr, flush=True)
+    print(json.dumps(line), flush=True)
 
 
 def _layer_bytes(geom):
