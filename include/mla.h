@@ -555,6 +555,7 @@ mla_status_t mla_decode_workspace_bytes(const mla_kv_geometry_t* geom, int32_t b
  *
  *  q       device [batch, num_heads, head_dim], q_row_stride elements between
  *          sequences, heads dense
+ *  batch   in [1, 65535]; at most 65535 query heads
  *  cache_lens  device [batch] int32
  *  page_table  device [batch, max_pages_per_seq] int32, entries past a
  *          sequence's last page are not read; an id outside [0, num_pages)

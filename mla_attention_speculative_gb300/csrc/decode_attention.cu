@@ -298,12 +298,14 @@ bool heads_fit(const mla_kv_geometry_t* g, int hg) {
 // lines are fetched again (heads of 80 in bf16: 637 MB for 437).  And single
 // lines a row apart come from DRAM slower than two at a time.  So a tile takes
 // as many neighbouring heads as make whole lines, two at least, a warp or two
-// each (32 sequences of 1024 to 32768: 80 wide 315 -> 216 us, 96 wide 315 ->
-// 248, 64 wide 189 -> 173; e4m3, 64 sequences: 64 wide 146 -> 102, 128 wide in
-// groups of 4 169 -> 159), if the cache is beyond what L2 keeps between two
+// each (32 sequences of 1024 to 32768: 80 wide 327 -> 223 us, 96 wide 329 ->
+// 259, 64 wide 187 -> 172; e4m3, 64 sequences: 64 wide 146 -> 102, 128 wide in
+// groups of 4 165 -> 160), if the cache is beyond what L2 keeps between two
 // heads: the merge and the join have more to do, and below that the lines are
-// found in L2 (16 sequences of up to 4099, 80 wide: 19.2 us with one head to a
-// tile, 21.4 with four).
+// found in L2 (16 sequences of up to 4099, 80 wide, found there: 22.5 us with one
+// head to a tile, 24.7 with four).  The lengths are known on the GPU only: short
+// sequences in a large pool with wide tables take the larger merges as well (32
+// of 100 positions, 80 wide: 13.8 us against 11.9).
 mla_status_t make_plan(const mla_kv_geometry_t* g, const mla_kv_cache_t* cache, int32_t batch,
                        int32_t max_pages, Plan* out) {
   const mla_status_t st = plan_for(g, batch, cache->page_size, max_pages, 1, out);
