@@ -551,7 +551,9 @@ mla_status_t mla_decode_workspace_bytes(const mla_kv_geometry_t* geom, int32_t b
  * does a head whose scores are all -inf.  T_b beyond the table's
  * max_pages_per_seq * page_size rows (2^31 - 1024 at most) counts as that
  * many.  An infinite value among the v rows seen gives that infinity (NaN beside
- * its opposite, or under a weight below 2^-100 of the largest).
+ * its opposite, or under a weight below 2^-100 of the largest).  The sums
+ * are fp32 and divided by the weights' sum at the end: values above 3.4e38 over
+ * the number of rows may leave its range.
  *
  *  q       device [batch, num_heads, head_dim], q_row_stride elements between
  *          sequences, heads dense
@@ -561,7 +563,8 @@ mla_status_t mla_decode_workspace_bytes(const mla_kv_geometry_t* geom, int32_t b
  *          sequence's last page are not read; an id outside [0, num_pages)
  *          reads as zero keys and values and is recorded as code 300 in the
  *          status word
- *  out     device [batch, num_heads, head_dim], dense
+ *  out     device [batch, num_heads, head_dim], dense; may be q itself when q is
+ *          dense.  No output may overlap another buffer otherwise.
  *  lse     device fp32 [batch, num_heads], may be NULL
  *  workspace  mla_decode_workspace_bytes() bytes, 256-byte aligned (may be
  *          NULL when that is 0)

@@ -444,6 +444,16 @@ extern "C" mla_status_t mla_decode_attention(
               (long long)q_row_stride, (long long)g->num_heads * g->head_dim);
     return MLA_ERR_INVALID_ARG;
   }
+  // in place only row for row: a head's queries are used by the CTA that writes its
+  // output, or by those whose parts the join, behind all of them, puts there
+  const int64_t row = (int64_t)g->num_heads * g->head_dim;
+  const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
+  const uintptr_t q1 = q0 + (uintptr_t)(((batch - 1) * q_row_stride + row) * eb);
+  const uintptr_t o1 = o0 + (uintptr_t)(batch * row * eb);
+  if (q0 < o1 && o0 < q1 && !(q == out && q_row_stride == row)) {
+    set_error("decode: out overlaps q without being q");
+    return MLA_ERR_INVALID_ARG;
+  }
   decode::Plan d;
   st = decode::make_plan(g, cache, batch, max_pages_per_seq, &d);
   if (st != MLA_OK) return st;

@@ -262,6 +262,19 @@ def test_decode_idle_slots_between_live_ones_cost_little():
     assert apart < 3 * together + 20, (apart, together)
 
 
+@pytest.mark.parametrize("lens,H,Hk,D,cache", [
+    (EDGES, 8, 2, 128, BF16), (EDGES, 40, 2, 64, E4M3), (EDGES, 20, 2, 64, FP32),
+    ([30001, 0, 700], 36, 2, 128, BF16), ([3, 0, 1, 9] * 200, 4, 2, 64, BF16)])
+def test_decode_in_place(lens, H, Hk, D, cache):
+    c = _decode_case(lens, H, Hk, D, 16, FP32 if cache == FP32 else BF16, cache, seed=7)
+    want = B.mla_decode_attention(**c)
+    for _ in range(3):
+        q = c["q"].clone()
+        got = B.mla_decode_attention(**dict(c, q=q), out=q)
+        torch.cuda.synchronize()
+        assert got is q and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("lens,H,Hk,D,page,cache,window", [
     (EDGES, 8, 4, 80, 16, BF16, 0), (EDGES, 8, 8, 40, 16, BF16, 0), (EDGES, 4, 2, 96, 7, BF16, 33),
     (EDGES, 12, 4, 112, 64, BF16, 0), (EDGES, 6, 2, 80, 16, BF16, 0), (EDGES, 3, 3, 80, 16, BF16, 0),

@@ -44,3 +44,29 @@ def test_the_package_exports_the_paged_steps():
                  "mla_decode_workspace_bytes", "PageStep", "PreparedPageStep",
                  "PreparedAppendLatent", "PreparedAppendKV", "PreparedDecodeAttention"):
         assert name in mla.__all__ and getattr(mla, name) is getattr(B, name)
+
+
+def _decode(**kw):
+    geom = B.KVGeometry(8, 2, 128, 0.0, 0, 0)
+    cache = B.KVCache(F, F + 0x1000, 16 * 2 * 128, 2 * 128, 128, 16, 10, None, None)
+    a = dict(q=F, qs=1024, lens=F, batch=3, table=F, W=4096, window=0, out=F + 0x100000, lse=F,
+             ws=F, wsb=0)
+    a.update(kw)
+    v = list(a.values())
+    return B.lib().mla_decode_attention(ctypes.byref(geom), v[0], v[1], ctypes.byref(cache),
+                                        *v[2:], None)
+
+
+@pytest.mark.parametrize("kw", [dict(out=F + 16), dict(out=F - 16), dict(out=F, qs=1032),
+                                dict(out=F + 2 * 1032 * 2 + 2032, qs=1032),
+                                dict(q=F + 3 * 2048 - 16, out=F)])
+def test_decode_out_may_be_q_but_not_overlap_it(kw):
+    assert _decode(**kw) == B.MLA_ERR_INVALID_ARG
+    assert "overlaps q" in B.mla_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(out=F), dict(out=F + 3 * 2048), dict(out=F - 3 * 2048),
+                                dict(out=F + (2 * 1032 + 1024) * 2, qs=1032)])
+def test_decode_out_beside_q_passes(kw):
+    # (the workspace is what is refused here)
+    assert _decode(**kw) == B.MLA_ERR_WORKSPACE
