@@ -581,6 +581,176 @@ mla_status_t mla_decode_attention(const mla_kv_geometry_t* geom, const void* q,
                                   int32_t window, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace mla_chunk_attention needs for `rows` rows of
+ * `batch` sequences with tables of max_pages_per_seq pages of page_size rows.
+ * It needs no initialisation.  Host only. */
+mla_status_t mla_chunk_workspace_bytes(const mla_kv_geometry_t* geom, int32_t batch, int32_t rows,
+                                       int32_t page_size, int32_t max_pages_per_seq,
+                                       size_t* bytes);
+
+/* Attention of a step's new rows over a paged key/value cache: the chunk of a
+ * prompt, or the draft rows of a verify step, of every sequence at once, as
+ * mla_page_step lays them out and after mla_append_kv has written them.
+ * Sequence b has rows row_start[b] .. row_start[b + 1] - 1 of the step; its row
+ * i (counted from row_start[b]) sits at position p = kept_lens[b] + i and sees
+ * the cached rows max(0, p + 1 - window) .. min(p, cache_lens[b] - 1) (window
+ * 0: from 0 on):
+ *   out[row][h] = sum_t softmax_t(scale * q[row][h] . k[t]) v[t]
+ *   lse[row][h] = log sum_t exp(scale * q[row][h] . k[t])       (natural log)
+ * A row that sees nothing (its page was missing, say, and its window ends
+ * behind the cached rows) gets zeros and lse = -inf, and so does a head whose
+ * scores are all -inf.  Rows outside every sequence are not written.
+ *
+ *  q       device [rows, num_heads, head_dim], q_row_stride elements between
+ *          rows, heads dense
+ *  rows    rows of q, out and lse; rows * num_heads below 2^31 - 1024.  0: no
+ *          work
+ *  kept_lens / cache_lens  device [batch] int32: mla_page_step's kept_lens and
+ *          cache_lens_out (negative counts as 0; cache_lens beyond the table
+ *          counts as what it holds)
+ *  row_start  device [batch + 1] int32, ascending (cut to [0, rows])
+ *  page_table  as for mla_decode_attention
+ *  out     device [rows, num_heads, head_dim], dense; no output may overlap
+ *          another buffer
+ *  lse     device fp32 [rows, num_heads], may be NULL
+ *  workspace  mla_chunk_workspace_bytes() bytes, 256-byte aligned
+ *
+ * What a row does not see does not touch it, infinities and NaN included; an
+ * infinite value seen gives that infinity (NaN beside its opposite, or under a
+ * weight below 2^-24 of the largest).  The lengths are read on the device and
+ * the work is cut into equal shares there; parts are joined in a fixed order, so
+ * repeated calls give the same bits.  Concurrent calls need a workspace each. */
+mla_status_t mla_chunk_attention(const mla_kv_geometry_t* geom, const void* q,
+                                 int64_t q_row_stride, int32_t rows, const mla_kv_cache_t* cache,
+                                 const int32_t* kept_lens, const int32_t* cache_lens,
+                                 const int32_t* row_start, int32_t batch,
+                                 const int32_t* page_table, int32_t max_pages_per_seq,
+                                 int32_t window, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The pages of a paged cache as a pool.  A page may be held by several
+ * sequences: shares[page] counts its holders beyond the first, so a page that
+ * one sequence holds and a page on the free list both have 0 (mla_page_step
+ * needs to know nothing of it).  Only whole pages are ever shared, so the rows
+ * that a sequence appends never fall into a shared one; a sequence cut back
+ * into a shared page is forked to an idle slot, which gets its last page's rows
+ * as a copy, and released.
+ *
+ * As above nothing is read on the host, and each call is one launch.  Outputs
+ * must not overlap inputs or one another, except where an argument says so; a
+ * call with separate outputs can be repeated with the same result.  Page ids
+ * outside [0, num_pages) are passed over and recorded as code 300 in the status
+ * word.  batch in [1, 65535]; batch * max_pages_per_seq at most 2^31 - 1; every
+ * array 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+
+/* Sequences forked to idle slots.  A slot b with held_pages[b] <= 0 and 0 <=
+ * src_of[b] < batch takes the rows of sequence s = src_of[b]; every other slot
+ * stays as it is (src_of[b] is not looked at where b holds pages).  With P =
+ * page_size, held = held_pages[s] in [0, max_pages_per_seq] and T =
+ * min(cache_lens[s], held * P):
+ *   page_table[b][j] = page_table[s][j], shares + 1      for j < floor(T / P)
+ *   if T is no multiple of P, the next page of the free list (in slot order)
+ *   becomes page_table[b][floor(T / P)], and the move (page_table[s][floor(T /
+ *   P)], that page, T mod P rows) is put on the list for mla_page_copy
+ *   cache_lens_out[b] = T, held_pages_out[b] = ceil(T / P)
+ * When the list has run out the slot gets the whole pages only and is that much
+ * shorter, and missing_out counts it.  Sources are taken as they were before the
+ * call.
+ *
+ *  shares / shares_out  device [num_pages]; may be one array
+ *  free_pages / free_span  as for mla_page_step; free_capacity >= 1
+ *  move_src_out / move_dst_out / move_rows_out  device [batch]; the first
+ *          moves_out[0] entries are written
+ *  missing_out / moves_out  device [1] */
+mla_status_t mla_page_fork(const int32_t* src_of, const int32_t* cache_lens,
+                           const int32_t* held_pages, int32_t batch, int32_t* page_table,
+                           int32_t max_pages_per_seq, int32_t page_size, int32_t num_pages,
+                           const int32_t* shares, const int32_t* free_pages,
+                           int32_t free_capacity, const int32_t* free_span,
+                           int32_t* cache_lens_out, int32_t* held_pages_out, int32_t* shares_out,
+                           int32_t* free_span_out, int32_t* missing_out, int32_t* move_src_out,
+                           int32_t* move_dst_out, int32_t* move_rows_out, int32_t* moves_out,
+                           void* stream);
+
+/* Pages given back.  Sequence b keeps kept_lens[b] rows (0 or less: it ends)
+ * and drops the pages behind them, entries ceil(kept / page_size) ..
+ * held_pages[b] - 1 of its table row.  A page that has holders left only loses
+ * one of them; the others go back to the free list in ascending order, in front
+ * of its first entry as far as there is room (mla_page_step takes from there),
+ * the rest behind its last one.
+ *
+ *  page_table  device [batch, max_pages_per_seq], read only
+ *  free_pages  device [free_capacity], free_capacity >= num_pages (so there is
+ *          always room); entries outside free_span are written
+ *  held_pages_out  device [batch]: the pages kept
+ *  shares / shares_out  device [num_pages]; may be one array
+ *  free_span_out  device [2]: the list with the pages given back
+ *  released_out  device [1]: how many those are */
+mla_status_t mla_page_release(const int32_t* kept_lens, const int32_t* held_pages, int32_t batch,
+                              const int32_t* page_table, int32_t max_pages_per_seq,
+                              int32_t page_size, int32_t num_pages, const int32_t* shares,
+                              int32_t* free_pages, int32_t free_capacity,
+                              const int32_t* free_span, int32_t* held_pages_out,
+                              int32_t* shares_out, int32_t* free_span_out, int32_t* released_out,
+                              void* stream);
+
+/* Bytes of device workspace mla_page_compact needs.  Host only. */
+mla_status_t mla_page_compact_workspace_bytes(int32_t num_pages, size_t* bytes);
+
+/* All held pages brought to the front of the pool.  The L distinct pages in
+ * entries 0 .. held_pages[b] - 1 of the table rows are live; the n-th live page
+ * at or beyond L moves to the n-th page below L that is not live.  Pages in no
+ * table row are free afterwards, whoever had them before.
+ *
+ *  page_table_out  device [batch, max_pages_per_seq]: the table with the new
+ *          ids, -1 behind a sequence's pages; may be page_table
+ *  shares / shares_out  device [num_pages]; may be one array
+ *  free_pages  device [free_capacity >= num_pages]: gets L .. num_pages - 1
+ *  free_span_out  device [2]: {0, num_pages - L}
+ *  move_src_out / move_dst_out  device [num_pages / 2]: the moves, for
+ *          mla_page_copy (no page is both a source and a destination)
+ *  moves_out  device [1]: how many there are
+ *  workspace  mla_page_compact_workspace_bytes() bytes, 256-byte aligned */
+mla_status_t mla_page_compact(const int32_t* held_pages, int32_t batch, const int32_t* page_table,
+                              int32_t max_pages_per_seq, int32_t num_pages, const int32_t* shares,
+                              int32_t* page_table_out, int32_t* shares_out, int32_t* free_pages,
+                              int32_t free_capacity, int32_t* free_span_out,
+                              int32_t* move_src_out, int32_t* move_dst_out, int32_t* moves_out,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* One cache tensor whose pages are copied: a page's row r is `heads` runs of
+ * `width` bytes, run h at base + page*page_stride + r*row_stride +
+ * h*head_stride (strides in bytes, any order; all multiples of 16). */
+typedef struct {
+  void* base;
+  int64_t page_stride;
+  int64_t row_stride;
+  int64_t head_stride;
+  int32_t heads;
+  int32_t width;
+} mla_page_view_t;
+
+/* The first move_rows[i] rows of page move_src[i] to page move_dst[i], for i <
+ * min(moves[0], capacity), in every one of up to 128 cache tensors (the keys
+ * and values, or latents and RoPE keys, of all layers that one page table
+ * addresses) at once.
+ *
+ *  views   host [num_views]
+ *  move_src / move_dst / move_rows  device [capacity]; move_rows NULL: whole
+ *          pages
+ *  moves   device [1]; NULL: `capacity` of them
+ *
+ * Destinations must be distinct and no page may be both a source and a
+ * destination (the lists of mla_page_fork and mla_page_compact are such).  A
+ * move with a page outside [0, num_pages) is passed over and recorded as code
+ * 300 in the status word. */
+mla_status_t mla_page_copy(const mla_page_view_t* views, int32_t num_views, int32_t page_size,
+                           int32_t num_pages, const int32_t* move_src, const int32_t* move_dst,
+                           const int32_t* move_rows, const int32_t* moves, int32_t capacity,
+                           void* stream);
+
 /* Per-kernel timing, for benchmarks.  While enabled, every kernel launch the
  * library makes is bracketed by a pair of CUDA events recorded on the call's
  * stream (events come from a library-owned pool; no device memory).  Do not

@@ -13,7 +13,10 @@ __all__ = [
     "mla_workspace_bytes", "mla_verify_attention", "make_geometry", "MlaError",
     "mla_page_step", "mla_append_latent", "mla_append_kv", "mla_decode_attention",
     "mla_decode_workspace_bytes", "PageStep", "PreparedPageStep", "PreparedAppendLatent",
-    "PreparedAppendKV", "PreparedDecodeAttention",
+    "PreparedAppendKV", "PreparedDecodeAttention", "mla_chunk_attention",
+    "mla_chunk_workspace_bytes", "mla_page_fork", "mla_page_release", "mla_page_compact",
+    "mla_page_copy", "PageFork", "PageRelease", "PageCompact", "PreparedChunkAttention",
+    "PreparedPageFork", "PreparedPageRelease", "PreparedPageCompact", "PreparedPageCopy",
 ]
 
 

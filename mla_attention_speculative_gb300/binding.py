@@ -54,6 +54,12 @@ class KVGeometry(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("cache_dtype", ctypes.c_int32)]
 
 
+class PageView(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
 class KVCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
@@ -102,6 +108,17 @@ _SIGS = {
     "mla_decode_workspace_bytes": (_I32, [_P, _I32, _I32, _I32, _P]),
     "mla_decode_attention": (_I32, [_P, _P, _I64, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P,
                                     ctypes.c_size_t, _P]),
+    "mla_chunk_workspace_bytes": (_I32, [_P, _I32, _I32, _I32, _I32, _P]),
+    "mla_chunk_attention": (_I32, [_P, _P, _I64, _I32, _P, _P, _P, _P, _I32, _P, _I32, _I32, _P,
+                                   _P, _P, ctypes.c_size_t, _P]),
+    "mla_page_fork": (_I32, [_P, _P, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P,
+                             _P, _P, _P, _P, _P, _P, _P]),
+    "mla_page_release": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P,
+                                _P, _P]),
+    "mla_page_compact_workspace_bytes": (_I32, [_I32, _P]),
+    "mla_page_compact": (_I32, [_P, _I32, _P, _I32, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _P,
+                                _P, ctypes.c_size_t, _P]),
+    "mla_page_copy": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _I32, _P]),
     "mla_kernel_timing_enable": (_I32, [_I32]),
     "mla_kernel_timing_read": (_I32, [ctypes.c_char_p, ctypes.c_size_t, _P, _P, _I32, _P,
                                       _I32]),
@@ -1021,3 +1038,344 @@ def mla_decode_attention(q, k_cache, v_cache, cache_lens, page_table, window: in
                                        k_scale, v_scale, out, lse, return_lse, workspace)
         call.run(stream)
     return (call.out, call.lse) if call.lse is not None else call.out
+
+
+def mla_chunk_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: int, batch: int,
+                              rows: int, page_size: int, max_pages: int, dtype=torch.bfloat16,
+                              cache_dtype=None) -> int:
+    geom = KVGeometry(num_heads, num_kv_heads, head_dim, 0.0, DTYPES[dtype],
+                      CACHE_DTYPES[cache_dtype if cache_dtype is not None else dtype])
+    out = ctypes.c_size_t(0)
+    _check(lib().mla_chunk_workspace_bytes(ctypes.byref(geom), batch, rows, page_size, max_pages,
+                                           ctypes.byref(out)), "mla_chunk_workspace_bytes")
+    return out.value
+
+
+class PreparedChunkAttention(_PreparedCall):
+    """mla_chunk_attention with its arguments marshalled once, for steps over fixed
+    buffers (lengths, row starts and tables are read on the device, so they may
+    change between runs and under a captured graph); ``run()`` issues it,
+    ``out`` and ``lse`` are its outputs.  The tensors must outlive the
+    object.  It has one workspace: runs on several streams, and graphs that
+    hold them, must not overlap (an object, or a ``workspace``, for each
+    otherwise)."""
+
+    def __init__(self, q, k_cache, v_cache, kept_lens, cache_lens, row_start, page_table,
+                 window: int = 0, scale: Optional[float] = None, k_scale=None, v_scale=None,
+                 out=None, lse=None, return_lse: bool = False, workspace=None):
+        N, H, D, qs = _head_rows("q", q)
+        _tensor("k_cache", k_cache, (None, None, None, D), dense=False)
+        Hk = k_cache.shape[2]
+        cache = _kv_cache(k_cache, v_cache, q.dtype, Hk, D, k_scale, v_scale)
+        _tensor("page_table", page_table, (None, None), torch.int32)
+        B = page_table.shape[0]
+        _tensor("kept_lens", kept_lens, (B,), torch.int32)
+        _tensor("cache_lens", cache_lens, (B,), torch.int32)
+        _tensor("row_start", row_start, (B + 1,), torch.int32)
+        if out is not None:
+            _tensor("out", out, (N, H, D), q.dtype)
+        if lse is not None:
+            _tensor("lse", lse, (N, H), torch.float32)
+        if workspace is not None:
+            _tensor("workspace", workspace)
+        dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, kept_lens=kept_lens,
+                          cache_lens=cache_lens, row_start=row_start, page_table=page_table,
+                          k_scale=k_scale, v_scale=v_scale, out=out, lse=lse,
+                          workspace=workspace)
+        if scale is not None and not float(scale) > 0.0:
+            raise ValueError("scale must be positive (None: 1/sqrt(head_dim))")
+        geom = KVGeometry(H, Hk, D, float(scale) if scale is not None else 0.0, DTYPES[q.dtype],
+                          CACHE_DTYPES[k_cache.dtype])
+        made = []
+        # (a row outside every sequence is not written: it starts as zeros, not as whatever was
+        # there)
+        if out is None:
+            out = torch.zeros((N, H, D), dtype=q.dtype, device=dev)
+            made.append(out)
+        if lse is None and return_lse:
+            lse = torch.zeros((N, H), dtype=torch.float32, device=dev)
+            made.append(lse)
+        if workspace is None:
+            nbytes = ctypes.c_size_t(0)
+            with torch.cuda.device(dev):
+                _check(lib().mla_chunk_workspace_bytes(
+                    ctypes.byref(geom), B, N, k_cache.shape[1], page_table.shape[1],
+                    ctypes.byref(nbytes)), "mla_chunk_workspace_bytes")
+            workspace = new_workspace(nbytes.value, dev)
+            made.append(workspace)
+        self.out, self.lse = out, lse
+        args = [ctypes.byref(geom), _ptr(q), qs, N, ctypes.byref(cache), _ptr(kept_lens),
+                _ptr(cache_lens), _ptr(row_start), B, _ptr(page_table), page_table.shape[1],
+                int(window), _ptr(out), _ptr(lse), _ptr(workspace),
+                workspace.numel() * workspace.element_size()]
+        keep = (geom, cache, q, k_cache, v_cache, kept_lens, cache_lens, row_start, page_table,
+                k_scale, v_scale, out, lse, workspace)
+        self._prepare("mla_chunk_attention", args, dev, keep, made)
+
+
+def mla_chunk_attention(q, k_cache, v_cache, kept_lens, cache_lens, row_start, page_table,
+                        window: int = 0, scale: Optional[float] = None, k_scale=None,
+                        v_scale=None, out=None, lse=None, return_lse: bool = False,
+                        workspace=None, stream=None):
+    """Attention of a step's new rows over a paged key/value cache.  Returns out, or
+    (out, lse) with ``return_lse`` or ``lse``.
+
+    ``q`` [N, H, D], the step's rows as mla_append_kv returns them; caches as
+    for mla_decode_attention, holding those rows; ``kept_lens`` int32 [B] (the
+    one given to mla_page_step), ``cache_lens`` [B] and ``row_start`` [B + 1] as
+    mla_page_step returns them: row i of a sequence sits at position kept + i and
+    sees itself and what is before it, the last ``window`` positions where that
+    is positive.  Rows behind the last sequence are left as they are."""
+    with _allocating_on(stream, q.device):
+        call = PreparedChunkAttention(q, k_cache, v_cache, kept_lens, cache_lens, row_start,
+                                      page_table, window, scale, k_scale, v_scale, out, lse,
+                                      return_lse, workspace)
+        call.run(stream)
+    return (call.out, call.lse) if call.lse is not None else call.out
+
+
+# ---------------------------------------------------------------------------
+# The pages of a cache as a pool.  ``shares`` int32 [num_pages] counts a page's
+# holders beyond the first; it starts as zeros.
+# ---------------------------------------------------------------------------
+
+class PageFork(NamedTuple):
+    """The outputs of mla_page_fork (device tensors, int32)."""
+    cache_lens: torch.Tensor   # [batch]
+    held_pages: torch.Tensor   # [batch]
+    shares: torch.Tensor       # [num_pages]
+    free_span: torch.Tensor    # [2]
+    missing: torch.Tensor      # [1]
+    move_src: torch.Tensor     # [batch], the first moves[0] of them
+    move_dst: torch.Tensor     # [batch]
+    move_rows: torch.Tensor    # [batch]
+    moves: torch.Tensor        # [1]
+
+
+class PageRelease(NamedTuple):
+    """The outputs of mla_page_release (device tensors, int32)."""
+    held_pages: torch.Tensor   # [batch]
+    shares: torch.Tensor       # [num_pages]
+    free_span: torch.Tensor    # [2]
+    released: torch.Tensor     # [1]
+
+
+class PageCompact(NamedTuple):
+    """The outputs of mla_page_compact (device tensors, int32)."""
+    page_table: torch.Tensor   # [batch, max_pages]
+    shares: torch.Tensor       # [num_pages]
+    free_span: torch.Tensor    # [2]
+    move_src: torch.Tensor     # [num_pages / 2, at least 1], the first moves[0] of them
+    move_dst: torch.Tensor     # [the same]
+    moves: torch.Tensor        # [1]
+
+
+class _PreparedPoolCall(_PreparedCall):
+    """What the page calls share: int32 tensors checked, outputs checked or made."""
+
+    def _pool(self, kind, inputs, shapes, out):
+        for name, (t, shape) in inputs.items():
+            _tensor(name, t, shape, torch.int32)
+        if out is not None:
+            if len(out) != len(shapes):
+                raise ValueError(f"out must be a {kind.__name__}")
+            for name, t in zip(kind._fields, out):
+                _tensor("out." + name, t, shapes[name], torch.int32)
+        given = {} if out is None else {"out_" + n: t for n, t in zip(kind._fields, out)}
+        dev = _one_device(**{n: t for n, (t, _) in inputs.items()}, **given)
+        made = ()
+        if out is None:
+            # (move lists are written as far as there are moves: the rest starts as zeros)
+            out = made = kind(*[torch.zeros(shapes[n], dtype=torch.int32, device=dev)
+                                if n.startswith("move_") else
+                                torch.empty(shapes[n], dtype=torch.int32, device=dev)
+                                for n in kind._fields])
+        self.out = kind(*out)
+        return dev, made
+
+
+class PreparedPageFork(_PreparedPoolCall):
+    """mla_page_fork with its arguments marshalled once; ``run()`` issues it and
+    ``out`` holds its outputs.  The tensors must outlive the object."""
+
+    def __init__(self, src_of, cache_lens, held_pages, page_table, shares, free_pages, free_span,
+                 page_size: int, out: Optional[PageFork] = None):
+        _tensor("page_table", page_table, (None, None), torch.int32)
+        _tensor("shares", shares, (None,), torch.int32)
+        B, W = page_table.shape
+        P = shares.numel()
+        inputs = dict(src_of=(src_of, (B,)), cache_lens=(cache_lens, (B,)),
+                      held_pages=(held_pages, (B,)), page_table=(page_table, (B, W)),
+                      shares=(shares, (P,)), free_pages=(free_pages, (None,)),
+                      free_span=(free_span, (2,)))
+        shapes = dict(cache_lens=(B,), held_pages=(B,), shares=(P,), free_span=(2,), missing=(1,),
+                      move_src=(B,), move_dst=(B,), move_rows=(B,), moves=(1,))
+        dev, made = self._pool(PageFork, inputs, shapes, out)
+        o = self.out
+        args = [_ptr(src_of), _ptr(cache_lens), _ptr(held_pages), B, _ptr(page_table), W,
+                int(page_size), P, _ptr(shares), _ptr(free_pages), free_pages.numel(),
+                _ptr(free_span), *[_ptr(t) for t in o]]
+        self._prepare("mla_page_fork", args, dev, (inputs, o), made)
+
+
+def mla_page_fork(src_of, cache_lens, held_pages, page_table, shares, free_pages, free_span,
+                  page_size: int, out: Optional[PageFork] = None, stream=None) -> PageFork:
+    """Fork sequences to idle slots: slot b takes the rows of sequence ``src_of[b]``
+    where that is in [0, B) and slot b holds no pages.
+
+    ``src_of``, ``cache_lens``, ``held_pages`` int32 [B]; ``page_table`` int32
+    [B, max_pages] (the forked slots' entries are written); ``shares`` int32
+    [num_pages]; ``free_pages`` and ``free_span`` as for mla_page_step.  Whole
+    pages are shared; a last one that is not full is replaced by a free page, and
+    the rows to copy are listed: ``mla_page_copy(caches, out.move_src,
+    out.move_dst, out.moves, out.move_rows)``, for the caches of all layers, has
+    to follow.  ``missing`` counts the slots that the free list had no page for.
+    ``out.shares`` may be ``shares``."""
+    with _allocating_on(stream, page_table.device):
+        call = PreparedPageFork(src_of, cache_lens, held_pages, page_table, shares, free_pages,
+                                free_span, page_size, out)
+        call.run(stream)
+    return call.out
+
+
+class PreparedPageRelease(_PreparedPoolCall):
+    """mla_page_release with its arguments marshalled once; ``run()`` issues it and
+    ``out`` holds its outputs.  The tensors must outlive the object."""
+
+    def __init__(self, kept_lens, held_pages, page_table, shares, free_pages, free_span,
+                 page_size: int, out: Optional[PageRelease] = None):
+        _tensor("page_table", page_table, (None, None), torch.int32)
+        _tensor("shares", shares, (None,), torch.int32)
+        B, W = page_table.shape
+        P = shares.numel()
+        inputs = dict(kept_lens=(kept_lens, (B,)), held_pages=(held_pages, (B,)),
+                      page_table=(page_table, (B, W)), shares=(shares, (P,)),
+                      free_pages=(free_pages, (None,)), free_span=(free_span, (2,)))
+        shapes = dict(held_pages=(B,), shares=(P,), free_span=(2,), released=(1,))
+        dev, made = self._pool(PageRelease, inputs, shapes, out)
+        args = [_ptr(kept_lens), _ptr(held_pages), B, _ptr(page_table), W, int(page_size), P,
+                _ptr(shares), _ptr(free_pages), free_pages.numel(), _ptr(free_span),
+                *[_ptr(t) for t in self.out]]
+        self._prepare("mla_page_release", args, dev, (inputs, self.out), made)
+
+
+def mla_page_release(kept_lens, held_pages, page_table, shares, free_pages, free_span,
+                     page_size: int, out: Optional[PageRelease] = None,
+                     stream=None) -> PageRelease:
+    """Give back the pages behind each sequence's ``kept_lens[b]`` rows (0: the
+    sequence ends), those that no other sequence holds to the free list.
+
+    ``free_pages`` has room for every page (as many entries as ``shares``) and is
+    written outside ``free_span``; ``page_table`` is only read.  ``out.held_pages``,
+    ``out.shares`` and ``out.free_span`` are the next call's inputs;
+    ``out.shares`` may be ``shares``."""
+    with _allocating_on(stream, page_table.device):
+        call = PreparedPageRelease(kept_lens, held_pages, page_table, shares, free_pages,
+                                   free_span, page_size, out)
+        call.run(stream)
+    return call.out
+
+
+class PreparedPageCompact(_PreparedPoolCall):
+    """mla_page_compact with its arguments marshalled once; ``run()`` issues it and
+    ``out`` holds its outputs.  The tensors must outlive the object.  It has one
+    workspace, as PreparedDecodeAttention has."""
+
+    def __init__(self, held_pages, page_table, shares, free_pages,
+                 out: Optional[PageCompact] = None, workspace=None):
+        _tensor("page_table", page_table, (None, None), torch.int32)
+        _tensor("shares", shares, (None,), torch.int32)
+        B, W = page_table.shape
+        P = shares.numel()
+        M = max(1, P // 2)
+        inputs = dict(held_pages=(held_pages, (B,)), page_table=(page_table, (B, W)),
+                      shares=(shares, (P,)), free_pages=(free_pages, (None,)))
+        shapes = dict(page_table=(B, W), shares=(P,), free_span=(2,), move_src=(M,),
+                      move_dst=(M,), moves=(1,))
+        if workspace is not None:
+            _tensor("workspace", workspace)
+        dev, made = self._pool(PageCompact, inputs, shapes, out)
+        _one_device(page_table=page_table, workspace=workspace)
+        if workspace is None:
+            nbytes = ctypes.c_size_t(0)
+            _check(lib().mla_page_compact_workspace_bytes(P, ctypes.byref(nbytes)),
+                   "mla_page_compact_workspace_bytes")
+            workspace = new_workspace(nbytes.value, dev)
+            made = tuple(made) + (workspace,)
+        o = self.out
+        args = [_ptr(held_pages), B, _ptr(page_table), W, P, _ptr(shares), _ptr(o.page_table),
+                _ptr(o.shares), _ptr(free_pages), free_pages.numel(), _ptr(o.free_span),
+                _ptr(o.move_src), _ptr(o.move_dst), _ptr(o.moves), _ptr(workspace),
+                workspace.numel() * workspace.element_size()]
+        self._prepare("mla_page_compact", args, dev, (inputs, o, workspace), made)
+
+
+def mla_page_compact(held_pages, page_table, shares, free_pages,
+                     out: Optional[PageCompact] = None, workspace=None,
+                     stream=None) -> PageCompact:
+    """Bring all held pages to the front of the pool: with L of them, those at or
+    beyond L go to the free places below, and L .. num_pages - 1 are free.
+
+    Every page in use must be in a table row.  ``mla_page_copy(caches,
+    out.move_src, out.move_dst, out.moves)``, for the caches of all layers, has
+    to follow; ``free_pages`` (as many entries as ``shares``) is rewritten.
+    ``out.page_table`` may be ``page_table`` and ``out.shares`` ``shares``."""
+    with _allocating_on(stream, page_table.device):
+        call = PreparedPageCompact(held_pages, page_table, shares, free_pages, out, workspace)
+        call.run(stream)
+    return call.out
+
+
+def _page_view(name: str, t: torch.Tensor) -> PageView:
+    """A cache [pages, page, width] or [pages, page, heads, width] in any stride order."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [pages, page, width] or [pages, page, heads, width]")
+    if t.numel() == 0 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must not be empty and its rows contiguous in their last "
+                         "dimension")
+    eb = t.element_size()
+    strides = [t.stride(i) * eb if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
+    heads = t.shape[2] if t.dim() == 4 else 1
+    return PageView(_ptr(t), strides[0], strides[1], strides[2] if t.dim() == 4 else 0, heads,
+                    t.shape[-1] * eb)
+
+
+class PreparedPageCopy(_PreparedCall):
+    """mla_page_copy with its arguments marshalled once; ``run()`` issues it.  The
+    tensors must outlive the object."""
+
+    def __init__(self, caches, move_src, move_dst, moves=None, move_rows=None):
+        caches = list(caches)
+        if not caches:
+            raise ValueError("caches must not be empty")
+        views = (PageView * len(caches))(*[_page_view(f"caches[{i}]", t)
+                                           for i, t in enumerate(caches)])
+        pages, page = caches[0].shape[:2]
+        for i, t in enumerate(caches):
+            if tuple(t.shape[:2]) != (pages, page):
+                raise ValueError(f"caches[{i}] must have caches[0]'s pages of as many rows")
+        _tensor("move_src", move_src, (None,), torch.int32)
+        n = move_src.numel()
+        _tensor("move_dst", move_dst, (n,), torch.int32)
+        if moves is not None:
+            _tensor("moves", moves, (1,), torch.int32)
+        if move_rows is not None:
+            _tensor("move_rows", move_rows, (n,), torch.int32)
+        dev = _one_device(move_src=move_src, move_dst=move_dst, moves=moves, move_rows=move_rows,
+                          **{f"caches[{i}]": t for i, t in enumerate(caches)})
+        args = [views, len(caches), page, pages, _ptr(move_src), _ptr(move_dst), _ptr(move_rows),
+                _ptr(moves), n]
+        keep = (views, caches, move_src, move_dst, moves, move_rows)
+        self._prepare("mla_page_copy", args, dev, keep)
+
+
+def mla_page_copy(caches, move_src, move_dst, moves=None, move_rows=None, stream=None) -> None:
+    """Copy pages in every cache tensor of a list at once (keys and values, or
+    latents and RoPE keys, of all layers; at most 128): the first
+    ``move_rows[i]`` rows (None: all) of page ``move_src[i]`` to page
+    ``move_dst[i]``, for i < ``moves[0]`` (None: all entries).
+
+    Caches are [num_pages, page_size, width] or [num_pages, page_size, heads,
+    width], of any type and stride order with contiguous last dimension.
+    Destinations must be distinct, and none a source."""
+    PreparedPageCopy(caches, move_src, move_dst, moves, move_rows).run(stream)

@@ -1,0 +1,186 @@
+// Interface between the chunk attention's entry point, its planner and its
+// kernels.
+//
+// The queries of one sequence and key/value head are taken as rows: row r is
+// token r / group, head r % group of its group, so that few tokens and many
+// heads fill a tile as well as many tokens and few heads.  A unit is a tile of
+// `bm` such rows; it costs kUnitCost plus one per tile of `bn` cached positions
+// that any of its rows sees.  All units, in order of sequence, key/value head
+// and tile, laid end to end are cut into equal shares, one per CTA, so a unit
+// may fall into several shares: each leaves a part, and the join adds them up.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "mla_internal.h"
+
+namespace mla {
+namespace chunk {
+
+constexpr int kMaxCtas = 512;
+// What a unit costs besides its tiles: its queries, its last wait and its outputs.
+constexpr int kUnitCost = 2;
+// A share does not begin in the first or last kSnap tiles of a unit: a part of one
+// or two tiles costs more to join than to do.
+constexpr int kSnap = 2;
+// The least a share holds, above what the snaps can take from it.
+constexpr int kMinShare = kUnitCost + 2 * kSnap + 2;
+
+// Where a share begins: a unit and a tile within it (b == batch: behind the last).
+struct Start {
+  int b, kvh, q, tile;
+};
+// A unit that is cut and begins in this share (its last segment): the shares that
+// hold a part of it, this one and the next ones (0: nothing to join).
+struct Record {
+  int parts, b, kvh, q;
+};
+
+struct Params {
+  const void* q;
+  int64_t q_stride;
+  const void *k, *v;
+  int64_t page_stride, row_stride, head_stride;
+  const float *k_scale, *v_scale;
+  const int32_t *kept, *lens, *row_start, *table;
+  void* out;
+  float* lse;
+  // workspace
+  Start* starts;     // [ctas + 1]
+  Record* rec;       // [ctas]
+  long long* base;   // [batch + 1] cost before each sequence
+  float2* part_ml;   // [2 * ctas][bm] running maximum (base 2) and sum
+  float* part_o;     // [2 * ctas][bm][dp] unnormalised
+  int heads, kv_heads, group, dim, dp, batch, rows, page, width, num_pages, window;
+  int capacity;      // rows of a table's pages
+  int bm, bn, ctas;
+  PageDiv page_div, group_div;
+  float scale_log2;  // softmax scale * log2(e)
+};
+
+// One sequence of a step.
+struct Sequence {
+  int row0, tokens;  // its rows of the step
+  int kept, length;  // position of the first one; cached rows
+  int tiles;         // units per key/value head
+
+  __device__ __forceinline__ void load(const Params& p, int b) {
+    const int a = p.row_start[b], z = p.row_start[b + 1];
+    row0 = min(max(a, 0), p.rows);
+    tokens = min(max(z, row0), p.rows) - row0;
+    kept = max(p.kept[b], 0);
+    length = min(max(p.lens[b], 0), p.capacity);
+    // (rows * heads < 2^31)
+    tiles = (tokens * p.group + p.bm - 1) / p.bm;
+  }
+};
+
+// What one unit covers.
+struct Unit {
+  int r0, r1;        // rows of its sequence and head: r0 .. r1 - 1
+  int lo, hi;        // positions that any of its rows sees: lo .. hi - 1
+  int tile0, tiles;  // tiles of bn positions
+
+  __device__ __forceinline__ void set(const Params& p, const Sequence& s, int q) {
+    r0 = q * p.bm;
+    r1 = min(r0 + p.bm, s.tokens * p.group);
+    const int first = p.group_div(r0), last = p.group_div(r1 - 1);
+    hi = (int)min((long long)s.kept + last + 1, (long long)s.length);
+    lo = p.window ? (int)min(max((long long)s.kept + first + 1 - p.window, 0ll), (long long)hi) : 0;
+    tile0 = lo / p.bn;
+    tiles = hi > lo ? (hi - 1) / p.bn + 1 - tile0 : 0;
+  }
+};
+
+// Last position token i sees, and the first one.
+__device__ __forceinline__ int last_seen(const Sequence& s, int i) {
+  return (int)min((long long)s.kept + i, (long long)s.length - 1);
+}
+__device__ __forceinline__ int first_seen(const Params& p, const Sequence& s, int i) {
+  return p.window ? (int)min(max((long long)s.kept + i + 1 - p.window, 0ll), 2147483647ll) : 0;
+}
+
+// The units of one share in order, with the segment of each that belongs to it.
+// Every thread of a warp calls it with the same state.
+struct Walk {
+  Start at, end;
+  Sequence seq;
+  Unit unit;
+  int t0, t1;        // tiles of the unit: t0 .. t1 - 1
+  bool first, last;  // the unit's first tile, its last one are among them
+  bool loaded;
+
+  __device__ __forceinline__ void begin(const Params& p, int cta) {
+    at = p.starts[cta];
+    end = p.starts[cta + 1];
+    loaded = false;
+  }
+  // The next segment; false behind the last.
+  __device__ __forceinline__ bool next(const Params& p) {
+    if (at.b == end.b && at.kvh == end.kvh && at.q == end.q && at.tile >= end.tile) return false;
+    // (a workspace that another call is writing at the same time gives wrong
+    // results, but no address outside this call's buffers)
+    if (at.b < 0 || at.b >= p.batch || at.kvh < 0 || at.kvh >= p.kv_heads || at.tile < 0)
+      return false;
+    if (!loaded) {
+      seq.load(p, at.b);
+      loaded = true;
+    }
+    if (at.q < 0 || at.q >= seq.tiles) return false;
+    unit.set(p, seq, at.q);
+    if (at.tile > unit.tiles) return false;
+    t0 = at.tile;
+    t1 = unit.tiles;
+    if (at.b == end.b && at.kvh == end.kvh && at.q == end.q) t1 = min(t1, end.tile);
+    first = t0 == 0;
+    last = t1 == unit.tiles;
+    return true;
+  }
+  // Past the segment.
+  __device__ __forceinline__ void advance(const Params& p) {
+    if (!last) {
+      at = end;
+      return;
+    }
+    at.tile = 0;
+    if (++at.q < seq.tiles) return;
+    at.q = 0;
+    if (++at.kvh < p.kv_heads) return;
+    at.kvh = 0;
+    at.b = next_sequence(p, at.b + 1);
+    loaded = false;
+  }
+  // The first sequence at or behind b that has rows, 32 at a time; `batch` if none.
+  __device__ __forceinline__ int next_sequence(const Params& p, int b) const {
+    const int lane = threadIdx.x & 31;
+    for (; b < p.batch; b += 32) {
+      const int x = b + lane;
+      bool some = false;
+      if (x < p.batch && x <= end.b) {
+        const int a = min(max(p.row_start[x], 0), p.rows), z = min(p.row_start[x + 1], p.rows);
+        some = z > a;
+      }
+      const unsigned any = __ballot_sync(~0u, some);
+      if (any) return b + __ffs(any) - 1;
+      if (b + 32 > end.b) break;
+    }
+    return p.batch;
+  }
+};
+
+// Element types of a call: q/out and cache bf16; q/out bf16 beside an e4m3
+// cache; all fp32.
+enum Kind { kBf16 = 0, kE4m3 = 1, kFp32 = 2 };
+
+struct Kernel {
+  int bm, bn, dp, threads, smem, occupancy;
+  cudaError_t (*launch)(const Params& p, int ctas, cudaStream_t stream);
+};
+Kernel kernel_cores(int kind, int dim);
+
+int cores_status(bool clear);
+
+}  // namespace chunk
+}  // namespace mla

@@ -1,0 +1,320 @@
+// Attention of a step's new rows over a paged key/value cache on CUDA cores.
+//
+// A CTA of 256 threads takes 64 query rows (tokens times the heads of one group)
+// against tiles of 64 cached positions: S = Q K^T with a 4 x 4 block of S to a
+// thread, a running maximum and sum per row in registers, P through shared
+// memory, and O += P V with 4 rows of DP / 16 columns to a thread.  Everything
+// is held and summed in fp32.
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "chunk_attention.h"
+#include "sm103_ptx.cuh"
+
+namespace mla {
+
+static __device__ int g_chunk_cores_status;
+
+namespace chunk {
+
+int cores_status(bool clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_chunk_cores_status, sizeof(int)) != cudaSuccess) return -1;
+  if (clear && v != 0) {
+    const int z = 0;
+    if (cudaMemcpyToSymbol(g_chunk_cores_status, &z, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
+}
+
+namespace {
+
+constexpr int kBM = 64, kBN = 64, kThreads = 256;
+
+template <int DP>
+struct Layout {
+  static constexpr int LD = DP + 4;   // floats of a row: 16-byte reads of eight rows meet no bank twice
+  static constexpr int LP = kBN + 4;
+  static constexpr int SMEM = (3 * 64 * LD + kBM * LP) * 4;
+  static constexpr int OCC = 2 * (SMEM + 1024) <= 227 * 1024 ? 2 : 1;
+};
+
+__device__ __forceinline__ void put16(float* dst, const float* src) {
+  *reinterpret_cast<float4*>(dst) = *reinterpret_cast<const float4*>(src);
+}
+__device__ __forceinline__ void put16(float* dst, const __nv_bfloat16* src) {
+  const uint4 r = *reinterpret_cast<const uint4*>(src);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    dst[2 * i] = __uint_as_float(w[i] << 16);
+    dst[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void put16(float* dst, const __nv_fp8_e4m3* src) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) dst[i] = float(src[i]);
+}
+
+template <typename T, typename CT, int DP>
+__global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(const Params p) {
+  using L = Layout<DP>;
+  constexpr int LD = L::LD, LP = L::LP, NO = DP / 32;
+  extern __shared__ float4 s_raw[];
+  float* sQ = reinterpret_cast<float*>(s_raw);
+  float* sK = sQ + 64 * LD;
+  float* sV = sK + 64 * LD;
+  float* sP = sV + 64 * LD;
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const int cta = blockIdx.x;
+  sm103::pdl_wait();
+  // columns past the heads' width stay zero
+  for (int i = tid; i < 3 * 64 * LD; i += kThreads) sQ[i] = 0.f;
+  __syncthreads();
+  Walk w;
+  w.begin(p, cta);
+  for (; w.next(p); w.advance(p)) {
+    const Sequence& s = w.seq;
+    const Unit& u = w.unit;
+    const int kvh = w.at.kvh, rows = u.r1 - u.r0;
+    __syncthreads();  // the queries before are used up
+    {
+      constexpr int N = 16 / (int)sizeof(T);
+      const int vecs = p.dim / N;
+      for (int x = tid; x < 64 * vecs; x += kThreads) {
+        const int r = x / vecs, c = (x - r * vecs) * N;
+        if (r >= rows) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) sQ[r * LD + c + e] = 0.f;
+          continue;
+        }
+        const int i = p.group_div(u.r0 + r), j = u.r0 + r - i * p.group;
+        put16(sQ + r * LD + c, (const T*)p.q + (int64_t)(s.row0 + i) * p.q_stride +
+                                   (int64_t)(kvh * p.group + j) * p.dim + c);
+      }
+    }
+    int first[4], last[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int i = p.group_div(u.r0 + min(ty * 4 + a, rows - 1));
+      first[a] = first_seen(p, s, i);
+      last[a] = last_seen(s, i);
+    }
+    // positions that every row of the unit sees
+    const int all0 = first_seen(p, s, p.group_div(u.r1 - 1)), all1 = last_seen(s, p.group_div(u.r0));
+    const float ks = p.k_scale ? p.k_scale[kvh] : 1.f;
+    // (a scale that is no finite number makes its heads NaN)
+    const float sl2 = isfinite(ks) ? p.scale_log2 * ks : NAN;
+    float m[4], l[4], o[4][2 * NO];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      m[a] = -INFINITY;
+      l[a] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2 * NO; ++c) o[a][c] = 0.f;
+    }
+    for (int t = w.t0; t < w.t1; ++t) {
+      const int pos0 = (u.tile0 + t) * kBN;
+      __syncthreads();  // the tile before is used up
+      {
+        constexpr int N = 16 / (int)sizeof(CT);
+        const int vecs = p.dim / N;
+        for (int x = tid; x < 64 * vecs; x += kThreads) {
+          const int r = x / vecs, c = (x - r * vecs) * N, pos = pos0 + r;
+          bool have = pos >= u.lo && pos < u.hi;
+          int64_t at = 0;
+          if (have) {
+            const int pg = p.page_div(pos);
+            const int id = p.table[(int64_t)w.at.b * p.width + pg];
+            if (id < 0 || id >= p.num_pages) {
+              atomicCAS(&g_chunk_cores_status, 0, kBadPageSite);
+              have = false;
+            } else {
+              at = id * p.page_stride + (int64_t)(pos - pg * p.page) * p.row_stride +
+                   kvh * p.head_stride + c;
+            }
+          }
+          if (have) {
+            put16(sK + r * LD + c, (const CT*)p.k + at);
+            put16(sV + r * LD + c, (const CT*)p.v + at);
+          } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) sK[r * LD + c + e] = sV[r * LD + c + e] = 0.f;
+          }
+        }
+      }
+      __syncthreads();
+      float x[4][4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) x[a][b] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < DP; d += 4) {
+        float4 qv[4], kv[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+          qv[a] = *reinterpret_cast<const float4*>(sQ + (ty * 4 + a) * LD + d);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          kv[b] = *reinterpret_cast<const float4*>(sK + (tx + 16 * b) * LD + d);
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            x[a][b] = fmaf(qv[a].x, kv[b].x, x[a][b]);
+            x[a][b] = fmaf(qv[a].y, kv[b].y, x[a][b]);
+            x[a][b] = fmaf(qv[a].z, kv[b].z, x[a][b]);
+            x[a][b] = fmaf(qv[a].w, kv[b].w, x[a][b]);
+          }
+      }
+      const bool edge = pos0 < all0 || pos0 + kBN - 1 > all1;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int pos = pos0 + tx + 16 * b;
+          x[a][b] = !edge || (pos >= first[a] && pos <= last[a]) ? x[a][b] * sl2 : -INFINITY;
+          top = fmaxf(top, x[a][b]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        const float mn = fmaxf(m[a], top), base = mn == -INFINITY ? 0.f : mn;
+        const float f = sm103::ex2(m[a] - base);
+        m[a] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          x[a][b] = sm103::ex2(x[a][b] - base);
+          sum += x[a][b];
+          sP[(ty * 4 + a) * LP + tx + 16 * b] = x[a][b];
+        }
+        l[a] = l[a] * f + sum;  // this thread's columns; the 16 threads' sums meet at the end
+        if (f != 1.f) {
+#pragma unroll
+          for (int c = 0; c < 2 * NO; ++c) o[a][c] *= f;
+        }
+      }
+      __syncwarp();  // a row's weights are made and used by one warp
+      auto products = [&](auto masked) {
+#pragma unroll 2
+        for (int k = 0; k < kBN; k += 4) {
+          float pw[4][4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const float4 y = *reinterpret_cast<const float4*>(sP + (ty * 4 + a) * LP + k);
+            pw[a][0] = y.x; pw[a][1] = y.y; pw[a][2] = y.z; pw[a][3] = y.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 vv[NO];
+#pragma unroll
+            for (int c = 0; c < NO; ++c)
+              vv[c] = *reinterpret_cast<const float2*>(sV + (k + e) * LD + 2 * tx + 32 * c);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              // a hidden position's value may be anything, also what zero times it is not zero
+              if (decltype(masked)::value && pw[a][e] == 0.f) continue;
+#pragma unroll
+              for (int c = 0; c < NO; ++c) {
+                o[a][2 * c] = fmaf(pw[a][e], vv[c].x, o[a][2 * c]);
+                o[a][2 * c + 1] = fmaf(pw[a][e], vv[c].y, o[a][2 * c + 1]);
+              }
+            }
+          }
+        }
+      };
+      if (edge) products(std::true_type());
+      else products(std::false_type());
+      __syncwarp();
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) l[a] += __shfl_xor_sync(~0u, l[a], d);
+    }
+    const bool whole = w.first && w.last;
+    const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
+    const int64_t slot = 2 * cta + (w.first ? 1 : 0);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int r = ty * 4 + a;
+      if (r >= rows) continue;
+      if (!whole) {
+        if (tx == 0) p.part_ml[slot * kBM + r] = make_float2(m[a], l[a]);
+        float* dst = p.part_o + (slot * kBM + r) * p.dp + 2 * tx;
+#pragma unroll
+        for (int c = 0; c < NO; ++c)
+          *reinterpret_cast<float2*>(dst + 32 * c) = make_float2(o[a][2 * c], o[a][2 * c + 1]);
+        continue;
+      }
+      const int i = p.group_div(u.r0 + r), j = u.r0 + r - i * p.group;
+      const int64_t head = (int64_t)(s.row0 + i) * p.heads + kvh * p.group + j;
+      const float inv = l[a] == 0.f ? 0.f : vs / l[a];
+#pragma unroll
+      for (int c = 0; c < NO; ++c) {
+        const int col = 2 * tx + 32 * c;
+        if (col >= p.dim) continue;
+        const float y0 = o[a][2 * c] * inv, y1 = o[a][2 * c + 1] * inv;
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float2*>((float*)p.out + head * p.dim + col) = make_float2(y0, y1);
+        else
+          *reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.out + head * p.dim + col) =
+              sm103::pack_bf16(y0, y1);
+      }
+      if (tx == 0 && p.lse)
+        p.lse[head] = l[a] == 0.f ? -INFINITY : (m[a] + log2f(l[a])) * 0.6931471805599453f;
+    }
+  }
+}
+
+template <typename T, typename CT, int DP>
+cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  auto* fn = chunk_cores_kernel<T, CT, DP>;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Layout<DP>::SMEM);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  KernelTimer kt("chunk_cores", stream);
+  return launch_dependent(fn, dim3((unsigned)ctas), dim3(kThreads), Layout<DP>::SMEM, stream, p);
+}
+
+template <typename T, typename CT, int DP>
+Kernel make() {
+  return {kBM, kBN, DP, kThreads, Layout<DP>::SMEM, Layout<DP>::OCC, launch<T, CT, DP>};
+}
+
+template <typename T, typename CT>
+Kernel pick(int dim) {
+  return dim <= 64    ? make<T, CT, 64>()
+         : dim <= 96  ? make<T, CT, 96>()
+         : dim <= 128 ? make<T, CT, 128>()
+         : dim <= 192 ? make<T, CT, 192>()
+                      : make<T, CT, 256>();
+}
+
+}  // namespace
+
+Kernel kernel_cores(int kind, int dim) {
+  return kind == kFp32   ? pick<float, float>(dim)
+         : kind == kE4m3 ? pick<__nv_bfloat16, __nv_fp8_e4m3>(dim)
+                         : pick<__nv_bfloat16, __nv_bfloat16>(dim);
+}
+
+}  // namespace chunk
+}  // namespace mla

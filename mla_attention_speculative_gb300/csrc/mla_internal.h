@@ -138,6 +138,9 @@ int indexer_device_status(bool clear);
 // attention (kBadPageSite or 0); they synchronise.
 int paged_device_status(bool clear);
 int decode_device_status(bool clear);
+// ... of the chunk attention and of the page pool kernels.
+int chunk_device_status(bool clear);
+int pool_device_status(bool clear);
 
 // Division by a page size of 1 .. 2^31 - 1, of positions below 2^31.  With
 // 2^(s-1) < page <= 2^s, m = ceil(2^(31+s) / page) < 2^32 overshoots by less
