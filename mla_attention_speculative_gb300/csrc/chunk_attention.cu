@@ -12,7 +12,16 @@
 
 namespace mla {
 
-int chunk_device_status(bool clear) { return chunk::cores_status(clear); }
+int chunk_device_status(bool clear) {
+  const int words[4] = {chunk::tma_status(clear), chunk::rows_status(clear),
+                        chunk::convert_status(clear), chunk::cores_status(clear)};
+  int v = 0;
+  for (int w : words) {
+    if (w < 0) return -1;
+    if (v == 0) v = w;
+  }
+  return v;
+}
 
 namespace chunk {
 namespace {
@@ -288,7 +297,9 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const Params p
               sm103::pack_bf16(a.x * inv, a.y * inv), sm103::pack_bf16(a.z * inv, a.w * inv));
       }
       if (i0 == 0 && p.lse)
-        p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        p.lse[head] =
+            L == 0.f ? -INFINITY
+                     : (M + (log2f(L) - (kind == kE4m3 ? kShift : 0.f))) * 0.6931471805599453f;
     }
     __syncthreads();
   }
@@ -302,7 +313,13 @@ int kind_of(const mla_kv_geometry_t* g) {
   return g->dtype == MLA_DTYPE_FP32 ? kFp32 : g->cache_dtype == MLA_DTYPE_E4M3 ? kE4m3 : kBf16;
 }
 
-Kernel kernel_of(const mla_kv_geometry_t* g) { return kernel_cores(kind_of(g), g->head_dim); }
+Kernel kernel_of(const mla_kv_geometry_t* g, int page_size) {
+  const int kind = kind_of(g), dim = g->head_dim;
+  return kind == kFp32        ? kernel_cores(dim)
+         : kind == kE4m3      ? kernel_convert(dim)
+         : page_size % 8 == 0 ? kernel_tma(dim)
+                              : kernel_rows(dim);
+}
 
 struct Plan {
   Kernel k;
@@ -315,7 +332,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 Plan make_plan(const mla_kv_geometry_t* g, int batch, int rows, int page_size, int max_pages) {
   Plan d;
-  d.k = kernel_of(g);
+  d.k = kernel_of(g, page_size);
   const int group = g->num_heads / g->num_kv_heads;
   const int64_t tiles = ((int64_t)page_size * max_pages + d.k.bn - 1) / d.k.bn;
   // no sequence has more than `rows` rows, and each may end in a unit of its own

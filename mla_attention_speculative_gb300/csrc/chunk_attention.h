@@ -174,13 +174,24 @@ struct Walk {
 // cache; all fp32.
 enum Kind { kBf16 = 0, kE4m3 = 1, kFp32 = 2 };
 
+// Weights beside an e4m3 cache are scaled by 2^kShift.
+constexpr float kShift = 7.f;
+
 struct Kernel {
   int bm, bn, dp, threads, smem, occupancy;
   cudaError_t (*launch)(const Params& p, int ctas, cudaStream_t stream);
 };
-Kernel kernel_cores(int kind, int dim);
+// CUDA cores (fp32); tensor cores with a bf16 cache in pages of whole runs of 8
+// rows, in any other pages, and with an e4m3 cache.
+Kernel kernel_cores(int dim);
+Kernel kernel_tma(int dim);
+Kernel kernel_rows(int dim);
+Kernel kernel_convert(int dim);
 
 int cores_status(bool clear);
+int tma_status(bool clear);
+int rows_status(bool clear);
+int convert_status(bool clear);
 
 }  // namespace chunk
 }  // namespace mla

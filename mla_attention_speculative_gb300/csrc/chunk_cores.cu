@@ -1,13 +1,11 @@
-// Attention of a step's new rows over a paged key/value cache on CUDA cores.
+// Attention of a step's new rows over a paged key/value cache on CUDA cores, for
+// fp32.
 //
 // A CTA of 256 threads takes 64 query rows (tokens times the heads of one group)
 // against tiles of 64 cached positions: S = Q K^T with a 4 x 4 block of S to a
 // thread, a running maximum and sum per row in registers, P through shared
 // memory, and O += P V with 4 rows of DP / 16 columns to a thread.  Everything
 // is held and summed in fp32.
-
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <mutex>
 #include <type_traits>
@@ -46,21 +44,7 @@ struct Layout {
 __device__ __forceinline__ void put16(float* dst, const float* src) {
   *reinterpret_cast<float4*>(dst) = *reinterpret_cast<const float4*>(src);
 }
-__device__ __forceinline__ void put16(float* dst, const __nv_bfloat16* src) {
-  const uint4 r = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    dst[2 * i] = __uint_as_float(w[i] << 16);
-    dst[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void put16(float* dst, const __nv_fp8_e4m3* src) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) dst[i] = float(src[i]);
-}
-
-template <typename T, typename CT, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(const Params p) {
   using L = Layout<DP>;
   constexpr int LD = L::LD, LP = L::LP, NO = DP / 32;
@@ -83,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
     const int kvh = w.at.kvh, rows = u.r1 - u.r0;
     __syncthreads();  // the queries before are used up
     {
-      constexpr int N = 16 / (int)sizeof(T);
+      constexpr int N = 4;
       const int vecs = p.dim / N;
       for (int x = tid; x < 64 * vecs; x += kThreads) {
         const int r = x / vecs, c = (x - r * vecs) * N;
@@ -93,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
           continue;
         }
         const int i = p.group_div(u.r0 + r), j = u.r0 + r - i * p.group;
-        put16(sQ + r * LD + c, (const T*)p.q + (int64_t)(s.row0 + i) * p.q_stride +
+        put16(sQ + r * LD + c, (const float*)p.q + (int64_t)(s.row0 + i) * p.q_stride +
                                    (int64_t)(kvh * p.group + j) * p.dim + c);
       }
     }
@@ -106,9 +90,7 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
     }
     // positions that every row of the unit sees
     const int all0 = first_seen(p, s, p.group_div(u.r1 - 1)), all1 = last_seen(s, p.group_div(u.r0));
-    const float ks = p.k_scale ? p.k_scale[kvh] : 1.f;
-    // (a scale that is no finite number makes its heads NaN)
-    const float sl2 = isfinite(ks) ? p.scale_log2 * ks : NAN;
+    const float sl2 = p.scale_log2;
     float m[4], l[4], o[4][2 * NO];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
@@ -121,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
       const int pos0 = (u.tile0 + t) * kBN;
       __syncthreads();  // the tile before is used up
       {
-        constexpr int N = 16 / (int)sizeof(CT);
+        constexpr int N = 4;
         const int vecs = p.dim / N;
         for (int x = tid; x < 64 * vecs; x += kThreads) {
           const int r = x / vecs, c = (x - r * vecs) * N, pos = pos0 + r;
@@ -139,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
             }
           }
           if (have) {
-            put16(sK + r * LD + c, (const CT*)p.k + at);
-            put16(sV + r * LD + c, (const CT*)p.v + at);
+            put16(sK + r * LD + c, (const float*)p.k + at);
+            put16(sV + r * LD + c, (const float*)p.v + at);
           } else {
 #pragma unroll
             for (int e = 0; e < N; ++e) sK[r * LD + c + e] = sV[r * LD + c + e] = 0.f;
@@ -239,7 +221,6 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
       for (int d = 8; d > 0; d >>= 1) l[a] += __shfl_xor_sync(~0u, l[a], d);
     }
     const bool whole = w.first && w.last;
-    const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
     const int64_t slot = 2 * cta + (w.first ? 1 : 0);
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
@@ -255,17 +236,13 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
       }
       const int i = p.group_div(u.r0 + r), j = u.r0 + r - i * p.group;
       const int64_t head = (int64_t)(s.row0 + i) * p.heads + kvh * p.group + j;
-      const float inv = l[a] == 0.f ? 0.f : vs / l[a];
+      const float inv = l[a] == 0.f ? 0.f : 1.f / l[a];
 #pragma unroll
       for (int c = 0; c < NO; ++c) {
         const int col = 2 * tx + 32 * c;
         if (col >= p.dim) continue;
         const float y0 = o[a][2 * c] * inv, y1 = o[a][2 * c + 1] * inv;
-        if constexpr (sizeof(T) == 4)
-          *reinterpret_cast<float2*>((float*)p.out + head * p.dim + col) = make_float2(y0, y1);
-        else
-          *reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.out + head * p.dim + col) =
-              sm103::pack_bf16(y0, y1);
+        *reinterpret_cast<float2*>((float*)p.out + head * p.dim + col) = make_float2(y0, y1);
       }
       if (tx == 0 && p.lse)
         p.lse[head] = l[a] == 0.f ? -INFINITY : (m[a] + log2f(l[a])) * 0.6931471805599453f;
@@ -273,14 +250,14 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
   }
 }
 
-template <typename T, typename CT, int DP>
+template <int DP>
 cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
   static std::mutex mu;
   static bool done[64] = {};
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto* fn = chunk_cores_kernel<T, CT, DP>;
+  auto* fn = chunk_cores_kernel<DP>;
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
@@ -294,26 +271,19 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
   return launch_dependent(fn, dim3((unsigned)ctas), dim3(kThreads), Layout<DP>::SMEM, stream, p);
 }
 
-template <typename T, typename CT, int DP>
+template <int DP>
 Kernel make() {
-  return {kBM, kBN, DP, kThreads, Layout<DP>::SMEM, Layout<DP>::OCC, launch<T, CT, DP>};
-}
-
-template <typename T, typename CT>
-Kernel pick(int dim) {
-  return dim <= 64    ? make<T, CT, 64>()
-         : dim <= 96  ? make<T, CT, 96>()
-         : dim <= 128 ? make<T, CT, 128>()
-         : dim <= 192 ? make<T, CT, 192>()
-                      : make<T, CT, 256>();
+  return {kBM, kBN, DP, kThreads, Layout<DP>::SMEM, Layout<DP>::OCC, launch<DP>};
 }
 
 }  // namespace
 
-Kernel kernel_cores(int kind, int dim) {
-  return kind == kFp32   ? pick<float, float>(dim)
-         : kind == kE4m3 ? pick<__nv_bfloat16, __nv_fp8_e4m3>(dim)
-                         : pick<__nv_bfloat16, __nv_bfloat16>(dim);
+Kernel kernel_cores(int dim) {
+  return dim <= 64    ? make<64>()
+         : dim <= 96  ? make<96>()
+         : dim <= 128 ? make<128>()
+         : dim <= 192 ? make<192>()
+                      : make<256>();
 }
 
 }  // namespace chunk
