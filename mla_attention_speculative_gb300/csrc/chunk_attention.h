@@ -102,14 +102,18 @@ __device__ __forceinline__ int first_seen(const Params& p, const Sequence& s, in
   return p.window ? (int)min(max((long long)s.kept + i + 1 - p.window, 0ll), 2147483647ll) : 0;
 }
 
-// The units of one share in order, with the segment of each that belongs to it.
-// Every thread of a warp calls it with the same state.
-struct Walk {
-  Start at, end;
-  Sequence seq;
+// What a share holds of one unit.
+struct Segment {
   Unit unit;
   int t0, t1;        // tiles of the unit: t0 .. t1 - 1
   bool first, last;  // the unit's first tile, its last one are among them
+};
+
+// The segments of one share in order.  Every thread of a warp calls it with the
+// same state.
+struct Walk {
+  Start at, end;
+  Sequence seq;
   bool loaded;
 
   __device__ __forceinline__ void begin(const Params& p, int cta) {
@@ -117,9 +121,23 @@ struct Walk {
     end = p.starts[cta + 1];
     loaded = false;
   }
+  __device__ __forceinline__ bool in_last() const {
+    return at.b == end.b && at.kvh == end.kvh && at.q == end.q;
+  }
+  // The segment at `at`, whose sequence is loaded.
+  __device__ __forceinline__ Segment segment(const Params& p) const {
+    Segment g;
+    g.unit.set(p, seq, at.q);
+    g.t0 = at.tile;
+    g.t1 = g.unit.tiles;
+    if (in_last()) g.t1 = min(g.t1, end.tile);
+    g.first = g.t0 == 0;
+    g.last = g.t1 == g.unit.tiles;
+    return g;
+  }
   // The next segment; false behind the last.
-  __device__ __forceinline__ bool next(const Params& p) {
-    if (at.b == end.b && at.kvh == end.kvh && at.q == end.q && at.tile >= end.tile) return false;
+  __device__ __forceinline__ bool next(const Params& p, Segment& g) {
+    if (in_last() && at.tile >= end.tile) return false;
     // (a workspace that another call is writing at the same time gives wrong
     // results, but no address outside this call's buffers)
     if (at.b < 0 || at.b >= p.batch || at.kvh < 0 || at.kvh >= p.kv_heads || at.tile < 0)
@@ -129,18 +147,12 @@ struct Walk {
       loaded = true;
     }
     if (at.q < 0 || at.q >= seq.tiles) return false;
-    unit.set(p, seq, at.q);
-    if (at.tile > unit.tiles) return false;
-    t0 = at.tile;
-    t1 = unit.tiles;
-    if (at.b == end.b && at.kvh == end.kvh && at.q == end.q) t1 = min(t1, end.tile);
-    first = t0 == 0;
-    last = t1 == unit.tiles;
-    return true;
+    g = segment(p);
+    return at.tile <= g.unit.tiles;
   }
   // Past the segment.
-  __device__ __forceinline__ void advance(const Params& p) {
-    if (!last) {
+  __device__ __forceinline__ void advance(const Params& p, const Segment& g) {
+    if (!g.last) {
       at = end;
       return;
     }

@@ -61,9 +61,10 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
   __syncthreads();
   Walk w;
   w.begin(p, cta);
-  for (; w.next(p); w.advance(p)) {
+  Segment g;
+  for (; w.next(p, g); w.advance(p, g)) {
     const Sequence& s = w.seq;
-    const Unit& u = w.unit;
+    const Unit& u = g.unit;
     const int kvh = w.at.kvh, rows = u.r1 - u.r0;
     __syncthreads();  // the queries before are used up
     {
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
 #pragma unroll
       for (int c = 0; c < 2 * NO; ++c) o[a][c] = 0.f;
     }
-    for (int t = w.t0; t < w.t1; ++t) {
+    for (int t = g.t0; t < g.t1; ++t) {
       const int pos0 = (u.tile0 + t) * kBN;
       __syncthreads();  // the tile before is used up
       {
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) l[a] += __shfl_xor_sync(~0u, l[a], d);
     }
-    const bool whole = w.first && w.last;
-    const int64_t slot = 2 * cta + (w.first ? 1 : 0);
+    const bool whole = g.first && g.last;
+    const int64_t slot = 2 * cta + (g.first ? 1 : 0);
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = ty * 4 + a;

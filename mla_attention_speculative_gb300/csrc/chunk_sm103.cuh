@@ -81,7 +81,7 @@ struct Shape {
   static constexpr int FULL = 0, EMPTY = NB, LANDED = 2 * NB, QFULL = 3 * NB, QEMPTY = QFULL + 2,
                        SFULL = QEMPTY + 1, PFULL = SFULL + 2, OFULL = PFULL + 2,
                        PVDONE = OFULL + 2, DRAIN = PVDONE + 2, BARS = DRAIN + 1;
-  static_assert(BARS * 8 + 16 + 8 * 4 <= 1024, "the barriers do not fit");
+  static_assert(BARS * 8 + 10 * 4 + 4 * NS * sizeof(Walk) <= 1024, "the barriers do not fit");
 };
 
 struct Maps {
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
   uint32_t* slot_word = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* dirty = reinterpret_cast<int*>(slot_word + 2);  // [8], by segment
+  Walk* walks = reinterpret_cast<Walk*>(slot_word + 10);          // [4 * NS], a softmax warp's
   float* q_scale = reinterpret_cast<float*>(tail + 1024);       // kConvert: [NS * 128]
   const uint32_t sQ = smem_u32(smem), sRing = sQ + NS * C::QB, sRaw = sRing + NB * C::SLOT;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
   const uint32_t tmem = *slot_word;
   pdl_wait();
   Walk w;
+  Segment g;
   w.begin(p, cta);
   bool ok = true;
 
@@ -203,10 +205,10 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t uses[2] = {0, 0}, o_uses = 0;
     int seg = 0;                              // segments with tiles before this one
-    for (; w.next(p); w.advance(p)) {
+    for (; w.next(p, g); w.advance(p, g)) {
       const Sequence& sq = w.seq;
-      const Unit& u = w.unit;
-      const int n = w.t1 - w.t0, rows = u.r1 - u.r0, kvh = w.at.kvh;
+      const Unit& u = g.unit;
+      const int n = g.t1 - g.t0, rows = u.r1 - u.r0, kvh = w.at.kvh;
       const bool split = NS == 2 && rows <= 128;  // both streams take the same rows
       const int r = (split ? 0 : 128 * s) + q;
       const int tok = p.group_div(u.r0 + min(r, rows - 1));
@@ -294,29 +296,67 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           sl2 *= q_scale[r];
         }
       }
+      // Where the walk stands waits in shared memory while the scores need the registers.
+      if (lane == 0) walks[warp] = w;
+      __syncwarp();
       // ---- tiles
+      const int tile_pos = (u.tile0 + g.t0) * kBN;
       float top = -INFINITY, m = -INFINITY, l = 0.f;  // the reference, times the scale; the sum
       const int step = split ? 2 : 1;
       int i = split ? s : 0;
       const bool any = i < n;
       for (bool begun = false; i < n; i += step, begun = true) {
         const int x = NS == 2 ? s : (i & 1);
-        const int pos0 = (u.tile0 + w.t0 + i) * kBN;
+        const int pos0 = tile_pos + i * kBN;
         const uint32_t tS = tmem + lane_base + C::TM_S + 128 * x;
         wait_or_fail(ok, bar(C::SFULL + x), uses[x] & 1, 101);
         tc_fence_after();
-        uint32_t v[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(tS + 32 * k, v + 32 * k);
-        tmem_wait_ld<128>(v);
-        if (seen.edge(pos0)) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (pos0 + j < first || pos0 + j > last) v[j] = 0xFF800000u;
-        }
+        // The scores are read twice, for their maximum and for the weights, 32 at a time
+        // with the next 32 on their way: kept in registers, 128 of them spill.
+        uint32_t u0[32], u1[32];
         float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const bool edge = seen.edge(pos0);
+        // f(scores, piece) for the four pieces; the first one is under way
+        auto pieces = [&](auto f) {
+          tmem_wait_ld<32>(u0);
+          tmem_ld32(tS + 32, u1);
+          f(u0, 0);
+          tmem_wait_ld<32>(u1);
+          tmem_ld32(tS + 64, u0);
+          f(u1, 1);
+          tmem_wait_ld<32>(u0);
+          tmem_ld32(tS + 96, u1);
+          f(u0, 2);
+          tmem_wait_ld<32>(u1);
+          f(u1, 3);
+        };
+        auto hide = [&](uint32_t* u, int k) {
 #pragma unroll
-        for (int j = 0; j < 128; ++j) t4[j & 3] = fmaxf(t4[j & 3], __uint_as_float(v[j]));
+          for (int j = 0; j < 32; ++j) {
+            const int pos = pos0 + 32 * k + j;
+            if (pos < first || pos > last) u[j] = 0xFF800000u;
+          }
+        };
+        auto highest = [&](const uint32_t* u) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            t4[(j >> 1) & 3] = fmaxf(t4[(j >> 1) & 3],
+                                     fmaxf(__uint_as_float(u[j]), __uint_as_float(u[j + 1])));
+        };
+        if (edge) {
+          // (few tiles: a loop, so that the code of the others stays together)
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            tmem_ld32(tS + 32 * k, u0);
+            tmem_wait_ld<32>(u0);
+            hide(u0, k);
+            highest(u0);
+          }
+        } else {
+          tmem_ld32(tS, u0);
+          pieces([&](uint32_t* u, int) { highest(u); });
+        }
+        tmem_ld32(tS, u0);
         const float mx = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         const float mn = mx == -INFINITY ? -INFINITY : mx * sl2;
         const bool need = mn > m + 8.f;
@@ -353,31 +393,40 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(shift - base, shift - base);
         const float ref = m == -INFINITY ? 0.f : top;
         uint64_t sum2[2] = {0ull, 0ull};
-        auto weights = [&](auto careful) {
+        auto weights = [&](uint32_t* u, int k, auto careful) {
+          // (step by step for 32 scores, so that no exponential waits for another)
+          float y[32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = __uint_as_float(v[32 * k + 2 * e]);
-              const float b = __uint_as_float(v[32 * k + 2 * e + 1]);
-              float ya, yb;
-              if constexpr (decltype(careful)::value) {
-                ya = fmaf(a - ref, sl2, shift);
-                yb = fmaf(b - ref, sl2, shift);
-              } else {
-                unpack2(fma2(pack2(a, b), sc2, off2), ya, yb);
-              }
-              ya = ex2(ya);
-              yb = ex2(yb);
-              sum2[e & 1] = add2(sum2[e & 1], pack2(ya, yb));
-              pk[e] = HALF ? pack_half(ya, yb) : pack_bf16(ya, yb);
+          for (int e = 0; e < 32; e += 2) {
+            const float a = __uint_as_float(u[e]), b = __uint_as_float(u[e + 1]);
+            if constexpr (decltype(careful)::value) {
+              y[e] = fmaf(a - ref, sl2, shift);
+              y[e + 1] = fmaf(b - ref, sl2, shift);
+            } else {
+              unpack2(fma2(pack2(a, b), sc2, off2), y[e], y[e + 1]);
             }
-            tmem_st16(tS + 16 * k, pk);
           }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = ex2(y[e]);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            sum2[e & 1] = add2(sum2[e & 1], pack2(y[2 * e], y[2 * e + 1]));
+            pk[e] = HALF ? pack_half(y[2 * e], y[2 * e + 1]) : pack_bf16(y[2 * e], y[2 * e + 1]);
+          }
+          tmem_st16(tS + 16 * k, pk);
         };
-        if (large) weights(std::true_type());
-        else weights(std::false_type());
+        if (edge || large) {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            tmem_wait_ld<32>(u0);
+            hide(u0, k);
+            weights(u0, k, std::true_type());
+            if (k < 3) tmem_ld32(tS + 32 * (k + 1), u0);
+          }
+        } else {
+          pieces([&](uint32_t* u, int k) { weights(u, k, std::false_type()); });
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(C::PFULL + x));
@@ -387,14 +436,15 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         l += a + b;
       }
       // ---- outputs
-      const bool whole = w.first && w.last;
-      const bool odd = n > 0;
+      w = const_cast<const Walk&>(walks[warp]);
+      g = w.segment(p);
+      const bool whole = g.first && g.last;
       if (any) {
         wait_or_fail(ok, bar(C::OFULL + s), o_uses & 1, 103);
         ++o_uses;
         tc_fence_after();
       }
-      const bool fix = odd && dirty[seg & 7] == seg;
+      const bool fix = n > 0 && dirty[seg & 7] == seg;
       float f0 = 1.f, f1 = 0.f;
       int c0 = 0, c1 = DP;
       const float2* other = nullptr;
@@ -417,70 +467,71 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       }
       const bool second = split && n > 1;  // stream 1 has an accumulator
       const float vs = HALF && p.v_scale ? p.v_scale[kvh] : 1.f;
-      const float inv = whole ? vs / l : 1.f;
+      const float inv = l == 0.f ? 0.f : vs / l;
       const bool live = r < rows;
       const int i_tok = p.group_div(u.r0 + min(r, rows - 1)),
                 head_in = u.r0 + min(r, rows - 1) - i_tok * p.group;
       const int64_t head = (int64_t)(sq.row0 + i_tok) * p.heads + kvh * p.group + head_in;
-      const int64_t part = (int64_t)(2 * cta + (w.first ? 1 : 0)) * p.bm + r;
+      const int64_t part = (int64_t)(2 * cta + (g.first ? 1 : 0)) * p.bm + r;
       // the accumulators' weights: mine and the other stream's
       const float wa = split && s == 1 ? f1 : f0, wb = split && s == 1 ? f0 : f1;
 #pragma unroll 1
-      for (int c = c0; c < c1; c += 32) {
-        uint32_t o[32];
+      for (int c = c0; c < c1; c += 16) {
+        uint32_t o[16];
         __syncwarp();
         if (n > 0) {
-          tmem_ld32(tmem + lane_base + (NS == 2 && !split ? DP * s : 0) + c, o);
+          tmem_ld16(tmem + lane_base + (NS == 2 && !split ? DP * s : 0) + c, o);
           if (second) {
-            uint32_t o1[32];
-            tmem_ld32(tmem + lane_base + DP + c, o1);
-            tmem_wait_ld<32>(o);
-            tmem_wait_ld<32>(o1);
+            uint32_t o1[16];
+            tmem_ld16(tmem + lane_base + DP + c, o1);
+            tmem_wait_ld<16>(o);
+            tmem_wait_ld<16>(o1);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               // (a stream without weight may hold anything)
               const float a = wa == 0.f ? 0.f : __uint_as_float(o[e]) * wa;
               const float b = wb == 0.f ? 0.f : __uint_as_float(o1[e]) * wb;
               o[e] = __float_as_uint(a + b);
             }
           } else {
-            tmem_wait_ld<32>(o);
+            tmem_wait_ld<16>(o);
           }
         }
-        if (!live) continue;
-        if (l == 0.f) {
+        if (live) {
+          if (l == 0.f) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        } else if (fix) {
-          const int lo = max(first, (u.tile0 + w.t0) * kBN),
-                    hi = min(last, (u.tile0 + w.t1) * kBN - 1);
-          for (int e = 0; e < 32; ++e) {
-            if (c + e >= p.dim) continue;
-            const float y = odd_values<FEED>(p, w.at.b, kvh, c + e, lo, hi, seen.lo, seen.hi);
-            // (the array stays in registers: no index at run time)
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
+          } else if (fix) {
+            const int lo = max(first, (u.tile0 + g.t0) * kBN),
+                      hi = min(last, (u.tile0 + g.t1) * kBN - 1);
+#pragma unroll 1
+            for (int e = 0; e < 16; ++e) {
+              if (c + e >= p.dim) continue;
+              const float y = odd_values<FEED>(p, w.at.b, kvh, c + e, lo, hi, seen.lo, seen.hi);
+              // (the array stays in registers: no index at run time)
 #pragma unroll
-            for (int g = 0; g < 32; ++g)
-              if (g == e) o[g] = __float_as_uint(__uint_as_float(o[g]) + y);
-          }
-        }
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e >= p.dim) continue;
-            uint32_t y[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float a = __uint_as_float(o[e + 2 * g]), b = __uint_as_float(o[e + 2 * g + 1]);
-              y[g] = l == 0.f ? 0u : pack_bf16(a * inv, b * inv);
+              for (int k = 0; k < 16; ++k)
+                if (k == e) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
             }
-            *reinterpret_cast<uint4*>((__nv_bfloat16*)p.out + head * p.dim + c + e) =
-                make_uint4(y[0], y[1], y[2], y[3]);
           }
-        } else {
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(p.part_o + part * p.dp + c + e) =
-                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 16; e += 8) {
+              if (c + e >= p.dim) continue;
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                y[k] = pack_bf16(__uint_as_float(o[e + 2 * k]) * inv,
+                                 __uint_as_float(o[e + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>((__nv_bfloat16*)p.out + head * p.dim + c + e) =
+                  make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(p.part_o + part * p.dp + c + e) =
+                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
         }
       }
       if (live && (!split || s == 0)) {
@@ -501,8 +552,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     const bool whole = nk == DP / 16;
     uint32_t at = 0;                   // blocks before this segment
     uint32_t puses[2] = {0, 0}, q_uses[2] = {0, 0};
-    for (; w.next(p); w.advance(p)) {
-      const int n = w.t1 - w.t0, rows = w.unit.r1 - w.unit.r0;
+    for (; w.next(p, g); w.advance(p, g)) {
+      const int n = g.t1 - g.t0, rows = g.unit.r1 - g.unit.r0;
       if (n == 0) continue;
       const bool split = NS == 2 && rows <= 128;
       if (lane == 0) {
@@ -614,15 +665,15 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     uint32_t at = 0, issued = 0;
     const int nbox = kBN / maps.box;
     const int rb = lane % nbox, ch = lane / nbox;
-    for (; w.next(p); w.advance(p)) {
-      const int n = w.t1 - w.t0;
-      const Unit& u = w.unit;
+    for (; w.next(p, g); w.advance(p, g)) {
+      const int n = g.t1 - g.t0;
+      const Unit& u = g.unit;
       const int kvh = w.at.kvh;
       const Seen seen(p, w.seq, u);
       // this lane's page of tile i (num_pages, all of whose boxes read zeros, for an id
       // outside the pool) and its first row there, where somebody sees these rows
       auto look = [&](int i, int& id, int& row) {
-        const int pos = (u.tile0 + w.t0 + i) * kBN + rb * maps.box;
+        const int pos = (u.tile0 + g.t0 + i) * kBN + rb * maps.box;
         id = -1;
         row = 0;
         if (i >= n || pos >= u.hi || pos + maps.box <= u.lo) return;
@@ -649,7 +700,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         }
       };
       auto visible = [&](int i) {
-        const int pos = (u.tile0 + w.t0 + i) * kBN + rb * maps.box;
+        const int pos = (u.tile0 + g.t0 + i) * kBN + rb * maps.box;
         return i < n && pos < u.hi && pos + maps.box > u.lo;
       };
       auto valid = [&](int id) {
@@ -672,7 +723,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           load(&maps.k, k_place(i + 1), id1, row1, have1, C::FULL);
         }
         load(&maps.v, v_place(i, n), id0, row0, have0,
-             seen.edge((u.tile0 + w.t0 + i) * kBN) ? C::LANDED : C::FULL);
+             seen.edge((u.tile0 + g.t0 + i) * kBN) ? C::LANDED : C::FULL);
         id0 = id1;
         row0 = row1;
         have0 = have1;
@@ -690,13 +741,13 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     // (its blocks arrive on a barrier of their own, the ring's is for the MMA)
     uint32_t at = 0, uses = 0;
     int seg = 0;
-    for (; w.next(p); w.advance(p)) {
-      const int n = w.t1 - w.t0;
-      const Unit& u = w.unit;
+    for (; w.next(p, g); w.advance(p, g)) {
+      const int n = g.t1 - g.t0;
+      const Unit& u = g.unit;
       if (n == 0) continue;
       const Seen seen(p, w.seq, u);
       for (int i = 0; i < n && ok; ++i) {
-        const int pos0 = (u.tile0 + w.t0 + i) * kBN;
+        const int pos0 = (u.tile0 + g.t0 + i) * kBN;
         if (!seen.edge(pos0)) continue;
         for (int blk = 0; blk < NBLK && ok; ++blk) {
           const uint32_t pos = at + (uint32_t)(v_place(i, n) * NBLK + blk), sl = pos % NB;
@@ -759,15 +810,16 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     // The blocks of this share in the ring's order.
     struct Blocks {
       Walk w;
+      Segment g;
       int n, i, blk;
       bool value, more;
       uint32_t pos;
       int seg;
       __device__ __forceinline__ void settle(const Params& p) {
-        while ((more = w.next(p))) {
-          n = w.t1 - w.t0;
+        while ((more = w.next(p, g))) {
+          n = g.t1 - g.t0;
           if (n > 0) break;
-          w.advance(p);
+          w.advance(p, g);
         }
         i = 0;
         blk = 0;
@@ -786,7 +838,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         // K0 K1 V0 K2 V1 .. V(n-1): i is the tile
         if (value) {
           if (i == n - 1) {
-            w.advance(p);
+            w.advance(p, g);
             ++seg;
             settle(p);
             return;
@@ -804,7 +856,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           i = i == 0 ? 0 : i - 1;
         }
       }
-      __device__ __forceinline__ int pos0() const { return (w.unit.tile0 + w.t0 + i) * kBN; }
+      __device__ __forceinline__ int pos0() const { return (g.unit.tile0 + g.t0 + i) * kBN; }
     };
     // Calls f(row, chunk, element offset or -1) for this thread's 16-byte chunks of a block.
     auto chunks_of = [&](const Blocks& z, auto f) {
@@ -818,7 +870,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       for (int row = tid / per_row; row < kBN; row += step) {
         const int pos = pos0 + row;
         int64_t off = -1;
-        if (pos >= z.w.unit.lo && pos < z.w.unit.hi && col < p.dim) {
+        if (pos >= z.g.unit.lo && pos < z.g.unit.hi && col < p.dim) {
           const int pg = p.page_div(pos);
           const int id = p.table[(int64_t)z.w.at.b * p.width + pg];
           if (id >= 0 && id < p.num_pages)
@@ -840,7 +892,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           cp_async16(sRing + sl * C::SLOT + (c >> 3) * 16384 + sw128_offset(row, (c & 7) * 8),
                      off >= 0 ? base + off * EB : base, off >= 0 ? 16u : 0u);
         });
-        const bool edge = z.value && Seen(p, z.w.seq, z.w.unit).edge(z.pos0());
+        const bool edge = z.value && Seen(p, z.w.seq, z.g.unit).edge(z.pos0());
         cp_async_mbar_arrive(bar((edge ? C::LANDED : C::FULL) + sl));
       }
       cp_async_wait_all();
@@ -872,7 +924,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         const uint32_t sl = z.pos % NB;
         if (z.pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (z.pos / NB - 1) & 1, 122);
         if (!ok) break;
-        const Seen seen(p, z.w.seq, z.w.unit);
+        const Seen seen(p, z.w.seq, z.g.unit);
         const bool edge = z.value && seen.edge(z.pos0());
         bool met = false;
         const bool narrow = DP - 128 * z.blk < 128 && DP > 128;

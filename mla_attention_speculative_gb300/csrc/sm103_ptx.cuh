@@ -163,6 +163,16 @@ __device__ __forceinline__ void bulk_wait_read1() {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// Give registers back, or take more, for all four warps of a warpgroup (multiples of
+// 8; the block's shares may not exceed what it was launched with).
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 // 2^x on the SFU (approximate, flushes denormals; 2^-inf = +0).
 __device__ __forceinline__ float ex2(float x) {
   float y;
