@@ -30,19 +30,14 @@ namespace {
 // Planner
 // ---------------------------------------------------------------------------
 //
-// Lengths are on the GPU only, so the shares are made there: one CTA sums the
-// costs of all sequences (a sequence a thread, a warp together where one has
-// many units) and a warp finds each share's beginning.
+// Lengths are on the GPU only, so the shares are made there.  Up to kInside
+// sequences each CTA of the attention finds its own share, which takes it 2 to 3
+// us; a launch ahead of it would take more (16 sequences 8.5 us by itself).
+// Beyond, one CTA sums the costs of all sequences and a warp finds each share's
+// beginning.
 
 constexpr int kPlanThreads = 1024;
 constexpr int kKeep = 2048;  // sequences whose sums stay in shared memory
-constexpr int kAlone = 4;    // units a thread adds up by itself
-
-__device__ __forceinline__ int unit_cost(const Params& p, const Sequence& s, int q) {
-  Unit u;
-  u.set(p, s, q);
-  return kUnitCost + u.tiles;
-}
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p) {
   __shared__ long long s_warp[32];
@@ -50,32 +45,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
   __shared__ Start s_start[kMaxCtas + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   sm103::pdl_wait();
-  long long carry = 0;
+  long long total = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    Sequence s = {0, 0, 0, 0, 0};
-    if (b < p.batch) s.load(p, b);
-    long long cost = 0;
-    if (s.tiles <= kAlone)
-      for (int q = 0; q < s.tiles; ++q) cost += unit_cost(p, s, q);
-    unsigned many = __ballot_sync(~0u, s.tiles > kAlone);
-    while (many) {
-      const int from = __ffs(many) - 1;
-      many &= many - 1;
-      Sequence x;
-      x.row0 = 0;
-      x.tokens = __shfl_sync(~0u, s.tokens, from);
-      x.kept = __shfl_sync(~0u, s.kept, from);
-      x.length = __shfl_sync(~0u, s.length, from);
-      x.tiles = __shfl_sync(~0u, s.tiles, from);
-      long long sum = 0;
-      for (int q = lane; q < x.tiles; q += 32) sum += unit_cost(p, x, q);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      if (lane == from) cost = sum;
-    }
-    cost *= p.kv_heads;
-    long long upto = cost;
+    long long upto = sequence_cost(p, b) * p.kv_heads;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, upto, o);
@@ -83,12 +56,12 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
     }
     if (lane == 31) s_warp[warp] = upto;
     __syncthreads();
-    long long before = carry;
+    long long before = total;
 #pragma unroll
     for (int w = 0; w < 32; ++w) {
       const long long y = s_warp[w];
       if (w < warp) before += y;
-      carry += y;
+      total += y;
     }
     if (b < p.batch) {
       p.base[b + 1] = before + upto;
@@ -98,94 +71,18 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
   }
   if (tid == 0) p.base[0] = s_base[0] = 0;
   __syncthreads();
-  const long long total = carry;
   auto base = [&](int b) { return p.batch <= kKeep ? s_base[b] : p.base[b]; };
-  const long long even = (total + p.ctas - 1) / p.ctas;
-  const long long share = even < kMinShare ? kMinShare : even;
   for (int c = warp; c <= p.ctas; c += kPlanThreads / 32) {
-    const long long x = (long long)c * share;
-    Start st = {p.batch, 0, 0, 0};
-    if (x < total && c < p.ctas) {
-      int lo = 0, hi = p.batch - 1;  // the first sequence whose cost ends behind x
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (base(mid + 1) > x) hi = mid; else lo = mid + 1;
-      }
-      Sequence s;
-      s.load(p, lo);
-      const long long one = (base(lo + 1) - base(lo)) / p.kv_heads;
-      long long rest = x - base(lo);
-      st.b = lo;
-      st.kvh = (int)(rest / one);
-      rest -= st.kvh * one;
-      int tiles = 0;
-      for (int q0 = 0;; q0 += 32) {
-        const int q = q0 + lane;
-        const int mine = q < s.tiles ? unit_cost(p, s, q) : 0;
-        long long upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(~0u, upto, o);
-          if (lane >= o) upto += y;
-        }
-        const unsigned behind = __ballot_sync(~0u, upto > rest);
-        if (behind) {
-          const int at = __ffs(behind) - 1;
-          st.q = q0 + at;
-          tiles = __shfl_sync(~0u, mine, at) - kUnitCost;
-          rest -= __shfl_sync(~0u, upto - mine, at);
-          break;
-        }
-        rest -= __shfl_sync(~0u, upto, 31);
-        if (q0 + 32 >= s.tiles) {  // (cannot be: x lies before this sequence's end)
-          st = {p.batch, 0, 0, 0};
-          break;
-        }
-      }
-      // rest: of the unit's cost, what lies before the share
-      st.tile = (int)rest - kUnitCost;
-      if (st.b < p.batch) {
-        if (st.tile <= kSnap) {
-          st.tile = 0;
-        } else if (st.tile >= tiles - kSnap) {
-          // the next unit's beginning
-          st.tile = 0;
-          if (++st.q == s.tiles) {
-            st.q = 0;
-            if (++st.kvh == p.kv_heads) {
-              st.kvh = 0;
-              // the next sequence with rows
-              const long long z = base(st.b + 1);
-              int a = st.b + 1, e = p.batch;
-              while (a < e) {
-                const int mid = (a + e) >> 1;
-                if (base(mid + 1) > z) e = mid; else a = mid + 1;
-              }
-              st.b = a;
-            }
-          }
-        }
-      }
-    }
+    const Place e = find_place(p, c, total, base);
     if (lane == 0) {
-      s_start[c] = st;
-      p.starts[c] = st;
+      s_start[c] = e.st;
+      p.starts[c] = e.st;
     }
   }
   __syncthreads();
-  for (int c = tid; c < p.ctas; c += kPlanThreads) {
-    Record r = {0, 0, 0, 0};
-    const Start e = s_start[c + 1], a = s_start[c];
-    auto same = [](const Start& x, const Start& y) {
-      return x.b == y.b && x.kvh == y.kvh && x.q == y.q;
-    };
-    // share c ends within a unit that it begins
-    if (e.b < p.batch && e.tile > 0 && !(same(a, e) && a.tile > 0)) {
-      int k = c + 1;
-      while (k + 1 <= p.ctas && same(s_start[k + 1], e)) ++k;
-      r = {k - c + 1, e.b, e.kvh, e.q};
-    }
-    p.rec[c] = r;
+  for (int c = warp; c < p.ctas; c += kPlanThreads / 32) {
+    const Place e = find_place(p, c + 1, total, base);
+    if (lane == 0) p.rec[c] = make_record(p, c, total, s_start[c], e);
   }
 }
 
@@ -193,115 +90,85 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
 // Join
 // ---------------------------------------------------------------------------
 
-constexpr int kJoinThreads = 256, kJoinRow = 64, kJoinRows = kJoinThreads / kJoinRow;
-constexpr int kJoinLoads = 8, kJoinY = 8;
+constexpr int kJoinThreads = 256, kJoinY = 32, kJoinLoads = 4;
 
 // The parts of a cut unit's rows are weighted by 2^(m - max m) and added up in
-// order, so repeated calls give the same bits.  64 threads take a row: a vector of
-// four columns each, and what threads are left walk over the parts side by side.
+// order, so repeated calls give the same bits.  A warp takes a row, a lane four
+// columns of it; the row's first parts are asked for beside their maxima and sums.
+// (Four rows to a CTA with barriers between the steps took 56 us for the 152 cut
+// units of 256 rows of a prompt of 8192.)
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const Params p, const int kind) {
-  __shared__ float s_w[kJoinRows][kMaxCtas], s_l[kJoinRows][kMaxCtas];
-  __shared__ float s_red[kJoinRows][2];
-  __shared__ float4 s_acc[kJoinThreads];
   sm103::pdl_wait();
-  const int tid = threadIdx.x, r = tid / kJoinRow, i0 = tid % kJoinRow, cta = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
   const Record rec = p.rec[cta];
+  const int rows = rec.r1 - rec.r0;
   // (a workspace that another call is writing at the same time gives wrong
   // results, but no address outside this call's buffers)
-  if (rec.parts <= 1 || rec.parts > p.ctas - cta || rec.b < 0 || rec.b >= p.batch || rec.kvh < 0 ||
-      rec.kvh >= p.kv_heads)
+  if (rec.parts <= 1 || rec.parts > p.ctas - cta || rec.kvh < 0 || rec.kvh >= p.kv_heads ||
+      rec.row0 < 0 || rec.r0 < 0 || rows > p.bm ||
+      rec.r1 > (int64_t)(p.rows - rec.row0) * p.group)
     return;
-  Sequence s;
-  s.load(p, rec.b);
-  if (rec.q < 0 || rec.q >= s.tiles) return;
-  Unit u;
-  u.set(p, s, rec.q);
-  const int rows = u.r1 - u.r0;
   auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
-  const int cols = p.dp / 4, groups = kJoinRow / cols;
-  const int grp = i0 / cols, c = i0 - grp * cols;
   const float vs = p.v_scale ? p.v_scale[rec.kvh] : 1.f;
-  for (int row0 = blockIdx.y * kJoinRows; row0 < rows; row0 += kJoinY * kJoinRows) {
-    const int row = row0 + r;
-    const bool live = row < rows;
-    const int parts = live ? rec.parts : 0;
+  const int64_t step = (int64_t)p.bm * p.dp;
+  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < rows;
+       row += kJoinY * (kJoinThreads / 32)) {
     float M = -INFINITY;
-    for (int k = i0; k < parts; k += kJoinRow) {
-      const float2 ml = p.part_ml[slot(k) * p.bm + row];
-      s_w[r][k] = ml.x;
-      s_l[r][k] = ml.y;
-      M = fmaxf(M, ml.x);
-    }
+    for (int k = lane; k < rec.parts; k += 32) M = fmaxf(M, p.part_ml[slot(k) * p.bm + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    if ((tid & 31) == 0) s_red[r][i0 >> 5] = M;
-    __syncthreads();
-    M = fmaxf(s_red[r][0], s_red[r][1]);
     const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int k = i0; k < parts; k += kJoinRow) {
-      const float w = sm103::ex2(s_w[r][k] - base);
-      s_w[r][k] = w;
-      L += w * s_l[r][k];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
-    __syncthreads();
-    if ((tid & 31) == 0) s_red[r][i0 >> 5] = L;
-    __syncthreads();
-    L = s_red[r][0] + s_red[r][1];
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (grp < groups) {
-      const float* part = p.part_o + (int64_t)row * p.dp + c * 4;
-      const int64_t step = (int64_t)p.bm * p.dp;
-      for (int k0 = grp; k0 < parts; k0 += groups * kJoinLoads) {
-        float4 x[kJoinLoads];
-#pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          const int k = k0 + i * groups;
-          if (k < parts) x[i] = *reinterpret_cast<const float4*>(part + slot(k) * step);
+    const int i = p.group_div(rec.r0 + row), j = rec.r0 + row - i * p.group;
+    const int64_t head = (int64_t)(rec.row0 + i) * p.heads + rec.kvh * p.group + j;
+    for (int c = 4 * lane; c - 4 * lane < p.dim; c += 128) {
+      const float* part = p.part_o + (int64_t)row * p.dp + c;
+      const bool mine = c < p.dim;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
+      for (int k0 = 0; k0 < rec.parts; k0 += 32) {
+        const int n = min(32, rec.parts - k0);
+        float w = 0.f, l = 0.f;
+        if (lane < n) {
+          const float2 ml = p.part_ml[slot(k0 + lane) * p.bm + row];
+          w = sm103::ex2(ml.x - base);
+          l = w * ml.y;
         }
 #pragma unroll
-        for (int i = 0; i < kJoinLoads; ++i) {
-          const int k = k0 + i * groups;
-          if (k < parts) {
-            const float w = s_w[r][k];
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+        L += l;
+        for (int k1 = 0; k1 < n; k1 += kJoinLoads) {
+          float4 x[kJoinLoads];
+#pragma unroll
+          for (int e = 0; e < kJoinLoads; ++e) {
+            x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine && k1 + e < n)
+              x[e] = *reinterpret_cast<const float4*>(part + slot(k0 + k1 + e) * step);
+          }
+#pragma unroll
+          for (int e = 0; e < kJoinLoads; ++e) {
+            const float we = __shfl_sync(~0u, w, (k1 + e) & 31);
+            if (k1 + e >= n) continue;
             // (a part whose rows all weigh nothing holds zeros, or NaN where the row is NaN)
-            a.x = fmaf(w, x[i].x, a.x);
-            a.y = fmaf(w, x[i].y, a.y);
-            a.z = fmaf(w, x[i].z, a.z);
-            a.w = fmaf(w, x[i].w, a.w);
+            a.x = fmaf(we, x[e].x, a.x);
+            a.y = fmaf(we, x[e].y, a.y);
+            a.z = fmaf(we, x[e].z, a.z);
+            a.w = fmaf(we, x[e].w, a.w);
           }
         }
       }
-    }
-    s_acc[tid] = a;
-    __syncthreads();
-    if (live) {
-      const int i = p.group_div(u.r0 + row), j = u.r0 + row - i * p.group;
-      const int64_t head = (int64_t)(s.row0 + i) * p.heads + rec.kvh * p.group + j;
-      if (i0 < cols && c * 4 < p.dim) {
-        for (int g = 1; g < groups; ++g) {
-          const float4 y = s_acc[r * kJoinRow + g * cols + c];
-          a.x += y.x;
-          a.y += y.y;
-          a.z += y.z;
-          a.w += y.w;
-        }
-        const float inv = L == 0.f ? 0.f : vs / L;
-        if (kind == kFp32)
-          *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c * 4) =
-              make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        else
-          *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c * 4) = make_uint2(
-              sm103::pack_bf16(a.x * inv, a.y * inv), sm103::pack_bf16(a.z * inv, a.w * inv));
-      }
-      if (i0 == 0 && p.lse)
+      if (c == 0 && p.lse)
         p.lse[head] =
             L == 0.f ? -INFINITY
                      : (M + (log2f(L) - (kind == kE4m3 ? kShift : 0.f))) * 0.6931471805599453f;
+      if (!mine) continue;
+      const float inv = L == 0.f ? 0.f : vs / L;
+      if (kind == kFp32)
+        *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c) =
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      else
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c) = make_uint2(
+            sm103::pack_bf16(a.x * inv, a.y * inv), sm103::pack_bf16(a.z * inv, a.w * inv));
     }
-    __syncthreads();
   }
 }
 
@@ -365,8 +232,8 @@ Plan make_plan(const mla_kv_geometry_t* g, int batch, int rows, int page_size, i
 }
 
 cudaError_t run(const Plan& d, const Params& p, int kind, cudaStream_t stream) {
-  cudaError_t e;
-  {
+  cudaError_t e = cudaSuccess;
+  if (p.starts != nullptr) {
     KernelTimer kt("chunk_plan", stream);
     e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
   }
@@ -485,7 +352,7 @@ extern "C" mla_status_t mla_chunk_attention(
   p.out = out;
   p.lse = lse;
   char* ws = (char*)workspace;
-  p.starts = (chunk::Start*)ws;
+  p.starts = batch > chunk::kInside ? (chunk::Start*)ws : nullptr;
   p.rec = (chunk::Record*)(ws + d.off_rec);
   p.base = (long long*)(ws + d.off_base);
   p.part_ml = (float2*)(ws + d.off_ml);

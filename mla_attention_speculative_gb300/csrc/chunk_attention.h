@@ -21,7 +21,7 @@ namespace chunk {
 
 constexpr int kMaxCtas = 512;
 // What a unit costs besides its tiles: its queries, its last wait and its outputs.
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 3;
 // A share does not begin in the first or last kSnap tiles of a unit: a part of one
 // or two tiles costs more to join than to do.
 constexpr int kSnap = 2;
@@ -33,9 +33,12 @@ struct Start {
   int b, kvh, q, tile;
 };
 // A unit that is cut and begins in this share (its last segment): the shares that
-// hold a part of it, this one and the next ones (0: nothing to join).
+// hold a part of it, this one and the next ones (0: nothing to join), and its rows.
 struct Record {
-  int parts, b, kvh, q;
+  int parts, kvh;
+  int row0;    // its sequence's first row of the step
+  int r0, r1;  // its rows of the sequence and head
+  int unused[3];
 };
 
 struct Params {
@@ -48,7 +51,7 @@ struct Params {
   void* out;
   float* lse;
   // workspace
-  Start* starts;     // [ctas + 1]
+  Start* starts;     // [ctas + 1]; NULL: each CTA finds its own
   Record* rec;       // [ctas]
   long long* base;   // [batch + 1] cost before each sequence
   float2* part_ml;   // [2 * ctas][bm] running maximum (base 2) and sum
@@ -116,9 +119,9 @@ struct Walk {
   Sequence seq;
   bool loaded;
 
-  __device__ __forceinline__ void begin(const Params& p, int cta) {
-    at = p.starts[cta];
-    end = p.starts[cta + 1];
+  __device__ __forceinline__ void begin(const Start& from, const Start& to) {
+    at = from;
+    end = to;
     loaded = false;
   }
   __device__ __forceinline__ bool in_last() const {
@@ -181,6 +184,203 @@ struct Walk {
     return p.batch;
   }
 };
+
+// ---------------------------------------------------------------------------
+// Where the shares begin
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ int unit_cost(const Params& p, const Sequence& s, int q) {
+  Unit u;
+  u.set(p, s, q);
+  return kUnitCost + u.tiles;
+}
+
+// The cost of one sequence and key/value head, b < batch or none; a warp together
+// where a lane's sequence has many units.
+__device__ __forceinline__ long long sequence_cost(const Params& p, int b) {
+  constexpr int kAlone = 4;  // units a thread adds up by itself
+  const int lane = threadIdx.x & 31;
+  Sequence s = {0, 0, 0, 0, 0};
+  if (b < p.batch) s.load(p, b);
+  long long cost = 0;
+  if (s.tiles <= kAlone)
+    for (int q = 0; q < s.tiles; ++q) cost += unit_cost(p, s, q);
+  unsigned many = __ballot_sync(~0u, s.tiles > kAlone);
+  while (many) {
+    const int from = __ffs(many) - 1;
+    many &= many - 1;
+    Sequence x;
+    x.row0 = 0;
+    x.tokens = __shfl_sync(~0u, s.tokens, from);
+    x.kept = __shfl_sync(~0u, s.kept, from);
+    x.length = __shfl_sync(~0u, s.length, from);
+    x.tiles = __shfl_sync(~0u, s.tiles, from);
+    long long sum = 0;
+    for (int q = lane; q < x.tiles; q += 32) sum += unit_cost(p, x, q);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == from) cost = sum;
+  }
+  return cost;
+}
+
+// What a share holds at least, in all of `total` cost.
+__device__ __forceinline__ long long share_size(const Params& p, long long total) {
+  const long long even = (total + p.ctas - 1) / p.ctas;
+  return even < kMinShare ? kMinShare : even;
+}
+
+// A share's beginning, and the unit that its place x lies in.
+struct Place {
+  Start st;
+  Sequence seq;
+  int q, tiles;      // that unit and its tiles
+  long long x0;      // where it begins
+  __device__ __forceinline__ bool inside() const { return st.tile > 0; }
+};
+
+// The place of share c, by a warp; base(b): the cost before sequence b.
+template <typename Base>
+__device__ __forceinline__ Place find_place(const Params& p, int c, long long total, Base base) {
+  const int lane = threadIdx.x & 31;
+  const long long x = (long long)c * share_size(p, total);
+  Place r;
+  r.st = {p.batch, 0, 0, 0};
+  r.seq = {0, 0, 0, 0, 0};
+  r.q = r.tiles = 0;
+  r.x0 = 0;
+  if (x >= total || c >= p.ctas) return r;
+  int lo = 0, hi = p.batch - 1;  // the first sequence whose cost ends behind x
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (base(mid + 1) > x) hi = mid; else lo = mid + 1;
+  }
+  r.seq.load(p, lo);
+  const long long from = base(lo), all = base(lo + 1) - from;
+  // (32-bit divisions where the numbers allow, and they mostly do)
+  long long one, rest = x - from;
+  int kvh;
+  if (all <= 0x7FFFFFFF) {
+    one = (int)all / p.kv_heads;
+    kvh = (int)rest / (int)one;
+  } else {
+    one = all / p.kv_heads;
+    kvh = (int)(rest / one);
+  }
+  rest -= kvh * one;
+  r.st.b = lo;
+  r.st.kvh = kvh;
+  for (int q0 = 0; q0 < r.seq.tiles; q0 += 32) {
+    const int q = q0 + lane;
+    const int mine = q < r.seq.tiles ? unit_cost(p, r.seq, q) : 0;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned behind = __ballot_sync(~0u, upto > rest);
+    if (behind) {
+      const int at = __ffs(behind) - 1;
+      r.q = q0 + at;
+      r.tiles = __shfl_sync(~0u, mine, at) - kUnitCost;
+      rest -= __shfl_sync(~0u, upto - mine, at);
+      break;
+    }
+    rest -= __shfl_sync(~0u, upto, 31);
+  }
+  r.x0 = x - rest;
+  r.st.q = r.q;
+  r.st.tile = (int)rest - kUnitCost;
+  if (r.st.tile <= kSnap) {
+    r.st.tile = 0;
+  } else if (r.st.tile >= r.tiles - kSnap) {
+    // the next unit's beginning
+    r.st.tile = 0;
+    if (++r.st.q == r.seq.tiles) {
+      r.st.q = 0;
+      if (++r.st.kvh == p.kv_heads) {
+        r.st.kvh = 0;
+        // the next sequence with rows: idle ones' sums are equal
+        const long long z = base(lo + 1);
+        int a = lo + 1, e = p.batch;
+        while (a < e) {
+          const int mid = (a + e) >> 1;
+          if (base(mid + 1) > z) e = mid; else a = mid + 1;
+        }
+        r.st.b = a;
+      }
+    }
+  }
+  return r;
+}
+
+// What share c leaves to join, given where it and the next one begin.
+__device__ __forceinline__ Record make_record(const Params& p, int c, long long total,
+                                              const Start& a, const Place& e) {
+  Record r = {0, 0, 0, 0, 0, {0, 0, 0}};
+  const bool same = a.b == e.st.b && a.kvh == e.st.kvh && a.q == e.st.q;
+  // share c ends within a unit that it begins
+  if (e.st.b >= p.batch || !e.inside() || (same && a.tile > 0)) return r;
+  // the places behind e, a share apart, that lie within the unit as well
+  const long long size = share_size(p, total);
+  const long long x = (long long)(c + 1) * size;
+  const long long last = e.x0 + kUnitCost + e.tiles - kSnap - 1;
+  Unit u;
+  u.set(p, e.seq, e.q);
+  r.parts = 2 + (int)((last - x) / size);
+  r.kvh = e.st.kvh;
+  r.row0 = e.seq.row0;
+  r.r0 = u.r0;
+  r.r1 = u.r1;
+  return r;
+}
+
+// The beginnings of this CTA's share and the next one's, and its record, with a
+// sequence to a thread: batch <= kInside.  `scratch`: shared memory, used until the
+// call returns.
+constexpr int kInside = 256;
+struct PlanScratch {
+  long long base[kInside + 1];
+  long long warp[kInside / 32];
+  Start start[2];
+};
+__device__ __forceinline__ void find_share(const Params& p, int cta, PlanScratch& t, Start& from,
+                                           Start& to) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long upto = 0;
+  if (warp < kInside / 32) {
+    upto = sequence_cost(p, tid) * p.kv_heads;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) t.warp[warp] = upto;
+  }
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kInside / 32; ++w) {
+    const long long y = t.warp[w];
+    if (w < warp) before += y;
+    total += y;
+  }
+  if (warp < kInside / 32) t.base[tid + 1] = before + upto;
+  if (tid == 0) t.base[0] = 0;
+  __syncthreads();
+  auto base = [&](int b) { return t.base[b]; };
+  Place e;
+  if (warp < 2) {
+    e = find_place(p, cta + warp, total, base);
+    if (lane == 0) t.start[warp] = e.st;
+  }
+  __syncthreads();
+  from = t.start[0];
+  to = t.start[1];
+  if (warp == 1 && lane == 0) p.rec[cta] = make_record(p, cta, total, from, e);
+  __syncthreads();
+}
 
 // Element types of a call: q/out and cache bf16; q/out bf16 beside an e4m3
 // cache; all fp32.

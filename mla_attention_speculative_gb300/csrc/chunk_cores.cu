@@ -56,11 +56,18 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const int cta = blockIdx.x;
   sm103::pdl_wait();
+  Start from, to;
+  if (p.starts == nullptr) {
+    find_share(p, cta, *reinterpret_cast<PlanScratch*>(s_raw), from, to);
+  } else {
+    from = p.starts[cta];
+    to = p.starts[cta + 1];
+  }
   // columns past the heads' width stay zero
   for (int i = tid; i < 3 * 64 * LD; i += kThreads) sQ[i] = 0.f;
   __syncthreads();
   Walk w;
-  w.begin(p, cta);
+  w.begin(from, to);
   Segment g;
   for (; w.next(p, g); w.advance(p, g)) {
     const Sequence& s = w.seq;

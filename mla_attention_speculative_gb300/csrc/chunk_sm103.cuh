@@ -20,10 +20,11 @@
 // the largest count).
 //
 // Keys and values come through a ring of 128-position blocks:
-//   kTma      one thread's TMA boxes, page by page, where pages are whole runs of
-//             8 rows (page sizes with a power of two of 8 or more in them)
-//   kRows     16-byte copies of single rows, for any other page size
-//   kConvert  the same into a staging ring, then e4m3 -> fp16 by the same threads
+//   kTma      one warp's TMA boxes, page by page, where pages are whole runs of 8
+//             rows (page sizes with a power of two of 8 or more in them)
+//   kRows     16-byte copies of single rows by four warps, for any other page size
+//   kConvert  e4m3: TMA boxes (of any page's rows) into a staging ring, and from there
+//             as fp16 by four warps
 // Rows that nobody sees, and elements of V that are not finite in a tile where a
 // row is hidden from some query, are set to zero before P V reads them (0 times
 // such an element is NaN); the latter are put back at the end, for the rows that
@@ -67,26 +68,54 @@ struct Shape {
   static constexpr int NBLK = (DP + 127) / 128;       // blocks of a tile of K or V
   static constexpr int QB = 128 * DP * 2;             // bytes of 128 queries
   static constexpr int SLOT = kBN * BW * 2;
-  static constexpr int RAW = FEED == kConvert ? kBN * BW : 0;
+  static constexpr int RAW = FEED == kConvert ? kBN * 128 : 0;  // a block's bytes, 128 a row
   static constexpr int NB = FEED == kConvert ? (DP == 64 ? 6 : 3) : (DP == 64 ? 10 : 5);
-  static constexpr int RS = FEED == kConvert ? (DP == 64 ? 6 : 3) : 0;
-  static constexpr int THREADS = 128 * NS + 128;
-  static constexpr int FEEDERS = FEED == kTma ? 32 : FEED == kRows ? 64 : 96;
+  static constexpr int RS = FEED == kConvert ? 4 : 0;
+  // warps: softmax, then the MMA issuer, the TMA boxes, V where rows are hidden (one is
+  // left over), and four that copy or convert
+  static constexpr int MMA = 4 * NS, TMA = MMA + 1, CLEAN = MMA + 2, FEEDER = MMA + 4;
+  static constexpr int FEEDERS = FEED == kTma ? 0 : 128;
+  static constexpr int THREADS = FEEDER * 32 + FEEDERS;
+  // 16 warps start with 128 registers a thread: 168 for the softmax, 88 for the others
+  static constexpr bool SHARES = THREADS == 512;
   static constexpr uint32_t TM_S = NS * DP;           // tensor memory: O, then two of S
   static constexpr int TAIL = 1024 + (FEED == kConvert ? NS * 128 * 4 : 0);
   static constexpr int SMEM = 1024 + NS * QB + NB * SLOT + RS * RAW + TAIL;
   static_assert(SMEM <= 232448, "more shared memory than a CTA may have");
   static_assert(TM_S + 256 <= 512, "more tensor memory than there is");
   // barriers
-  static constexpr int FULL = 0, EMPTY = NB, LANDED = 2 * NB, QFULL = 3 * NB, QEMPTY = QFULL + 2,
-                       SFULL = QEMPTY + 1, PFULL = SFULL + 2, OFULL = PFULL + 2,
-                       PVDONE = OFULL + 2, DRAIN = PVDONE + 2, BARS = DRAIN + 1;
+  static constexpr int FULL = 0, EMPTY = NB, LANDED = 2 * NB, RFULL = 3 * NB, REMPTY = RFULL + RS,
+                       QFULL = REMPTY + RS, SFULL = QFULL + 1, PHALF = SFULL + 2,
+                       PFULL = PHALF + 2,                       OFULL = PFULL + 2, PVDONE = OFULL + 2, DRAIN = PVDONE + 2,
+                       BARS = DRAIN + 1;
   static_assert(BARS * 8 + 10 * 4 + 4 * NS * sizeof(Walk) <= 1024, "the barriers do not fit");
 };
 
 struct Maps {
   CUtensorMap k, v;
   int box;  // rows of a box
+};
+
+// A block of a ring of N and the phase of its barriers.
+struct Slot {
+  uint32_t i, phase;
+  template <int N>
+  __device__ __forceinline__ void move(uint32_t by) {  // by at most 2 N
+    i += by;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (i >= N) {
+        i -= N;
+        phase ^= 1;
+      }
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void move_far(uint32_t by) {
+    i += by;
+    phase ^= (i / N) & 1;
+    i %= N;
+  }
 };
 
 // The place of a block in the ring's order K0 K1 V0 K2 V1 .. V(n-1).
@@ -175,31 +204,47 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       mbar_init(bar(C::EMPTY + i), 1);
       mbar_init(bar(C::LANDED + i), FEED == kTma ? 1 : C::FEEDERS);
     }
+    for (int i = 0; i < C::RS; ++i) {
+      mbar_init(bar(C::RFULL + i), 1);
+      mbar_init(bar(C::REMPTY + i), C::FEEDERS);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::QFULL + i), 128);
       mbar_init(bar(C::SFULL + i), 1);
+      mbar_init(bar(C::PHALF + i), 128);
       mbar_init(bar(C::PFULL + i), 128);
       mbar_init(bar(C::OFULL + i), 1);
       mbar_init(bar(C::PVDONE + i), 1);
     }
-    mbar_init(bar(C::QEMPTY), 1);
+    mbar_init(bar(C::QFULL), 128 * NS);
     mbar_init(bar(C::DRAIN), 1);
     for (int i = 0; i < 8; ++i) dirty[i] = -1;
     fence_mbar_init();
   }
-  if (warp == 4 * NS) tmem_alloc(smem_u32(slot_word), 512);
+  if (warp == C::MMA) tmem_alloc(smem_u32(slot_word), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot_word;
   pdl_wait();
+  Start from, to;
+  if (p.starts == nullptr) {
+    // (the place of the queries, which come later)
+    find_share(p, cta, *reinterpret_cast<PlanScratch*>(smem), from, to);
+  } else {
+    from = p.starts[cta];
+    to = p.starts[cta + 1];
+  }
   Walk w;
   Segment g;
-  w.begin(p, cta);
+  w.begin(from, to);
   bool ok = true;
 
+  if (warp >= 4 * NS) {
+    if constexpr (C::SHARES) regs_dec<104>();
+  }
   if (warp < 4 * NS) {
     // ------------------------------------------------------------- softmax
+    if constexpr (C::SHARES) regs_inc<152>();
     const int s = warp >> 2;                  // stream
     const int q = (warp & 3) * 32 + lane;     // its row, and its tensor memory lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -223,9 +268,9 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         // hidden scores below the others)
         sl2 = isfinite(ks) ? fmaxf(sl2 * fabsf(ks), 1e-37f) : NAN;
       }
+      // This stream's queries.  The products that read the ones before are done, and
+      // with both streams' arrivals everything of the segment before is.
       if (n > 0 && (!split || s == 0)) {
-        // ---- this stream's queries
-        if (seg > 0) wait_or_fail(ok, bar(C::QEMPTY), (seg - 1) & 1, 100);
         constexpr int CH = DP / 8;  // 16-byte chunks of a row
         const uint32_t dst0 = sQ + (split ? 0 : s) * C::QB;
         const int row0 = (warp & 3) * 32;
@@ -239,7 +284,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
                        : 0);
         };
         if constexpr (!HALF) {
-#pragma unroll 4
+#pragma unroll 8
           for (int k = 0; k < CH; ++k) {
             const int e = k * 32 + lane, row = row0 + e / CH, c = e % CH;
             bool have;
@@ -250,45 +295,56 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           cp_async_wait_all();
         } else {
           constexpr int LPR = CH <= 8 ? 8 : CH <= 16 ? 16 : 32;  // lanes to a row
-          for (int k = 0; k < LPR; ++k) {
-            const int row = row0 + k * (32 / LPR) + lane / LPR, c = lane % LPR;
-            bool have;
-            const __nv_bfloat16* src = source(row, c, have);
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (have) x = *reinterpret_cast<const uint4*>(src);
-            const uint32_t word[4] = {x.x, x.y, x.z, x.w};
-            float f[8], top = 0.f;
+          constexpr int AT_ONCE = 4;
+#pragma unroll 1
+          for (int k0 = 0; k0 < LPR; k0 += AT_ONCE) {
+            uint4 x[AT_ONCE];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[2 * e] = __uint_as_float(word[e] << 16);
-              f[2 * e + 1] = __uint_as_float(word[e] & 0xFFFF0000u);
-              top = fmaxf(top, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+            for (int k = 0; k < AT_ONCE; ++k) {
+              const int row = row0 + (k0 + k) * (32 / LPR) + lane / LPR, c = lane % LPR;
+              bool have;
+              const __nv_bfloat16* src = source(row, c, have);
+              x[k] = make_uint4(0u, 0u, 0u, 0u);
+              if (have) x[k] = *reinterpret_cast<const uint4*>(src);
             }
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            // 2^-exponent of the largest; the row's scores are scaled back
-            float down = 1.f, up = 1.f;
-            if (top > 0.f && isfinite(top)) {
-              const int ex = ilogbf(top);
-              down = ldexpf(1.f, -ex);
-              up = ldexpf(1.f, ex);
-            }
-            if (c == 0) q_scale[(split ? 0 : 128 * s) + row] = up;
-            down *= ksign;
-            if (c < CH) {
-              const uint32_t at = dst0 + (c >> 3) * 16384 + sw128_offset(row, (c & 7) * 8);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                           "r"(pack_half(f[0] * down, f[1] * down)),
-                           "r"(pack_half(f[2] * down, f[3] * down)),
-                           "r"(pack_half(f[4] * down, f[5] * down)),
-                           "r"(pack_half(f[6] * down, f[7] * down))
-                           : "memory");
+            for (int k = 0; k < AT_ONCE; ++k) {
+              const int row = row0 + (k0 + k) * (32 / LPR) + lane / LPR, c = lane % LPR;
+              const uint32_t word[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              float f[8], most = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                f[2 * e] = __uint_as_float(word[e] << 16);
+                f[2 * e + 1] = __uint_as_float(word[e] & 0xFFFF0000u);
+                most = fmaxf(most, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+              }
+#pragma unroll
+              for (int o = LPR / 2; o > 0; o >>= 1)
+                most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+              // 2^-exponent of the largest; the row's scores are scaled back
+              float down = 1.f, up = 1.f;
+              if (most > 0.f && isfinite(most)) {
+                const int ex = ilogbf(most);
+                down = ldexpf(1.f, -ex);
+                up = ldexpf(1.f, ex);
+              }
+              if (c == 0) q_scale[(split ? 0 : 128 * s) + row] = up;
+              down *= ksign;
+              if (c < CH) {
+                const uint32_t at = dst0 + (c >> 3) * 16384 + sw128_offset(row, (c & 7) * 8);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                             "r"(pack_half(f[0] * down, f[1] * down)),
+                             "r"(pack_half(f[2] * down, f[3] * down)),
+                             "r"(pack_half(f[4] * down, f[5] * down)),
+                             "r"(pack_half(f[6] * down, f[7] * down))
+                             : "memory");
+              }
             }
           }
         }
         fence_async_shared();
-        mbar_arrive(bar(C::QFULL + s));
       }
+      if (n > 0) mbar_arrive(bar(C::QFULL));
       if constexpr (HALF) {
         if (n > 0) {
           if (split) named_bar_sync(1, 256);  // stream 1 reads the scales stream 0 wrote
@@ -415,6 +471,11 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
             pk[e] = HALF ? pack_half(y[2 * e], y[2 * e + 1]) : pack_bf16(y[2 * e], y[2 * e + 1]);
           }
           tmem_st16(tS + 16 * k, pk);
+          if (k & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar((k == 1 ? C::PHALF : C::PFULL) + x));
+          }
         };
         if (edge || large) {
 #pragma unroll 1
@@ -427,9 +488,6 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         } else {
           pieces([&](uint32_t* u, int k) { weights(u, k, std::false_type()); });
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(C::PFULL + x));
         ++uses[x];
         float a, b;
         unpack2(add2(sum2[0], sum2[1]), a, b);
@@ -447,20 +505,22 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       const bool fix = n > 0 && dirty[seg & 7] == seg;
       float f0 = 1.f, f1 = 0.f;
       int c0 = 0, c1 = DP;
-      const float2* other = nullptr;
       if (split) {
-        // the streams' sums meet: each half of the columns by one of them (a place of the
-        // queries that are not there holds the other's maximum and sum)
-        float2* sums = reinterpret_cast<float2*>(smem + C::QB);
-        sums[128 * s + q] = make_float2(m, any ? l : 0.f);
+        // The streams' sums meet, each half of the columns in one of them; a row's maximum
+        // and sum go to the other stream through the scores' tensor memory.
+        uint32_t z[16] = {__float_as_uint(m), __float_as_uint(any ? l : 0.f)};
+        tmem_st16(tmem + lane_base + C::TM_S + 128 * s, z);
+        tmem_wait_st();
+        tc_fence_before();
         named_bar_sync(1, 256);
         tc_fence_after();
-        other = sums + 128 * (s ^ 1) + q;
-        const float2 z = *other;
-        const float mm = fmaxf(m, z.x), ref = mm == -INFINITY ? 0.f : mm;
+        tmem_ld16(tmem + lane_base + C::TM_S + 128 * (s ^ 1), z);
+        tmem_wait_ld<16>(z);
+        const float zm = __uint_as_float(z[0]), zl = __uint_as_float(z[1]);
+        const float mm = fmaxf(m, zm), ref = mm == -INFINITY ? 0.f : mm;
         f0 = ex2(m - ref);
-        f1 = ex2(z.x - ref);
-        l = l * f0 + z.y * f1;
+        f1 = ex2(zm - ref);
+        l = l * f0 + zl * f1;
         m = mm;
         c0 = s * (DP / 2);
         c1 = c0 + DP / 2;
@@ -475,39 +535,58 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       const int64_t part = (int64_t)(2 * cta + (g.first ? 1 : 0)) * p.bm + r;
       // the accumulators' weights: mine and the other stream's
       const float wa = split && s == 1 ? f1 : f0, wb = split && s == 1 ? f0 : f1;
-#pragma unroll 1
-      for (int c = c0; c < c1; c += 16) {
-        uint32_t o[16];
-        __syncwarp();
-        if (n > 0) {
-          tmem_ld16(tmem + lane_base + (NS == 2 && !split ? DP * s : 0) + c, o);
-          if (second) {
-            uint32_t o1[16];
-            tmem_ld16(tmem + lane_base + DP + c, o1);
-            tmem_wait_ld<16>(o);
-            tmem_wait_ld<16>(o1);
+      // 32 columns at a time through shared memory (the place of this warp's queries), so
+      // that a row's columns leave side by side.
+      const uint32_t stage = sQ + s * C::QB + (warp & 3) * 4096;
+      const int row0 = (split ? 0 : 128 * s) + (warp & 3) * 32;
+      const int rows_here = min(max(rows - row0, 0), 32);
+      // where this lane's four rows go (whole: four 8-column vectors of a row side by side)
+      int64_t out_at[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              // (a stream without weight may hold anything)
-              const float a = wa == 0.f ? 0.f : __uint_as_float(o[e]) * wa;
-              const float b = wb == 0.f ? 0.f : __uint_as_float(o1[e]) * wb;
-              o[e] = __float_as_uint(a + b);
+      for (int k = 0; k < 4; ++k) {
+        const int row = 8 * k + (lane >> 2), x = u.r0 + row0 + row;
+        const int i = p.group_div(x), j = x - i * p.group;
+        out_at[k] = row < rows_here
+                        ? ((int64_t)(sq.row0 + i) * p.heads + kvh * p.group + j) * p.dim +
+                              8 * (lane & 3)
+                        : -1;
+      }
+      float* part_at = p.part_o + ((int64_t)(2 * cta + (g.first ? 1 : 0)) * p.bm + row0) * p.dp;
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 32) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[16];
+          const int col = c + 16 * half;
+          __syncwarp();
+          if (n > 0) {
+            tmem_ld16(tmem + lane_base + (NS == 2 && !split ? DP * s : 0) + col, o);
+            if (second) {
+              uint32_t o1[16];
+              tmem_ld16(tmem + lane_base + DP + col, o1);
+              tmem_wait_ld<16>(o);
+              tmem_wait_ld<16>(o1);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                // (a stream without weight may hold anything)
+                const float a = wa == 0.f ? 0.f : __uint_as_float(o[e]) * wa;
+                const float b = wb == 0.f ? 0.f : __uint_as_float(o1[e]) * wb;
+                o[e] = __float_as_uint(a + b);
+              }
+            } else {
+              tmem_wait_ld<16>(o);
             }
-          } else {
-            tmem_wait_ld<16>(o);
           }
-        }
-        if (live) {
           if (l == 0.f) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0u;
-          } else if (fix) {
+          } else if (fix && live) {
             const int lo = max(first, (u.tile0 + g.t0) * kBN),
                       hi = min(last, (u.tile0 + g.t1) * kBN - 1);
 #pragma unroll 1
             for (int e = 0; e < 16; ++e) {
-              if (c + e >= p.dim) continue;
-              const float y = odd_values<FEED>(p, w.at.b, kvh, c + e, lo, hi, seen.lo, seen.hi);
+              if (col + e >= p.dim) continue;
+              const float y = odd_values<FEED>(p, w.at.b, kvh, col + e, lo, hi, seen.lo, seen.hi);
               // (the array stays in registers: no index at run time)
 #pragma unroll
               for (int k = 0; k < 16; ++k)
@@ -517,22 +596,53 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 16; e += 8) {
-              if (c + e >= p.dim) continue;
               uint32_t y[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 y[k] = pack_bf16(__uint_as_float(o[e + 2 * k]) * inv,
                                  __uint_as_float(o[e + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>((__nv_bfloat16*)p.out + head * p.dim + c + e) =
-                  make_uint4(y[0], y[1], y[2], y[3]);
+              const uint32_t at =
+                  stage + lane * 64 + (((2 * half + e / 8) ^ ((lane >> 1) & 3)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]),
+                           "r"(y[1]), "r"(y[2]), "r"(y[3])
+                           : "memory");
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4*>(p.part_o + part * p.dp + c + e) =
-                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 16; e += 4) {
+              const uint32_t at = stage + lane * 128 + (((4 * half + e / 4) ^ (lane & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[e]),
+                           "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3])
+                           : "memory");
+            }
           }
         }
+        __syncwarp();
+        auto staged = [&](uint32_t at) {
+          uint4 x;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                       : "r"(at)
+                       : "memory");
+          return x;
+        };
+        if (whole) {
+          const uint32_t from = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // rows 8 k + lane / 4
+            if (out_at[k] >= 0 && c + 8 * (lane & 3) < p.dim)
+              *reinterpret_cast<uint4*>((__nv_bfloat16*)p.out + out_at[k] + c) =
+                  staged(from + k * 512);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = 4 * k + (lane >> 3), ch = lane & 7;
+            if (row < rows_here)
+              *reinterpret_cast<uint4*>(part_at + row * p.dp + c + 4 * ch) =
+                  staged(stage + row * 128 + ((ch ^ (row & 7)) << 4));
+          }
+        }
+        __syncwarp();
       }
       if (live && (!split || s == 0)) {
         if (!whole) p.part_ml[part] = make_float2(m, l);
@@ -545,37 +655,44 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       }
       if (n > 0) ++seg;
     }
-  } else if (warp == 4 * NS) {
+  } else if (warp == C::MMA) {
     // ----------------------------------------------------------------- MMA
+    // One thread issues for both streams in turn, O += P V of a tile and S of the next
+    // one.  (An issuer for each, whose instructions the pipe takes alternately, made
+    // both streams wait longer: 8192 rows 649 us against 579.)
     const uint32_t id_s = HALF ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
     const int nk = (p.dim + 15) / 16;  // steps of 16 columns
-    const bool whole = nk == DP / 16;
-    uint32_t at = 0;                   // blocks before this segment
-    uint32_t puses[2] = {0, 0}, q_uses[2] = {0, 0};
+    const bool full_width = nk == DP / 16;
+    Slot ring = {0, 0};            // of this segment's first block
+    uint32_t before[2] = {0, 0};   // tiles of each stream (or S buffer) before it
+    uint32_t seg = 0;
+    // (what the thread does between two tiles' instructions is what the pipe waits for:
+    // few waits, and few instructions)
+    const uint64_t dk0 = sdesc_sw128(sRing, 16, 1024), dv0 = sdesc_sw128(sRing, 16384, 1024);
+    const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
+    const uint32_t first_n = (min(p.dim, C::BW) + 15) & ~15, last_n = (p.dim - 128 + 15) & ~15;
     for (; w.next(p, g); w.advance(p, g)) {
       const int n = g.t1 - g.t0, rows = g.unit.r1 - g.unit.r0;
       if (n == 0) continue;
       const bool split = NS == 2 && rows <= 128;
       if (lane == 0) {
-        auto block = [&](int place, int blk) { return at + (uint32_t)(place * NBLK + blk); };
-        auto landed = [&](uint32_t pos) {
-          wait_or_fail(ok, bar(C::FULL + pos % NB), (pos / NB) & 1, 110);
+        auto landed = [&](const Slot& t) {
+          wait_or_fail(ok, bar(C::FULL + t.i), t.phase, 110);
+          if (FEED == kRows) fence_async_shared();
         };
-        auto scores = [&](int x, int tile, int i, bool wait, bool free) {
-          const uint64_t dq = sdesc_sw128(sQ + tile * C::QB, 16, 1024);
+        // S = Q K^T of the tile at `t`.  `wait`: its first use, `free`: its last one
+        auto scores = [&](int x, uint64_t dq, Slot t, bool wait, bool free) {
+          const uint32_t dst = tmem + C::TM_S + 128 * x;
 #pragma unroll
           for (int blk = 0; blk < NBLK; ++blk) {
-            const uint32_t pos = block(k_place(i), blk);
-            if (wait) landed(pos);
+            if (blk > 0) t.move<NB>(1);
+            if (wait) landed(t);
             if (!ok) return;
-            if (FEED != kTma) fence_async_shared();
-            tc_fence_after();
-            const uint64_t dk = sdesc_sw128(sRing + (pos % NB) * C::SLOT, 16, 1024);
-            const uint32_t dst = tmem + C::TM_S + 128 * x;
+            const uint64_t dk = dk0 + (uint64_t)(t.i * (C::SLOT >> 4));
             const uint64_t dqb = dq + (uint64_t)(blk * 2048);
             // (a condition on single MMAs of the unrolled form made the compiler give some of
             // them another one's descriptor: so either all of them, or a loop)
-            if (whole) {
+            if (full_width) {
 #pragma unroll
               for (int k = 0; k < C::BW / 16; ++k)
                 if (blk * (C::BW / 16) + k < DP / 16)
@@ -589,141 +706,188 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
                 mma_bf16(dst, dqb + off, dk + off, id_s, (blk | k) != 0);
               }
             }
-            if (free) mma_commit(bar(C::EMPTY + pos % NB));
+            if (free) mma_commit(bar(C::EMPTY + t.i));
           }
           mma_commit(bar(C::SFULL + x));
         };
-        auto products = [&](int x, int o, int i, bool begin, bool wait, bool free) {
-          wait_or_fail(ok, bar(C::PFULL + x), puses[x] & 1, 111);
-          ++puses[x];
+        // O += P V of the tile at `t`, number j of its stream or S buffer.  The first half
+        // of P is enough to begin with.
+        auto products = [&](int x, int o, Slot t, int j, bool begin, bool wait, bool free) {
+          const uint32_t parity = (before[x] + (uint32_t)j) & 1;
+          if (wait) landed(t);
+          wait_or_fail(ok, bar(C::PHALF + x), parity, 111);
+          if (!ok) return;
+          tc_fence_after();
 #pragma unroll
           for (int blk = 0; blk < NBLK; ++blk) {
-            const uint32_t pos = block(v_place(i, n), blk), sl = pos % NB;
-            if (wait) landed(pos);
-            if (!ok) return;
-            if (FEED != kTma) fence_async_shared();
-            tc_fence_after();
-            const uint64_t dv = sdesc_sw128(sRing + sl * C::SLOT, 16384, 1024);
-            const int cols = min(p.dim - 128 * blk, C::BW);
-            const int nn = (cols + 15) & ~15;
+            if (blk > 0) {
+              t.move<NB>(1);
+              if (wait) landed(t);
+              if (!ok) return;
+            }
+            const uint64_t dv = dv0 + (uint64_t)(t.i * (C::SLOT >> 4));
+            const uint32_t nn = blk == 0 ? first_n : last_n;
             const uint32_t id_o = HALF ? idesc_f16(128, nn, 0, 1) : idesc_bf16(128, nn, 0, 1);
+            const uint32_t dst = tmem + o * DP + 128 * blk, from = tmem + C::TM_S + 128 * x;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_tmem_a(tmem + o * DP + 128 * blk, tmem + C::TM_S + 128 * x + 8 * k,
-                              dv + 128 * k, id_o, !begin || k > 0);
-            if (free) mma_commit(bar(C::EMPTY + sl));
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_tmem_a(dst, from + 8 * k, dv + 128 * k, id_o, !begin || k > 0);
+            if (blk == 0) {
+              wait_or_fail(ok, bar(C::PFULL + x), parity, 112);
+              if (!ok) return;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int k = 4; k < 8; ++k)
+              mma_bf16_tmem_a(dst, from + 8 * k, dv + 128 * k, id_o, 1);
+            if (free) mma_commit(bar(C::EMPTY + t.i));
           }
         };
-        wait_or_fail(ok, bar(C::QFULL), q_uses[0] & 1, 113);
-        ++q_uses[0];
+        // where the next tiles of K and V lie: K0 K1 V0 K2 V1 .. V(n-1)
+        Slot kt = ring, vt = ring;
+        vt.move<NB>((n == 1 ? 1 : 2) * NBLK);
+        wait_or_fail(ok, bar(C::QFULL), seg & 1, 113);
         if (NS == 2 && !split) {
-          wait_or_fail(ok, bar(C::QFULL + 1), q_uses[1] & 1, 114);
-          ++q_uses[1];
-          scores(0, 0, 0, true, false);
-          scores(1, 1, 0, false, true);
-          if (n == 1) mma_commit(bar(C::QEMPTY));
+          const uint64_t dq1 = dq0 + (C::QB >> 4);
+          scores(0, dq0, kt, true, false);
+          scores(1, dq1, kt, false, true);
+          kt.move<NB>(NBLK);
           for (int i = 0; i < n && ok; ++i) {
-            products(0, 0, i, i == 0, true, false);
-            if (i + 1 < n) scores(0, 0, i + 1, true, false);
+            products(0, 0, vt, i, i == 0, true, false);
+            if (i + 1 < n) scores(0, dq0, kt, true, false);
             else mma_commit(bar(C::OFULL));
-            products(1, 1, i, i == 0, false, true);
-            if (i + 1 < n) {
-              scores(1, 1, i + 1, false, true);
-              if (i + 2 == n) mma_commit(bar(C::QEMPTY));
-            } else {
-              mma_commit(bar(C::OFULL + 1));
-            }
+            products(1, 1, vt, i, i == 0, false, true);
+            if (i + 1 < n) scores(1, dq1, kt, false, true);
+            else mma_commit(bar(C::OFULL + 1));
+            kt.move<NB>(2 * NBLK);
+            vt.move<NB>((i + 2 < n ? 2 : 1) * NBLK);
           }
         } else {
-          scores(0, 0, 0, true, true);
-          if (n > 1) scores(1, 0, 1, true, true);
-          if (n <= 2) mma_commit(bar(C::QEMPTY));
+          scores(0, dq0, kt, true, true);
+          kt.move<NB>(NBLK);
+          if (n > 1) {
+            scores(1, dq0, kt, true, true);
+            kt.move<NB>(2 * NBLK);
+          }
           for (int i = 0; i < n && ok; ++i) {
             const int x = i & 1;
-            products(x, NS == 2 ? x : 0, i, NS == 2 ? i < 2 : i == 0, true, true);
+            products(x, NS == 2 ? x : 0, vt, i >> 1, NS == 2 ? i < 2 : i == 0, true, true);
+            vt.move<NB>((i + 2 < n ? 2 : 1) * NBLK);
             if (NS == 1) mma_commit(bar(C::PVDONE + x));
             if (i + 2 < n) {
-              scores(x, 0, i + 2, true, true);
-              if (i + 3 == n) mma_commit(bar(C::QEMPTY));
+              scores(x, dq0, kt, true, true);
+              kt.move<NB>(2 * NBLK);
             }
             if (NS == 2 ? i + 2 >= n : i + 1 == n) mma_commit(bar(C::OFULL + (NS == 2 ? x : 0)));
           }
         }
-        at += (uint32_t)(2 * n * NBLK);
+        ring.move_far<NB>((uint32_t)(2 * n * NBLK));
+        before[0] += (uint32_t)(NS == 2 && !split ? n : (n + 1) >> 1);
+        before[1] += (uint32_t)(NS == 2 && !split ? n : n >> 1);
+        ++seg;
       }
       __syncwarp();
     }
     if (lane == 0) {
-      // nothing this thread issued may still run when tensor memory is given back
+      // nothing that was issued may still run when tensor memory is given back
       mma_commit(bar(C::DRAIN));
       if (!mbar_wait(bar(C::DRAIN), 0)) report(115);
     }
     __syncwarp();
-  } else if (FEED == kTma && warp == 4 * NS + 1) {
+  } else if (FEED != kRows && warp == C::TMA) {
     // ------------------------------------------------------------ TMA boxes
-    // A lane issues one box: rows `box` of the tile, 64 columns.
+    // A lane issues a box, `box` rows of the tile: 64 bf16 columns, or 128 bytes of e4m3
+    // into the staging ring.
+    constexpr int SLOTS = FEED == kTma ? NB : C::RS;
+    constexpr int TO_FULL = FEED == kTma ? C::FULL : C::RFULL;
+    constexpr int TO_EMPTY = FEED == kTma ? C::EMPTY : C::REMPTY;
     uint32_t at = 0, issued = 0;
     const int nbox = kBN / maps.box;
-    const int rb = lane % nbox, ch = lane / nbox;
+    const bool one_each = nbox <= 32;  // a lane has one box of rows at most
+    const int rb = one_each ? lane % nbox : 0, ch = one_each ? lane / nbox : 0;
     for (; w.next(p, g); w.advance(p, g)) {
       const int n = g.t1 - g.t0;
       const Unit& u = g.unit;
       const int kvh = w.at.kvh;
       const Seen seen(p, w.seq, u);
-      // this lane's page of tile i (num_pages, all of whose boxes read zeros, for an id
-      // outside the pool) and its first row there, where somebody sees these rows
-      auto look = [&](int i, int& id, int& row) {
-        const int pos = (u.tile0 + g.t0 + i) * kBN + rb * maps.box;
+      // the page of rows k of tile i (num_pages, all of whose boxes read zeros, for an id
+      // outside the pool) and the first row there, where somebody sees these rows
+      auto first_pos = [&](int i, int k) { return (u.tile0 + g.t0 + i) * kBN + k * maps.box; };
+      auto visible = [&](int i, int k) {
+        const int pos = first_pos(i, k);
+        return i < n && pos < u.hi && pos + maps.box > u.lo;
+      };
+      auto look = [&](int i, int k, int& id, int& row) {
         id = -1;
         row = 0;
-        if (i >= n || pos >= u.hi || pos + maps.box <= u.lo) return;
-        const int pg = p.page_div(pos);
+        if (!visible(i, k)) return;
+        const int pos = first_pos(i, k), pg = p.page_div(pos);
         row = pos - pg * p.page;
         id = p.table[(int64_t)w.at.b * p.width + pg];
-      };
-      auto load = [&](const CUtensorMap* map, int place, int id, int row, bool have, int full) {
-#pragma unroll
-        for (int blk = 0; blk < NBLK; ++blk) {
-          const uint32_t pos = at + (uint32_t)(place * NBLK + blk), sl = pos % NB;
-          if (pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (pos / NB - 1) & 1, 120);
-          ok = __all_sync(~0u, ok);
-          if (!ok) return;
-          issued = pos + 1;
-          const bool mine = have && ch < (DP - 128 * blk < 128 ? (DP - 128 * blk) / 64 : C::BW / 64);
-          const unsigned all = __ballot_sync(~0u, mine);
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar(full + sl), (uint32_t)__popc(all) * maps.box * 128);
-          __syncwarp();
-          if (mine)
-            tma_load_4d(sRing + sl * C::SLOT + ch * 16384 + rb * maps.box * 128, map,
-                        bar(full + sl), 128 * blk + 64 * ch, row, kvh, id);
-        }
-      };
-      auto visible = [&](int i) {
-        const int pos = (u.tile0 + g.t0 + i) * kBN + rb * maps.box;
-        return i < n && pos < u.hi && pos + maps.box > u.lo;
       };
       auto valid = [&](int id) {
         if (id >= 0 && id < p.num_pages) return id;
         report(kBadPageSite);
         return p.num_pages;
       };
+      auto box_load = [&](const CUtensorMap* map, uint32_t sl, int full, int blk, int k, int c,
+                          int row, int id) {
+        if constexpr (FEED == kTma)
+          tma_load_4d(sRing + sl * C::SLOT + c * 16384 + k * maps.box * 128, map, bar(full + sl),
+                      128 * blk + 64 * c, row, kvh, id);
+        else
+          tma_load_4d(sRaw + sl * C::RAW + k * maps.box * 128, map, bar(full + sl), 128 * blk, row,
+                      kvh, id);
+      };
+      auto load = [&](const CUtensorMap* map, int place, int i, int id, int row, bool have,
+                      int full) {
+#pragma unroll
+        for (int blk = 0; blk < NBLK; ++blk) {
+          const uint32_t pos = at + (uint32_t)(place * NBLK + blk), sl = pos % SLOTS;
+          if (pos >= SLOTS) wait_or_fail(ok, bar(TO_EMPTY + sl), (pos / SLOTS - 1) & 1, 120);
+          ok = __all_sync(~0u, ok);
+          if (!ok) return;
+          issued = pos + 1;
+          const int chunks = FEED == kConvert             ? 1
+                             : DP - 128 * blk < 128 ? (DP - 128 * blk) / 64
+                                                    : C::BW / 64;
+          if (one_each) {
+            const bool mine = have && ch < chunks;
+            const unsigned all = __ballot_sync(~0u, mine);
+            if (lane == 0)
+              mbar_arrive_expect_tx(bar(full + sl), (uint32_t)__popc(all) * maps.box * 128);
+            __syncwarp();
+            if (mine) box_load(map, sl, full, blk, rb, ch, row, id);
+          } else {
+            int boxes = 0;
+            for (int k = lane; k < nbox; k += 32) boxes += visible(i, k) ? 1 : 0;
+            boxes = __reduce_add_sync(~0u, boxes);
+            if (lane == 0) mbar_arrive_expect_tx(bar(full + sl), (uint32_t)boxes * maps.box * 128);
+            __syncwarp();
+            for (int k = lane; k < nbox; k += 32) {
+              int id1, row1;
+              look(i, k, id1, row1);
+              if (visible(i, k)) box_load(map, sl, full, blk, k, 0, row1, valid(id1));
+            }
+          }
+        }
+      };
       // ids are asked for two tiles ahead
       int id0, row0, id1, row1, id2, row2;
-      look(0, id0, row0);
-      look(1, id1, row1);
-      bool have0 = visible(0);
+      look(0, rb, id0, row0);
+      look(1, rb, id1, row1);
+      bool have0 = visible(0, rb);
       if (have0) id0 = valid(id0);
-      if (n > 0) load(&maps.k, k_place(0), id0, row0, have0, C::FULL);
+      if (n > 0) load(&maps.k, k_place(0), 0, id0, row0, have0, TO_FULL);
       for (int i = 0; i < n && ok; ++i) {
-        look(i + 2, id2, row2);
-        const bool have1 = visible(i + 1);
+        look(i + 2, rb, id2, row2);
+        const bool have1 = visible(i + 1, rb);
         if (i + 1 < n) {
           if (have1) id1 = valid(id1);
-          load(&maps.k, k_place(i + 1), id1, row1, have1, C::FULL);
+          load(&maps.k, k_place(i + 1), i + 1, id1, row1, have1, TO_FULL);
         }
-        load(&maps.v, v_place(i, n), id0, row0, have0,
-             seen.edge((u.tile0 + g.t0 + i) * kBN) ? C::LANDED : C::FULL);
+        load(&maps.v, v_place(i, n), i, id0, row0, have0,
+             FEED == kTma && seen.edge(first_pos(i, 0)) ? C::LANDED : TO_FULL);
         id0 = id1;
         row0 = row1;
         have0 = have1;
@@ -734,9 +898,9 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       if (!ok) break;
     }
     // nothing may still be landing when the CTA exits
-    for (uint32_t pos = issued > NB ? issued - NB : 0; pos < issued; ++pos)
-      mbar_wait(bar(C::FULL + pos % NB), (pos / NB) & 1);
-  } else if (FEED != kConvert && warp == 4 * NS + 2) {
+    for (uint32_t pos = issued > SLOTS ? issued - SLOTS : 0; pos < issued; ++pos)
+      mbar_wait(bar(TO_FULL + pos % SLOTS), (pos / SLOTS) & 1);
+  } else if (FEED != kConvert && warp == C::CLEAN) {
     // -------------------------------------------------- V where rows are hidden
     // (its blocks arrive on a barrier of their own, the ring's is for the MMA)
     uint32_t at = 0, uses = 0;
@@ -801,12 +965,9 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       ++seg;
       at += (uint32_t)(2 * n * NBLK);
     }
-  } else if (FEED != kTma) {
-    // ---------------------------------------------------- rows one by one
-    // kRows: warps 1 and 3 behind the MMA warp; kConvert: warps 1, 2 and 3.
-    const int wi = warp - 4 * NS - 1;
-    const int tid = (FEED == kRows ? wi / 2 : wi) * 32 + lane;
-    constexpr int EB = FEED == kConvert ? 1 : 2;  // bytes of a cached element
+  } else if (FEED != kTma && warp >= C::FEEDER) {
+    // ------------------------------------------- rows one by one, or conversions
+    const int tid = (warp - C::FEEDER) * 32 + lane;
     // The blocks of this share in the ring's order.
     struct Blocks {
       Walk w;
@@ -825,8 +986,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         blk = 0;
         value = false;
       }
-      __device__ __forceinline__ void begin(const Params& p, int cta) {
-        w.begin(p, cta);
+      __device__ __forceinline__ void begin(const Params& p, const Start& from, const Start& to) {
+        w.begin(from, to);
         pos = 0;
         seg = 0;
         settle(p);
@@ -858,117 +1019,88 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       }
       __device__ __forceinline__ int pos0() const { return (g.unit.tile0 + g.t0 + i) * kBN; }
     };
-    // Calls f(row, chunk, element offset or -1) for this thread's 16-byte chunks of a block.
-    auto chunks_of = [&](const Blocks& z, auto f) {
-      constexpr int E = 16 / EB;
-      const bool narrow = DP - 128 * z.blk < 128 && DP > 128;  // the 64 columns behind 128
-      const int per_row = (narrow ? 64 : C::BW) / E;
-      const int c = tid % per_row, step = C::FEEDERS / per_row;
-      const int pos0 = z.pos0(), kvh = z.w.at.kvh, col = 128 * z.blk + c * E;
-      const int64_t head = kvh * p.head_stride + col;
-#pragma unroll 4
-      for (int row = tid / per_row; row < kBN; row += step) {
-        const int pos = pos0 + row;
-        int64_t off = -1;
-        if (pos >= z.g.unit.lo && pos < z.g.unit.hi && col < p.dim) {
-          const int pg = p.page_div(pos);
-          const int id = p.table[(int64_t)z.w.at.b * p.width + pg];
-          if (id >= 0 && id < p.num_pages)
-            off = id * p.page_stride + (int64_t)(pos - pg * p.page) * p.row_stride + head;
-          else
-            report(kBadPageSite);
-        }
-        f(row, c, off);
-      }
-    };
+    Blocks z;
     if constexpr (FEED == kRows) {
-      Blocks z;
-      for (z.begin(p, cta); z.more && ok; z.step(p)) {
+      for (z.begin(p, from, to); z.more && ok; z.step(p)) {
         const uint32_t sl = z.pos % NB;
         if (z.pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (z.pos / NB - 1) & 1, 121);
         if (!ok) break;
-        const char* base = (const char*)(z.value ? p.v : p.k);
-        chunks_of(z, [&](int row, int c, int64_t off) {
+        const __nv_bfloat16* base = (const __nv_bfloat16*)(z.value ? p.v : p.k);
+        // 16-byte chunk c of every `step`-th row; the block behind 128 columns may have 64
+        const int per_row = DP > 128 && DP - 128 * z.blk < 128 ? 8 : C::BW / 8;
+        const int c = tid % per_row, step = C::FEEDERS / per_row;
+        const int pos0 = z.pos0(), kvh = z.w.at.kvh, col = 128 * z.blk + c * 8;
+        const int64_t head = kvh * p.head_stride + col;
+#pragma unroll 4
+        for (int row = tid / per_row; row < kBN; row += step) {
+          const int pos = pos0 + row;
+          const __nv_bfloat16* src = nullptr;
+          if (pos >= z.g.unit.lo && pos < z.g.unit.hi && col < p.dim) {
+            const int pg = p.page_div(pos);
+            const int id = p.table[(int64_t)z.w.at.b * p.width + pg];
+            if (id >= 0 && id < p.num_pages)
+              src = base + id * p.page_stride + (int64_t)(pos - pg * p.page) * p.row_stride + head;
+            else
+              report(kBadPageSite);
+          }
           cp_async16(sRing + sl * C::SLOT + (c >> 3) * 16384 + sw128_offset(row, (c & 7) * 8),
-                     off >= 0 ? base + off * EB : base, off >= 0 ? 16u : 0u);
-        });
-        const bool edge = z.value && Seen(p, z.w.seq, z.g.unit).edge(z.pos0());
+                     src ? src : base, src ? 16u : 0u);
+        }
+        const bool edge = z.value && Seen(p, z.w.seq, z.g.unit).edge(pos0);
         cp_async_mbar_arrive(bar((edge ? C::LANDED : C::FULL) + sl));
       }
       cp_async_wait_all();
     } else if constexpr (FEED == kConvert) {
-      // A thread converts the very chunks that it copied, so the staging ring needs no
-      // barriers: its own groups of copies order it.
-      constexpr int RS = C::RS;
-      Blocks ahead, z;
-      ahead.begin(p, cta);
-      z.begin(p, cta);
-      auto raw_at = [&](uint32_t pos, int row, int c) {
-        return sRaw + (pos % RS) * C::RAW + row * C::BW + c * 16;
-      };
-      auto ask = [&]() {
-        if (ahead.more) {
-          const char* base = (const char*)(ahead.value ? p.v : p.k);
-          chunks_of(ahead, [&](int row, int c, int64_t off) {
-            cp_async16(raw_at(ahead.pos, row, c), off >= 0 ? base + off : base,
-                       off >= 0 ? 16u : 0u);
-          });
-          ahead.step(p);
-        }
-        cp_async_commit();
-      };
-      for (int k = 0; k < RS - 1; ++k) ask();
-      for (; z.more && ok; z.step(p)) {
-        ask();
-        cp_async_wait_group<RS - 1>();
-        const uint32_t sl = z.pos % NB;
+      for (z.begin(p, from, to); z.more && ok; z.step(p)) {
+        const uint32_t sl = z.pos % NB, rs = z.pos % C::RS;
+        wait_or_fail(ok, bar(C::RFULL + rs), (z.pos / C::RS) & 1, 123);
         if (z.pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (z.pos / NB - 1) & 1, 122);
         if (!ok) break;
-        const Seen seen(p, z.w.seq, z.g.unit);
-        const bool edge = z.value && seen.edge(z.pos0());
+        const bool edge = z.value && Seen(p, z.w.seq, z.g.unit).edge(z.pos0());
+        const int lo = z.g.unit.lo - z.pos0(), hi = z.g.unit.hi - z.pos0();  // rows that are seen
         bool met = false;
-        const bool narrow = DP - 128 * z.blk < 128 && DP > 128;
-        const int per_row = (narrow ? 64 : C::BW) / 16;
-        const int c = tid % per_row;
+        constexpr int PER_ROW = C::BW / 16;  // 16-element chunks
+        const int c = tid % PER_ROW;
+        const uint32_t from = sRaw + rs * C::RAW + c * 16;
+        const uint32_t to = sRing + sl * C::SLOT + (c >> 2) * 16384;
+        const int c8 = (c & 3) * 16;  // the chunk's first column of 64
 #pragma unroll 4
-        for (int row = tid / per_row; row < kBN; row += C::FEEDERS / per_row) {
+        for (int row = tid / PER_ROW; row < kBN; row += C::FEEDERS / PER_ROW) {
           uint32_t x[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                       : "r"(raw_at(z.pos, row, c))
+                       : "r"(from + row * 128)
                        : "memory");
           if (edge) {
+            const bool seen_row = row >= lo && row < hi;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t nan = __vcmpeq4(x[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-              met |= nan != 0;
-              x[e] &= ~nan;
+              met |= seen_row && nan != 0;
+              x[e] = seen_row ? x[e] & ~nan : 0u;
             }
           }
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_half2(x[e], y[2 * e], y[2 * e + 1]);
-          const uint32_t part = sRing + sl * C::SLOT + (c >> 2) * 16384;
-          const int c8 = (c & 3) * 2;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           part + sw128_offset(row, c8 * 8)),
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + sw128_offset(row, c8)),
                        "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                        : "memory");
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           part + sw128_offset(row, c8 * 8 + 8)),
+                           to + sw128_offset(row, c8 + 8)),
                        "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
                        : "memory");
         }
         if (met) dirty[z.seg & 7] = z.seg;
+        mbar_arrive(bar(C::REMPTY + rs));
         fence_async_shared();
         mbar_arrive(bar(C::FULL + sl));
       }
-      cp_async_wait_all();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4 * NS) {
+  if (warp == C::MMA) {
     __syncwarp();
     tmem_dealloc(tmem, 512);
   }
@@ -993,20 +1125,21 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
     }
   }
   Maps maps = {};
-  if (FEED == kTma) {
-    maps.box = p.page & -p.page;
+  if (FEED != kRows) {
+    constexpr int EB = FEED == kTma ? 2 : 1;
+    maps.box = p.page & -p.page;  // the largest power of two in the page size
     if (maps.box > kBN) maps.box = kBN;
     // (the stride of a dimension of one element is not used: any multiple of 16 bytes will do)
     auto stride = [&](int64_t elements, int extent) {
-      return extent > 1 ? (uint64_t)elements * 2 : (uint64_t)((p.dim * 2 + 15) / 16 * 16);
+      return (uint64_t)(extent > 1 ? elements : p.dim) * EB;
     };
     const uint64_t dims[4] = {(uint64_t)p.dim, (uint64_t)p.page, (uint64_t)p.kv_heads,
                               (uint64_t)p.num_pages};
     const uint64_t strides[3] = {stride(p.row_stride, p.page), stride(p.head_stride, p.kv_heads),
                                  stride(p.page_stride, p.num_pages)};
-    const uint32_t box[4] = {64, (uint32_t)maps.box, 1, 1};
-    if (!make_tmap_bf16_4d(&maps.k, p.k, dims, strides, box) ||
-        !make_tmap_bf16_4d(&maps.v, p.v, dims, strides, box))
+    const uint32_t box[4] = {128u / EB, (uint32_t)maps.box, 1, 1};
+    auto* make = FEED == kTma ? make_tmap_bf16_4d : make_tmap_u8_4d;
+    if (!make(&maps.k, p.k, dims, strides, box) || !make(&maps.v, p.v, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   KernelTimer kt("chunk_sm103", stream);

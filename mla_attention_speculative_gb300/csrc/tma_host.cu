@@ -127,4 +127,13 @@ bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t dims[4
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool make_tmap_u8_4d(CUtensorMap* map, const void* base, const uint64_t dims[4],
+                     const uint64_t strides_bytes[3], const uint32_t box[4]) {
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
+  const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
+  return encode_cached(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, d, st, b,
+                       CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 }  // namespace mla

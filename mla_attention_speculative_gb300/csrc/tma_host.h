@@ -32,5 +32,8 @@ bool make_tmap_f32_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64
 // memory with box[3] outermost.
 bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t dims[4],
                        const uint64_t strides_bytes[3], const uint32_t box[4]);
+// The same for bytes, without a swizzle: a box's rows lie box[0] bytes apart.
+bool make_tmap_u8_4d(CUtensorMap* map, const void* base, const uint64_t dims[4],
+                     const uint64_t strides_bytes[3], const uint32_t box[4]);
 
 }  // namespace mla
