@@ -341,16 +341,20 @@ __device__ __forceinline__ Record make_record(const Params& p, int c, long long 
 // call returns.
 constexpr int kInside = 256;
 struct PlanScratch {
-  long long base[kInside + 1];
+  long long cost[kInside], base[kInside + 1];
   long long warp[kInside / 32];
   Start start[2];
 };
 __device__ __forceinline__ void find_share(const Params& p, int cta, PlanScratch& t, Start& from,
                                            Start& to) {
+  constexpr int kWarps = kInside / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // neighbouring sequences in different warps, so that long ones are added up side by side
+  if (warp < kWarps) t.cost[lane * kWarps + warp] = sequence_cost(p, lane * kWarps + warp) * p.kv_heads;
+  __syncthreads();
   long long upto = 0;
-  if (warp < kInside / 32) {
-    upto = sequence_cost(p, tid) * p.kv_heads;
+  if (warp < kWarps) {
+    upto = t.cost[tid];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, upto, o);
@@ -361,12 +365,12 @@ __device__ __forceinline__ void find_share(const Params& p, int cta, PlanScratch
   __syncthreads();
   long long total = 0, before = 0;
 #pragma unroll
-  for (int w = 0; w < kInside / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     const long long y = t.warp[w];
     if (w < warp) before += y;
     total += y;
   }
-  if (warp < kInside / 32) t.base[tid + 1] = before + upto;
+  if (warp < kWarps) t.base[tid + 1] = before + upto;
   if (tid == 0) t.base[0] = 0;
   __syncthreads();
   auto base = [&](int b) { return t.base[b]; };

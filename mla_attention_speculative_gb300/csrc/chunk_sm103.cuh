@@ -69,8 +69,10 @@ struct Shape {
   static constexpr int QB = 128 * DP * 2;             // bytes of 128 queries
   static constexpr int SLOT = kBN * BW * 2;
   static constexpr int RAW = FEED == kConvert ? kBN * 128 : 0;  // a block's bytes, 128 a row
-  static constexpr int NB = FEED == kConvert ? (DP == 64 ? 6 : 3) : (DP == 64 ? 10 : 5);
-  static constexpr int RS = FEED == kConvert ? 4 : 0;
+  static constexpr int NB =
+      FEED == kConvert ? (DP == 64 ? 6 : DP == 128 ? 3 : 4) : (DP == 64 ? 10 : 5);
+  static constexpr int RS = FEED == kConvert ? (DP <= 128 ? 4 : 2) : 0;
+  static_assert(NB >= (NBLK == 1 ? 3 : 2 * NBLK), "the ring is too short");
   // warps: softmax, then the MMA issuer, the TMA boxes, V where rows are hidden (one is
   // left over), and four that copy or convert
   static constexpr int MMA = 4 * NS, TMA = MMA + 1, CLEAN = MMA + 2, FEEDER = MMA + 4;
@@ -372,19 +374,19 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         uint32_t u0[32], u1[32];
         float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         const bool edge = seen.edge(pos0);
-        // f(scores, piece) for the four pieces; the first one is under way
+        // f(scores, piece) for the four pieces; the first one is under way.  (A loop: code
+        // that stays in the instruction cache beside the MMA warp's is worth more than the
+        // few instructions that an unrolled form saves.)
         auto pieces = [&](auto f) {
-          tmem_wait_ld<32>(u0);
-          tmem_ld32(tS + 32, u1);
-          f(u0, 0);
-          tmem_wait_ld<32>(u1);
-          tmem_ld32(tS + 64, u0);
-          f(u1, 1);
-          tmem_wait_ld<32>(u0);
-          tmem_ld32(tS + 96, u1);
-          f(u0, 2);
-          tmem_wait_ld<32>(u1);
-          f(u1, 3);
+#pragma unroll 1
+          for (int k = 0; k < 4; k += 2) {
+            tmem_wait_ld<32>(u0);
+            tmem_ld32(tS + 32 * (k + 1), u1);
+            f(u0, k);
+            tmem_wait_ld<32>(u1);
+            if (k == 0) tmem_ld32(tS + 64, u0);
+            f(u1, k + 1);
+          }
         };
         auto hide = [&](uint32_t* u, int k) {
 #pragma unroll
@@ -657,12 +659,14 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     }
   } else if (warp == C::MMA) {
     // ----------------------------------------------------------------- MMA
-    // One thread issues for both streams in turn, O += P V of a tile and S of the next
+    // The whole warp walks and waits, so that descriptors are uniform registers, and one
+    // thread of it issues for both streams in turn, O += P V of a tile and S of the next
     // one.  (An issuer for each, whose instructions the pipe takes alternately, made
     // both streams wait longer: 8192 rows 649 us against 579.)
     const uint32_t id_s = HALF ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
     const int nk = (p.dim + 15) / 16;  // steps of 16 columns
     const bool full_width = nk == DP / 16;
+    const bool leader = elect_one();
     Slot ring = {0, 0};            // of this segment's first block
     uint32_t before[2] = {0, 0};   // tiles of each stream (or S buffer) before it
     uint32_t seg = 0;
@@ -675,7 +679,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       const int n = g.t1 - g.t0, rows = g.unit.r1 - g.unit.r0;
       if (n == 0) continue;
       const bool split = NS == 2 && rows <= 128;
-      if (lane == 0) {
+      {
         auto landed = [&](const Slot& t) {
           wait_or_fail(ok, bar(C::FULL + t.i), t.phase, 110);
           if (FEED == kRows) fence_async_shared();
@@ -692,6 +696,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
             const uint64_t dqb = dq + (uint64_t)(blk * 2048);
             // (a condition on single MMAs of the unrolled form made the compiler give some of
             // them another one's descriptor: so either all of them, or a loop)
+            if (!leader) continue;
             if (full_width) {
 #pragma unroll
               for (int k = 0; k < C::BW / 16; ++k)
@@ -707,8 +712,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
               }
             }
             if (free) mma_commit(bar(C::EMPTY + t.i));
+            if (blk == NBLK - 1) mma_commit(bar(C::SFULL + x));
           }
-          mma_commit(bar(C::SFULL + x));
         };
         // O += P V of the tile at `t`, number j of its stream or S buffer.  The first half
         // of P is enough to begin with.
@@ -729,18 +734,22 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
             const uint32_t nn = blk == 0 ? first_n : last_n;
             const uint32_t id_o = HALF ? idesc_f16(128, nn, 0, 1) : idesc_bf16(128, nn, 0, 1);
             const uint32_t dst = tmem + o * DP + 128 * blk, from = tmem + C::TM_S + 128 * x;
+            if (leader) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_tmem_a(dst, from + 8 * k, dv + 128 * k, id_o, !begin || k > 0);
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_tmem_a(dst, from + 8 * k, dv + 128 * k, id_o, !begin || k > 0);
+            }
             if (blk == 0) {
               wait_or_fail(ok, bar(C::PFULL + x), parity, 112);
               if (!ok) return;
               tc_fence_after();
             }
+            if (leader) {
 #pragma unroll
-            for (int k = 4; k < 8; ++k)
-              mma_bf16_tmem_a(dst, from + 8 * k, dv + 128 * k, id_o, 1);
-            if (free) mma_commit(bar(C::EMPTY + t.i));
+              for (int k = 4; k < 8; ++k)
+                mma_bf16_tmem_a(dst, from + 8 * k, dv + 128 * k, id_o, 1);
+              if (free) mma_commit(bar(C::EMPTY + t.i));
+            }
           }
         };
         // where the next tiles of K and V lie: K0 K1 V0 K2 V1 .. V(n-1)
@@ -748,17 +757,17 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         vt.move<NB>((n == 1 ? 1 : 2) * NBLK);
         wait_or_fail(ok, bar(C::QFULL), seg & 1, 113);
         if (NS == 2 && !split) {
-          const uint64_t dq1 = dq0 + (C::QB >> 4);
-          scores(0, dq0, kt, true, false);
-          scores(1, dq1, kt, false, true);
+          constexpr uint64_t kTile = C::QB >> 4;
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) scores(x, dq0 + x * kTile, kt, x == 0, x == 1);
           kt.move<NB>(NBLK);
           for (int i = 0; i < n && ok; ++i) {
-            products(0, 0, vt, i, i == 0, true, false);
-            if (i + 1 < n) scores(0, dq0, kt, true, false);
-            else mma_commit(bar(C::OFULL));
-            products(1, 1, vt, i, i == 0, false, true);
-            if (i + 1 < n) scores(1, dq1, kt, false, true);
-            else mma_commit(bar(C::OFULL + 1));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              products(x, x, vt, i, i == 0, x == 0, x == 1);
+              if (i + 1 < n) scores(x, dq0 + x * kTile, kt, x == 0, x == 1);
+              else if (leader) mma_commit(bar(C::OFULL + x));
+            }
             kt.move<NB>(2 * NBLK);
             vt.move<NB>((i + 2 < n ? 2 : 1) * NBLK);
           }
@@ -773,12 +782,13 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
             const int x = i & 1;
             products(x, NS == 2 ? x : 0, vt, i >> 1, NS == 2 ? i < 2 : i == 0, true, true);
             vt.move<NB>((i + 2 < n ? 2 : 1) * NBLK);
-            if (NS == 1) mma_commit(bar(C::PVDONE + x));
+            if (NS == 1 && leader) mma_commit(bar(C::PVDONE + x));
             if (i + 2 < n) {
               scores(x, dq0, kt, true, true);
               kt.move<NB>(2 * NBLK);
             }
-            if (NS == 2 ? i + 2 >= n : i + 1 == n) mma_commit(bar(C::OFULL + (NS == 2 ? x : 0)));
+            if (leader && (NS == 2 ? i + 2 >= n : i + 1 == n))
+              mma_commit(bar(C::OFULL + (NS == 2 ? x : 0)));
           }
         }
         ring.move_far<NB>((uint32_t)(2 * n * NBLK));
@@ -788,7 +798,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       }
       __syncwarp();
     }
-    if (lane == 0) {
+    if (leader) {
       // nothing that was issued may still run when tensor memory is given back
       mma_commit(bar(C::DRAIN));
       if (!mbar_wait(bar(C::DRAIN), 0)) report(115);
@@ -1024,6 +1034,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       for (z.begin(p, from, to); z.more && ok; z.step(p)) {
         const uint32_t sl = z.pos % NB;
         if (z.pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (z.pos / NB - 1) & 1, 121);
+        ok = __all_sync(~0u, ok);
         if (!ok) break;
         const __nv_bfloat16* base = (const __nv_bfloat16*)(z.value ? p.v : p.k);
         // 16-byte chunk c of every `step`-th row; the block behind 128 columns may have 64
@@ -1055,6 +1066,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         const uint32_t sl = z.pos % NB, rs = z.pos % C::RS;
         wait_or_fail(ok, bar(C::RFULL + rs), (z.pos / C::RS) & 1, 123);
         if (z.pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (z.pos / NB - 1) & 1, 122);
+        ok = __all_sync(~0u, ok);
         if (!ok) break;
         const bool edge = z.value && Seen(p, z.w.seq, z.g.unit).edge(z.pos0());
         const int lo = z.g.unit.lo - z.pos0(), hi = z.g.unit.hi - z.pos0();  // rows that are seen
