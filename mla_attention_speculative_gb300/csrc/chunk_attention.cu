@@ -90,13 +90,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
 // Join
 // ---------------------------------------------------------------------------
 
-constexpr int kJoinThreads = 256, kJoinY = 32, kJoinLoads = 4;
+constexpr int kJoinThreads = 256, kJoinY = 16, kJoinLoads = 16;
 
 // The parts of a cut unit's rows are weighted by 2^(m - max m) and added up in
 // order, so repeated calls give the same bits.  A warp takes a row, a lane four
-// columns of it; the row's first parts are asked for beside their maxima and sums.
-// (Four rows to a CTA with barriers between the steps took 56 us for the 152 cut
-// units of 256 rows of a prompt of 8192.)
+// columns of it at a time; with few parts, as in a prompt, two rows side by side,
+// all of whose parts are asked for beside their maxima and sums (152 cut units of
+// 256 rows: one trip to memory, not three).
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const Params p, const int kind) {
   sm103::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
@@ -111,18 +111,78 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const Params p
   auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
   const float vs = p.v_scale ? p.v_scale[rec.kvh] : 1.f;
   const int64_t step = (int64_t)p.bm * p.dp;
-  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < rows;
-       row += kJoinY * (kJoinThreads / 32)) {
+  auto write = [&](int row, int c, const float4& a, float M, float L) {
+    const int i = p.group_div(rec.r0 + row), j = rec.r0 + row - i * p.group;
+    const int64_t head = (int64_t)(rec.row0 + i) * p.heads + rec.kvh * p.group + j;
+    if (c == 0 && p.lse)
+      p.lse[head] =
+          L == 0.f ? -INFINITY
+                   : (M + (log2f(L) - (kind == kE4m3 ? kShift : 0.f))) * 0.6931471805599453f;
+    if (c >= p.dim) return;
+    const float inv = L == 0.f ? 0.f : vs / L;
+    if (kind == kFp32)
+      *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c) =
+          make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    else
+      *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c) = make_uint2(
+          sm103::pack_bf16(a.x * inv, a.y * inv), sm103::pack_bf16(a.z * inv, a.w * inv));
+  };
+  // (a part whose rows all weigh nothing holds zeros, or NaN where the row is NaN)
+  auto add = [](float4& a, float w, const float4& x) {
+    a.x = fmaf(w, x.x, a.x);
+    a.y = fmaf(w, x.y, a.y);
+    a.z = fmaf(w, x.z, a.z);
+    a.w = fmaf(w, x.w, a.w);
+  };
+  constexpr int kWarps = kJoinThreads / 32, kFew = 4, kPair = 2;
+  if (rec.parts <= kFew) {
+    for (int row0 = (blockIdx.y * kWarps + warp) * kPair; row0 < rows;
+         row0 += kJoinY * kWarps * kPair) {
+      for (int c = 4 * lane; c - 4 * lane < p.dim; c += 128) {
+        float2 ml[kPair][kFew];
+        float4 x[kPair][kFew];
+#pragma unroll
+        for (int r = 0; r < kPair; ++r) {
+#pragma unroll
+          for (int k = 0; k < kFew; ++k) {
+            ml[r][k] = make_float2(-INFINITY, 0.f);
+            x[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k >= rec.parts || row0 + r >= rows) continue;
+            ml[r][k] = p.part_ml[slot(k) * p.bm + row0 + r];
+            if (c < p.dim)
+              x[r][k] = *reinterpret_cast<const float4*>(p.part_o + slot(k) * step +
+                                                         (int64_t)(row0 + r) * p.dp + c);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kPair; ++r) {
+          if (row0 + r >= rows) continue;
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int k = 0; k < kFew; ++k) M = fmaxf(M, ml[r][k].x);
+          const float base = M == -INFINITY ? 0.f : M;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kFew; ++k) {
+            if (k >= rec.parts) continue;
+            const float w = sm103::ex2(ml[r][k].x - base);
+            L = fmaf(w, ml[r][k].y, L);
+            add(a, w, x[r][k]);
+          }
+          write(row0 + r, c, a, M, L);
+        }
+      }
+    }
+    return;
+  }
+  for (int row = blockIdx.y * kWarps + warp; row < rows; row += kJoinY * kWarps) {
     float M = -INFINITY;
     for (int k = lane; k < rec.parts; k += 32) M = fmaxf(M, p.part_ml[slot(k) * p.bm + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
     const float base = M == -INFINITY ? 0.f : M;
-    const int i = p.group_div(rec.r0 + row), j = rec.r0 + row - i * p.group;
-    const int64_t head = (int64_t)(rec.row0 + i) * p.heads + rec.kvh * p.group + j;
     for (int c = 4 * lane; c - 4 * lane < p.dim; c += 128) {
       const float* part = p.part_o + (int64_t)row * p.dp + c;
-      const bool mine = c < p.dim;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       float L = 0.f;
       for (int k0 = 0; k0 < rec.parts; k0 += 32) {
@@ -139,35 +199,17 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const Params p
         for (int k1 = 0; k1 < n; k1 += kJoinLoads) {
           float4 x[kJoinLoads];
 #pragma unroll
-          for (int e = 0; e < kJoinLoads; ++e) {
-            x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine && k1 + e < n)
+          for (int e = 0; e < kJoinLoads; ++e)
+            if (c < p.dim && k1 + e < n)
               x[e] = *reinterpret_cast<const float4*>(part + slot(k0 + k1 + e) * step);
-          }
 #pragma unroll
           for (int e = 0; e < kJoinLoads; ++e) {
             const float we = __shfl_sync(~0u, w, (k1 + e) & 31);
-            if (k1 + e >= n) continue;
-            // (a part whose rows all weigh nothing holds zeros, or NaN where the row is NaN)
-            a.x = fmaf(we, x[e].x, a.x);
-            a.y = fmaf(we, x[e].y, a.y);
-            a.z = fmaf(we, x[e].z, a.z);
-            a.w = fmaf(we, x[e].w, a.w);
+            if (c < p.dim && k1 + e < n) add(a, we, x[e]);
           }
         }
       }
-      if (c == 0 && p.lse)
-        p.lse[head] =
-            L == 0.f ? -INFINITY
-                     : (M + (log2f(L) - (kind == kE4m3 ? kShift : 0.f))) * 0.6931471805599453f;
-      if (!mine) continue;
-      const float inv = L == 0.f ? 0.f : vs / L;
-      if (kind == kFp32)
-        *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c) =
-            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-      else
-        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.out + head * p.dim + c) = make_uint2(
-            sm103::pack_bf16(a.x * inv, a.y * inv), sm103::pack_bf16(a.z * inv, a.w * inv));
+      write(row, c, a, M, L);
     }
   }
 }

@@ -25,8 +25,8 @@ constexpr int kUnitCost = 3;
 // A share does not begin in the first or last kSnap tiles of a unit: a part of one
 // or two tiles costs more to join than to do.
 constexpr int kSnap = 2;
-// The least a share holds, above what the snaps can take from it.
-constexpr int kMinShare = kUnitCost + 2 * kSnap + 2;
+// The least a share holds.
+constexpr int kMinShare = kUnitCost + 1;
 
 // Where a share begins: a unit and a tile within it (b == batch: behind the last).
 struct Start {

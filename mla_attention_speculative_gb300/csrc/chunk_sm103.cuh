@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       const bool second = split && n > 1;  // stream 1 has an accumulator
       const float vs = HALF && p.v_scale ? p.v_scale[kvh] : 1.f;
       const float inv = l == 0.f ? 0.f : vs / l;
-      const bool live = r < rows;
+      const bool live = r < rows, none = __any_sync(~0u, l == 0.f);
       const int i_tok = p.group_div(u.r0 + min(r, rows - 1)),
                 head_in = u.r0 + min(r, rows - 1) - i_tok * p.group;
       const int64_t head = (int64_t)(sq.row0 + i_tok) * p.heads + kvh * p.group + head_in;
@@ -556,66 +556,65 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       float* part_at = p.part_o + ((int64_t)(2 * cta + (g.first ? 1 : 0)) * p.bm + row0) * p.dp;
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        if (n > 0) {
+          tmem_ld32(tmem + lane_base + (NS == 2 && !split ? DP * s : 0) + c, o);
+          if (second) {
+            uint32_t o1[32];
+            tmem_ld32(tmem + lane_base + DP + c, o1);
+            tmem_wait_ld<32>(o);
+            tmem_wait_ld<32>(o1);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t o[16];
-          const int col = c + 16 * half;
-          __syncwarp();
-          if (n > 0) {
-            tmem_ld16(tmem + lane_base + (NS == 2 && !split ? DP * s : 0) + col, o);
-            if (second) {
-              uint32_t o1[16];
-              tmem_ld16(tmem + lane_base + DP + col, o1);
-              tmem_wait_ld<16>(o);
-              tmem_wait_ld<16>(o1);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                // (a stream without weight may hold anything)
-                const float a = wa == 0.f ? 0.f : __uint_as_float(o[e]) * wa;
-                const float b = wb == 0.f ? 0.f : __uint_as_float(o1[e]) * wb;
-                o[e] = __float_as_uint(a + b);
-              }
-            } else {
-              tmem_wait_ld<16>(o);
-            }
-          }
-          if (l == 0.f) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
-          } else if (fix && live) {
-            const int lo = max(first, (u.tile0 + g.t0) * kBN),
-                      hi = min(last, (u.tile0 + g.t1) * kBN - 1);
-#pragma unroll 1
-            for (int e = 0; e < 16; ++e) {
-              if (col + e >= p.dim) continue;
-              const float y = odd_values<FEED>(p, w.at.b, kvh, col + e, lo, hi, seen.lo, seen.hi);
-              // (the array stays in registers: no index at run time)
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (k == e) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
-            }
-          }
-          if (whole) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              uint32_t y[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                y[k] = pack_bf16(__uint_as_float(o[e + 2 * k]) * inv,
-                                 __uint_as_float(o[e + 2 * k + 1]) * inv);
-              const uint32_t at =
-                  stage + lane * 64 + (((2 * half + e / 8) ^ ((lane >> 1) & 3)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]),
-                           "r"(y[1]), "r"(y[2]), "r"(y[3])
-                           : "memory");
-            }
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), wb, __uint_as_float(o[e]) * wa));
           } else {
+            tmem_wait_ld<32>(o);
+          }
+        }
+        if (none) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const uint32_t at = stage + lane * 128 + (((4 * half + e / 4) ^ (lane & 7)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[e]),
-                           "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3])
-                           : "memory");
+          for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : o[e];
+        }
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              y[k] = pack_bf16(__uint_as_float(o[e + 2 * k]) * inv,
+                               __uint_as_float(o[e + 2 * k + 1]) * inv);
+            const uint32_t at = stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]),
+                         "r"(y[1]), "r"(y[2]), "r"(y[3])
+                         : "memory");
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const uint32_t at = stage + lane * 128 + (((e / 4) ^ (lane & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[e]),
+                         "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3])
+                         : "memory");
+          }
+        }
+        if (fix && live && l != 0.f) {
+          // what was set to zero, added to the staged values
+          const int lo = max(first, (u.tile0 + g.t0) * kBN),
+                    hi = min(last, (u.tile0 + g.t1) * kBN - 1);
+#pragma unroll 1
+          for (int e = 0; e < 32 && c + e < p.dim; ++e) {
+            const float y = odd_values<FEED>(p, w.at.b, kvh, c + e, lo, hi, seen.lo, seen.hi);
+            if (y == 0.f) continue;
+            if (whole) {
+              __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(
+                  smem + (stage - sQ) + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4) +
+                  (e & 7) * 2);
+              *v = __float2bfloat16(__bfloat162float(*v) + y * inv);
+            } else {
+              float* v = reinterpret_cast<float*>(smem + (stage - sQ) + lane * 128 +
+                                                  (((e / 4) ^ (lane & 7)) << 4) + (e & 3) * 4);
+              *v += y;
             }
           }
         }
