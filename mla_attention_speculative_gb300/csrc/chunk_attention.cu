@@ -90,14 +90,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
 // Join
 // ---------------------------------------------------------------------------
 
-constexpr int kJoinThreads = 256, kJoinY = 16, kJoinLoads = 16;
+constexpr int kJoinThreads = 256, kJoinY = 32, kJoinLoads = 8;
 
 // The parts of a cut unit's rows are weighted by 2^(m - max m) and added up in
 // order, so repeated calls give the same bits.  A warp takes a row, a lane four
 // columns of it at a time; with few parts, as in a prompt, two rows side by side,
 // all of whose parts are asked for beside their maxima and sums (152 cut units of
 // 256 rows: one trip to memory, not three).
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const Params p, const int kind) {
+__global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const Params p, const int kind) {
   sm103::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
   const Record rec = p.rec[cta];
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const Params p
     a.z = fmaf(w, x.z, a.z);
     a.w = fmaf(w, x.w, a.w);
   };
-  constexpr int kWarps = kJoinThreads / 32, kFew = 4, kPair = 2;
+  constexpr int kWarps = kJoinThreads / 32, kFew = 4, kPair = 1;
   if (rec.parts <= kFew) {
     for (int row0 = (blockIdx.y * kWarps + warp) * kPair; row0 < rows;
          row0 += kJoinY * kWarps * kPair) {

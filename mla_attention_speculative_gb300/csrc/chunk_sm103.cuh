@@ -70,8 +70,8 @@ struct Shape {
   static constexpr int SLOT = kBN * BW * 2;
   static constexpr int RAW = FEED == kConvert ? kBN * 128 : 0;  // a block's bytes, 128 a row
   static constexpr int NB =
-      FEED == kConvert ? (DP == 64 ? 6 : DP == 128 ? 3 : 4) : (DP == 64 ? 10 : 5);
-  static constexpr int RS = FEED == kConvert ? (DP <= 128 ? 4 : 2) : 0;
+      FEED == kConvert ? (DP == 64 ? 6 : 4) : (DP == 64 ? 10 : 5);
+  static constexpr int RS = FEED == kConvert ? 2 : 0;
   static_assert(NB >= (NBLK == 1 ? 3 : 2 * NBLK), "the ring is too short");
   // warps: softmax, then the MMA issuer, the TMA boxes, V where rows are hidden (one is
   // left over), and four that copy or convert
@@ -1075,22 +1075,15 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         const uint32_t from = sRaw + rs * C::RAW + c * 16;
         const uint32_t to = sRing + sl * C::SLOT + (c >> 2) * 16384;
         const int c8 = (c & 3) * 16;  // the chunk's first column of 64
-#pragma unroll 4
-        for (int row = tid / PER_ROW; row < kBN; row += C::FEEDERS / PER_ROW) {
-          uint32_t x[4];
+        constexpr int STEP = C::FEEDERS / PER_ROW, ROUNDS = kBN / STEP;
+        const int row0 = tid / PER_ROW;
+        auto load = [&](int row, uint32_t (&x)[4]) {
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                        : "r"(from + row * 128)
                        : "memory");
-          if (edge) {
-            const bool seen_row = row >= lo && row < hi;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t nan = __vcmpeq4(x[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-              met |= seen_row && nan != 0;
-              x[e] = seen_row ? x[e] & ~nan : 0u;
-            }
-          }
+        };
+        auto put = [&](int row, const uint32_t (&x)[4]) {
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_half2(x[e], y[2 * e], y[2 * e + 1]);
@@ -1101,6 +1094,30 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
                            to + sw128_offset(row, c8 + 8)),
                        "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
                        : "memory");
+        };
+        if (!edge) {
+#pragma unroll
+          for (int k0 = 0; k0 < ROUNDS; k0 += 4) {
+            uint32_t x[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) load(row0 + (k0 + k) * STEP, x[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) put(row0 + (k0 + k) * STEP, x[k]);
+          }
+        } else {
+#pragma unroll 1
+          for (int row = row0; row < kBN; row += STEP) {
+            uint32_t x[4];
+            load(row, x);
+            const bool seen_row = row >= lo && row < hi;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t nan = __vcmpeq4(x[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              met |= seen_row && nan != 0;
+              x[e] = seen_row ? x[e] & ~nan : 0u;
+            }
+            put(row, x);
+          }
         }
         if (met) dirty[z.seg & 7] = z.seg;
         mbar_arrive(bar(C::REMPTY + rs));
