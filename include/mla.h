@@ -637,12 +637,12 @@ mla_status_t mla_chunk_attention(const mla_kv_geometry_t* geom, const void* q,
  * into a shared page is forked to an idle slot, which gets its last page's rows
  * as a copy, and released.
  *
- * As above nothing is read on the host, and each call is one launch.  Outputs
- * must not overlap inputs or one another, except where an argument says so; a
- * call with separate outputs can be repeated with the same result.  Page ids
- * outside [0, num_pages) are passed over and recorded as code 300 in the status
- * word.  batch in [1, 65535]; batch * max_pages_per_seq at most 2^31 - 1; every
- * array 16-byte aligned.
+ * As above nothing is read on the host.  Outputs must not overlap inputs or one
+ * another, except where an argument says so; a call with separate outputs can be
+ * repeated with the same result.  Page ids outside [0, num_pages) are passed over
+ * and recorded as code 300 in the status word.  batch in [1, 65535]; batch *
+ * max_pages_per_seq at most 2^31 - 1; num_pages at most 2^30; every array 16-byte
+ * aligned.
  * ------------------------------------------------------------------------ */
 
 /* Sequences forked to idle slots.  A slot b with held_pages[b] <= 0 and 0 <=

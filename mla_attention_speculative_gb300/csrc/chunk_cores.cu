@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
 #pragma unroll
         for (int b = 0; b < 4; ++b) x[a][b] = 0.f;
 #pragma unroll 4
-      for (int d = 0; d < DP; d += 4) {
+      for (int d = 0; d < p.dim; d += 4) {
         float4 qv[4], kv[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a)

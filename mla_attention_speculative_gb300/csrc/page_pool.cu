@@ -5,11 +5,13 @@
 //
 // The first three only count and move 32-bit words, a few per sequence and
 // page, so latency bounds them.  Each needs phases that see all of what the
-// phase before wrote (counts changed before pages at zero are listed, say), so
-// each is one launch of one cluster of eight CTAs, whose hardware barrier takes
-// a fraction of a launch's time.  Whatever is placed in order (pages of the free
-// list, moves) is placed by exclusive sums over consecutive runs, one run a
-// thread, so results never depend on the order in which threads arrive.
+// phase before wrote (counts changed before pages at zero are listed, say).  For
+// tables of up to kWide entries they are one launch of one cluster of eight CTAs,
+// whose hardware barrier takes a fraction of a launch's time; beyond, the phases
+// that walk over table entries are launches of their own over the whole machine.
+// Whatever is placed in order (pages of the free list, moves) is placed by
+// exclusive sums over consecutive runs, so results never depend on the order in
+// which threads arrive.
 
 #include <cuda_runtime.h>
 
@@ -41,16 +43,26 @@ constexpr int kRun = 4;  // entries of a table row a thread has on their way at 
 
 __device__ __forceinline__ void bad_page() { atomicCAS(&g_pool_status, 0, kBadPageSite); }
 
-// A run of `n` consecutive items for each thread of the cluster.
+// A run of `n` consecutive items for each thread of the cluster, or for each warp.
 struct Run {
   int lo, hi;
-  __device__ __forceinline__ Run(int n, int rank) {
-    const int per = (int)(((long long)n + kAll - 1) / kAll);
-    const long long a = (long long)(rank * kThreads + (int)threadIdx.x) * per;
+  __device__ __forceinline__ Run(int n, int at, int of) {
+    const int per = (int)(((long long)n + of - 1) / of);
+    const long long a = (long long)at * per;
     lo = (int)min((long long)n, a);
     hi = (int)min((long long)n, a + per);
   }
 };
+__device__ __forceinline__ Run thread_run(int n, int rank) {
+  return Run(n, rank * kThreads + (int)threadIdx.x, kAll);
+}
+// (whole lines: a warp's run is read 32 neighbours at a time)
+__device__ __forceinline__ Run warp_run(int n, int rank) {
+  Run r((n + 31) / 32, rank * (kThreads / 32) + (int)(threadIdx.x >> 5), kAll / 32);
+  r.lo = min(n, r.lo * 32);
+  r.hi = min(n, r.hi * 32);
+  return r;
+}
 
 struct Scan {
   int warp[kThreads / 32];
@@ -91,13 +103,14 @@ __device__ __forceinline__ int cluster_scan(Scan& s, int x, int rank, int& all) 
   return before + sum - x;
 }
 
-// Copies n words where the output is another array than the input.
-__device__ __forceinline__ void copy_words(const int32_t* from, int32_t* to, int n, int rank) {
+// Copies n words where the output is another array than the input, by all threads of
+// the launch.
+__device__ __forceinline__ void copy_words(const int32_t* from, int32_t* to, int n) {
   if (from == to) return;
-  const int g = rank * kThreads + threadIdx.x, quads = n / 4;
-  for (int i = g; i < quads; i += kAll)
+  const int g = blockIdx.x * kThreads + threadIdx.x, quads = n / 4, all = gridDim.x * kThreads;
+  for (int i = g; i < quads; i += all)
     reinterpret_cast<int4*>(to)[i] = reinterpret_cast<const int4*>(from)[i];
-  for (int i = quads * 4 + g; i < n; i += kAll) to[i] = from[i];
+  for (int i = quads * 4 + g; i < n; i += all) to[i] = from[i];
 }
 
 struct FreeSpan {
@@ -115,12 +128,12 @@ struct FreeSpan {
 // other as if they were one row, so that single entries of many sequences fill its
 // lanes, and several warps share a sequence where there are few.
 template <typename Where, typename F>
-__device__ __forceinline__ void for_entries(int batch, int rank, Where where, F f) {
-  constexpr int kWarps = kAll / 32;
-  const int lane = threadIdx.x & 31, warp = rank * (kThreads / 32) + (threadIdx.x >> 5);
-  const int size = min(32, (batch + kWarps - 1) / kWarps), groups = (batch + size - 1) / size;
-  const int share = max(1, kWarps / groups);  // warps that share a group
-  for (int g = warp / share; g < groups; g += kWarps / share) {
+__device__ __forceinline__ void for_entries(int batch, Where where, F f) {
+  const int warps = gridDim.x * (kThreads / 32);
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int size = min(32, (batch + warps - 1) / warps), groups = (batch + size - 1) / size;
+  const int share = max(1, warps / groups);  // warps that share a group
+  for (int g = warp / share; g < groups; g += warps / share) {
     const int mine = g * size + lane;
     int lo = 0, hi = 0, x = 0;
     if (lane < size && mine < batch) where(mine, lo, hi, x);
@@ -181,13 +194,37 @@ struct ForkParams {
   }
 };
 
+// The whole pages of the forked slots.
+__device__ __forceinline__ void fork_entries(const ForkParams& p) {
+  for_entries(
+      p.batch,
+      [&](int b, int&, int& hi, int& s) {
+        s = p.source(b);
+        if (s >= 0) p.rows(s, hi);
+      },
+      [&](const int (&b)[kRun], const int (&j)[kRun], const int (&s)[kRun]) {
+        int id[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (j[i] >= 0) id[i] = p.table[(long long)s[i] * p.width + j[i]];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+          if (j[i] < 0) continue;
+          p.table[(long long)b[i] * p.width + j[i]] = id[i];
+          if (id[i] >= 0 && id[i] < p.num_pages) atomicAdd(p.shares_out + id[i], 1);
+          else bad_page();
+        }
+      });
+}
+
+// One cluster.  `entries`: the whole pages as well, not in a launch behind this one.
 __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
-    page_fork_kernel(const ForkParams p) {
+    page_fork_kernel(const ForkParams p, const bool entries) {
   __shared__ Scan s_scan;
   const int rank = (int)sm103::cluster_ctarank();
   sm103::pdl_wait();
-  copy_words(p.shares, p.shares_out, p.num_pages, rank);
-  const Run run(p.batch, rank);
+  copy_words(p.shares, p.shares_out, p.num_pages);
+  const Run run = thread_run(p.batch, rank);
   int wants = 0;
   for (int b = run.lo; b < run.hi; ++b) {
     const int s = p.source(b);
@@ -231,26 +268,13 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
     p.missing[0] = all - taken;
     p.moves[0] = taken;
   }
-  for_entries(
-      p.batch, rank,
-      [&](int b, int&, int& hi, int& s) {
-        s = p.source(b);
-        if (s >= 0) p.rows(s, hi);
-      },
-      [&](const int (&b)[kRun], const int (&j)[kRun], const int (&s)[kRun]) {
-        int id[kRun];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-          if (j[i] >= 0) id[i] = p.table[(long long)s[i] * p.width + j[i]];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-          if (j[i] < 0) continue;
-          p.table[(long long)b[i] * p.width + j[i]] = id[i];
-          if (id[i] >= 0 && id[i] < p.num_pages) atomicAdd(p.shares_out + id[i], 1);
-          else bad_page();
-        }
-      });
+  if (entries) fork_entries(p);
   sm103::cluster_sync();  // no CTA ends while another reads its sum
+}
+
+__global__ void __launch_bounds__(kThreads) page_fork_entries_kernel(const ForkParams p) {
+  sm103::pdl_wait();
+  fork_entries(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -273,18 +297,9 @@ struct ReleaseParams {
 
 // A count holds the holders of a page beyond the first, so every drop takes one
 // off and the pages that end below zero are the ones nobody holds any more.
-__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
-    page_release_kernel(const ReleaseParams p) {
-  __shared__ Scan s_scan;
-  const int rank = (int)sm103::cluster_ctarank();
-  sm103::pdl_wait();
-  const FreeSpan free(p.free_span, p.free_capacity);
-  if (p.shares != p.shares_out) {
-    copy_words(p.shares, p.shares_out, p.num_pages, rank);
-    sm103::cluster_sync();
-  }
+__device__ __forceinline__ void release_entries(const ReleaseParams& p) {
   for_entries(
-      p.batch, rank, [&](int b, int& lo, int& hi, int&) { p.range(b, lo, hi); },
+      p.batch, [&](int b, int& lo, int& hi, int&) { p.range(b, lo, hi); },
       [&](const int (&b)[kRun], const int (&j)[kRun], const int (&)[kRun]) {
         int id[kRun];
 #pragma unroll
@@ -297,26 +312,56 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
           else bad_page();
         }
       });
-  for (int b = rank * kThreads + threadIdx.x; b < p.batch; b += kAll) {
+  for (int b = blockIdx.x * kThreads + threadIdx.x; b < p.batch; b += gridDim.x * kThreads) {
     int need, h;
     p.range(b, need, h);
     p.held_out[b] = need;
   }
-  sm103::cluster_sync();
-  const Run run(p.num_pages, rank);
-  int freed = 0;
-  for (int i = run.lo; i < run.hi; ++i) freed += __ldcg(p.shares_out + i) < 0 ? 1 : 0;
+}
+
+// One cluster.  `entries`: the drops as well, not in launches ahead of this one.
+__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
+    page_release_kernel(const ReleaseParams p, const bool entries) {
+  __shared__ Scan s_scan;
+  const int rank = (int)sm103::cluster_ctarank(), lane = threadIdx.x & 31;
+  sm103::pdl_wait();
+  const FreeSpan free(p.free_span, p.free_capacity);
+  if (entries) {
+    if (p.shares != p.shares_out) {
+      copy_words(p.shares, p.shares_out, p.num_pages);
+      sm103::cluster_sync();
+    }
+    release_entries(p);
+    sm103::cluster_sync();
+  }
+  const Run run = warp_run(p.num_pages, rank);
+  auto freed = [&](int i) { return i + lane < run.hi && __ldcg(p.shares_out + i + lane) < 0; };
+  int mine = 0;  // of this warp
+#pragma unroll 8
+  for (int i = run.lo; i < run.hi; i += 32) mine += __popc(__ballot_sync(~0u, freed(i)));
   int all;
-  int at = cluster_scan(s_scan, freed, rank, all);
+  int at = cluster_scan(s_scan, lane == 0 ? mine : 0, rank, all);
+  at = __shfl_sync(~0u, at, 0);
   // in front of the list as far as there is room, the others behind it
   const int front = min(all, free.first);
-  for (int i = run.lo; i < run.hi && freed > 0; ++i) {
-    if (__ldcg(p.shares_out + i) >= 0) continue;
-    const long long to = at < front ? free.first - front + at : (long long)free.end + at - front;
-    if (to < p.free_capacity) p.free_pages[to] = i;
-    p.shares_out[i] = 0;
-    ++at;
-    --freed;
+  constexpr int kAhead = 4;  // words of a lane on their way together
+  for (int i0 = run.lo; i0 < run.hi && mine > 0; i0 += 32 * kAhead) {
+    bool is[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) is[k] = freed(i0 + 32 * k);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + 32 * k + lane;
+      const unsigned those = __ballot_sync(~0u, is[k]);
+      if (is[k]) {
+        const int n = at + __popc(those & ((1u << lane) - 1));
+        const long long to = n < front ? free.first - front + n : (long long)free.end + n - front;
+        if (to < p.free_capacity) p.free_pages[to] = i;
+        p.shares_out[i] = 0;
+      }
+      at += __popc(those);
+      mine -= __popc(those);
+    }
   }
   if (rank == 0 && threadIdx.x == 0) {
     p.span_out[0] = free.first - front;
@@ -326,6 +371,17 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
   sm103::cluster_sync();
 }
 
+__global__ void __launch_bounds__(kThreads)
+    copy_words_kernel(const int32_t* from, int32_t* to, const int n) {
+  sm103::pdl_wait();
+  copy_words(from, to, n);
+}
+
+__global__ void __launch_bounds__(kThreads) page_release_entries_kernel(const ReleaseParams p) {
+  sm103::pdl_wait();
+  release_entries(p);
+}
+
 // ---------------------------------------------------------------------------
 // Compact
 // ---------------------------------------------------------------------------
@@ -333,22 +389,22 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
 struct CompactParams {
   const int32_t *held, *table, *shares;
   int32_t *table_out, *shares_out, *free_pages, *span_out, *move_src, *move_dst, *moves;
-  int32_t* mark;  // workspace [num_pages]: 1 for a live page, then 1 + its place among the moves
+  int32_t* mark;  // workspace [num_pages]: 1 for a live page; 1 + its place among the moves
   int batch, width, num_pages;
 };
 
-// With L live pages, the n-th live page at or beyond L goes to the n-th hole below
-// L; sources and destinations have no page in common.
-__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
-    page_compact_kernel(const CompactParams p) {
-  __shared__ Scan s_live, s_high;
-  const int rank = (int)sm103::cluster_ctarank(), g = rank * kThreads + threadIdx.x;
-  sm103::pdl_wait();
-  for (int i = g; i < p.num_pages; i += kAll) p.mark[i] = 0;
-  sm103::cluster_sync();
-  auto held = [&](int b) { return min(max(p.held[b], 0), p.width); };
+__device__ __forceinline__ int compact_held(const CompactParams& p, int b) {
+  return min(max(p.held[b], 0), p.width);
+}
+
+__device__ __forceinline__ void compact_clear(const CompactParams& p) {
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.num_pages; i += gridDim.x * kThreads)
+    p.mark[i] = 0;
+}
+
+__device__ __forceinline__ void compact_mark(const CompactParams& p) {
   for_entries(
-      p.batch, rank, [&](int b, int&, int& hi, int&) { hi = held(b); },
+      p.batch, [&](int b, int&, int& hi, int&) { hi = compact_held(p, b); },
       [&](const int (&b)[kRun], const int (&j)[kRun], const int (&)[kRun]) {
         int id[kRun];
 #pragma unroll
@@ -361,25 +417,75 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
           else bad_page();
         }
       });
-  sm103::cluster_sync();
-  const Run run(p.num_pages, rank);
-  int live = 0;
-  for (int i = run.lo; i < run.hi; ++i) live += __ldcg(p.mark + i);
+}
+
+// With L = `total` live pages.
+__device__ __forceinline__ void compact_table(const CompactParams& p, int total) {
+  for_entries(
+      p.batch,
+      [&](int b, int&, int& hi, int& h) {
+        hi = p.width;
+        h = compact_held(p, b);
+      },
+      [&](const int (&b)[kRun], const int (&j)[kRun], const int (&h)[kRun]) {
+        int id[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          id[i] = j[i] >= 0 && j[i] < h[i] ? p.table[(long long)b[i] * p.width + j[i]] : -1;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (id[i] >= total && id[i] < p.num_pages)
+            id[i] = __ldcg(p.move_dst + __ldcg(p.mark + id[i]) - 1);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (j[i] >= 0) p.table_out[(long long)b[i] * p.width + j[i]] = id[i];
+      });
+}
+
+// One cluster.  The n-th live page at or beyond L goes to the n-th hole below L;
+// sources and destinations have no page in common.  `entries`: the marks and the
+// table as well, not in launches ahead of this one and behind it.
+__global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
+    page_compact_kernel(const CompactParams p, const bool entries) {
+  __shared__ Scan s_live, s_high;
+  const int rank = (int)sm103::cluster_ctarank(), g = rank * kThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1;
+  sm103::pdl_wait();
+  if (entries) {
+    compact_clear(p);
+    sm103::cluster_sync();
+    compact_mark(p);
+    sm103::cluster_sync();
+  }
+  const Run run = warp_run(p.num_pages, rank);
+  auto live = [&](int i) { return i + lane < run.hi && __ldcg(p.mark + i + lane) != 0; };
+  int mine = 0;  // live pages of this warp
+#pragma unroll 4
+  for (int i = run.lo; i < run.hi; i += 32) mine += __popc(__ballot_sync(~0u, live(i)));
   int total;
-  const int before = cluster_scan(s_live, live, rank, total);
-  int high = 0;
-  for (int i = max(run.lo, total); i < run.hi; ++i) high += __ldcg(p.mark + i);
+  int before = cluster_scan(s_live, lane == 0 ? mine : 0, rank, total);
+  before = __shfl_sync(~0u, before, 0);
+  int high = 0;  // those at or beyond L
+#pragma unroll 4
+  for (int i = run.lo; i < run.hi; i += 32)
+    high += __popc(__ballot_sync(~0u, live(i) && i + lane >= total));
   int moves;
-  int from = cluster_scan(s_high, high, rank, moves);
-  int hole = run.lo - before;
-  for (int i = run.lo; i < run.hi; ++i) {
-    const bool is_live = __ldcg(p.mark + i) != 0;
-    if (i < total && !is_live) {
-      p.move_dst[hole++] = i;
-    } else if (i >= total && is_live) {
-      p.move_src[from] = i;
-      p.mark[i] = ++from;
+  int from = cluster_scan(s_high, lane == 0 ? high : 0, rank, moves);
+  from = __shfl_sync(~0u, from, 0);
+  for (int i = run.lo; i < run.hi; i += 32) {
+    const bool is = live(i);
+    const unsigned those = __ballot_sync(~0u, is);
+    const unsigned up = __ballot_sync(~0u, is && i + lane >= total);
+    if (!is && i + lane < min(total, run.hi)) {
+      p.move_dst[i + lane - before - __popc(those & below)] = i + lane;
+    } else if (is && i + lane >= total) {
+      const int n = from + __popc(up & below);
+      p.move_src[n] = i + lane;
+      p.mark[i + lane] = n + 1;
     }
+    before += __popc(those);
+    from += __popc(up);
   }
   sm103::cluster_sync();
   for (int i = g; i < moves; i += kAll) {
@@ -402,26 +508,21 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
     p.span_out[1] = p.num_pages - total;
     p.moves[0] = moves;
   }
-  for_entries(
-      p.batch, rank,
-      [&](int b, int&, int& hi, int& h) {
-        hi = p.width;
-        h = held(b);
-      },
-      [&](const int (&b)[kRun], const int (&j)[kRun], const int (&h)[kRun]) {
-        int id[kRun];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-          id[i] = j[i] >= 0 && j[i] < h[i] ? p.table[(long long)b[i] * p.width + j[i]] : -1;
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-          if (id[i] >= total && id[i] < p.num_pages)
-            id[i] = __ldcg(p.move_dst + __ldcg(p.mark + id[i]) - 1);
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-          if (j[i] >= 0) p.table_out[(long long)b[i] * p.width + j[i]] = id[i];
-      });
+  if (entries) compact_table(p, total);
   sm103::cluster_sync();
+}
+
+__global__ void __launch_bounds__(kThreads) page_compact_clear_kernel(const CompactParams p) {
+  sm103::pdl_wait();
+  compact_clear(p);
+}
+__global__ void __launch_bounds__(kThreads) page_compact_mark_kernel(const CompactParams p) {
+  sm103::pdl_wait();
+  compact_mark(p);
+}
+__global__ void __launch_bounds__(kThreads) page_compact_table_kernel(const CompactParams p) {
+  sm103::pdl_wait();
+  compact_table(p, p.num_pages - p.span_out[1]);
 }
 
 // ---------------------------------------------------------------------------
@@ -547,14 +648,23 @@ mla_status_t apart(const char* what, const Range* in, int ni, const Range* out, 
 
 mla_status_t sizes_ok(const char* what, int batch, int width, int page, int num_pages) {
   if (batch < 1 || batch > 65535 || width < 1 || page < 1 || num_pages < 1 ||
-      (int64_t)batch * width > INT_MAX) {
-    set_error("%s: need 1 <= batch <= 65535, max_pages_per_seq, page_size and num_pages >= 1, "
-              "batch * max_pages_per_seq < 2^31 (batch=%d max_pages=%d page_size=%d num_pages=%d)",
+      num_pages > (1 << 30) || (int64_t)batch * width > INT_MAX) {
+    set_error("%s: need 1 <= batch <= 65535, max_pages_per_seq and page_size >= 1, num_pages in "
+              "[1, 2^30], batch * max_pages_per_seq < 2^31 (batch=%d max_pages=%d page_size=%d "
+              "num_pages=%d)",
               what, batch, width, page, num_pages);
     return MLA_ERR_INVALID_ARG;
   }
   return MLA_OK;
 }
+
+// Table entries beyond which a walk over them is a launch over the whole machine: eight
+// CTAs take about 4000 entries a microsecond, a launch costs two.
+constexpr int64_t kWide = 32768;
+
+bool wide(int batch, int width) { return (int64_t)batch * width > kWide; }
+
+dim3 whole_machine() { return dim3((unsigned)device_sm_count() * 2); }
 
 mla_status_t launched(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
@@ -626,7 +736,12 @@ extern "C" mla_status_t mla_page_fork(
   p.div = PageDiv(page_size);
   const cudaStream_t s = (cudaStream_t)stream;
   KernelTimer kt("page_fork", s);
-  return launched(launch_dependent(page_fork_kernel, dim3(kCtas), dim3(kThreads), 0, s, p));
+  const bool split = wide(batch, max_pages_per_seq);
+  cudaError_t e =
+      launch_dependent(page_fork_kernel, dim3(kCtas), dim3(kThreads), 0, s, p, !split);
+  if (e == cudaSuccess && split)
+    e = launch_dependent(page_fork_entries_kernel, whole_machine(), dim3(kThreads), 0, s, p);
+  return launched(e);
 }
 
 extern "C" mla_status_t mla_page_release(
@@ -677,7 +792,16 @@ extern "C" mla_status_t mla_page_release(
   p.div = PageDiv(page_size);
   const cudaStream_t s = (cudaStream_t)stream;
   KernelTimer kt("page_release", s);
-  return launched(launch_dependent(page_release_kernel, dim3(kCtas), dim3(kThreads), 0, s, p));
+  const bool split = wide(batch, max_pages_per_seq);
+  cudaError_t e = cudaSuccess;
+  if (split && shares != shares_out)
+    e = launch_dependent(copy_words_kernel, whole_machine(), dim3(kThreads), 0, s, shares,
+                         shares_out, num_pages);
+  if (e == cudaSuccess && split)
+    e = launch_dependent(page_release_entries_kernel, whole_machine(), dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(page_release_kernel, dim3(kCtas), dim3(kThreads), 0, s, p, !split);
+  return launched(e);
 }
 
 extern "C" mla_status_t mla_page_compact_workspace_bytes(int32_t num_pages, size_t* bytes) {
@@ -749,7 +873,17 @@ extern "C" mla_status_t mla_page_compact(
   p.num_pages = num_pages;
   const cudaStream_t s = (cudaStream_t)stream;
   KernelTimer kt("page_compact", s);
-  return launched(launch_dependent(page_compact_kernel, dim3(kCtas), dim3(kThreads), 0, s, p));
+  const bool split = wide(batch, max_pages_per_seq);
+  const dim3 all = whole_machine();
+  cudaError_t e = cudaSuccess;
+  if (split) e = launch_dependent(page_compact_clear_kernel, all, dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess && split)
+    e = launch_dependent(page_compact_mark_kernel, all, dim3(kThreads), 0, s, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(page_compact_kernel, dim3(kCtas), dim3(kThreads), 0, s, p, !split);
+  if (e == cudaSuccess && split)
+    e = launch_dependent(page_compact_table_kernel, all, dim3(kThreads), 0, s, p);
+  return launched(e);
 }
 
 extern "C" mla_status_t mla_page_copy(const mla_page_view_t* views, int32_t num_views,
