@@ -504,7 +504,6 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         ++o_uses;
         tc_fence_after();
       }
-      const bool fix = n > 0 && dirty[seg & 7] == seg;
       float f0 = 1.f, f1 = 0.f;
       int c0 = 0, c1 = DP;
       if (split) {
@@ -528,6 +527,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         c1 = c0 + DP / 2;
       }
       const bool second = split && n > 1;  // stream 1 has an accumulator
+      // (both streams' products are done: the other's tiles may have been the odd ones)
+      const bool fix = n > 0 && dirty[seg & 7] == seg;
       const float vs = HALF && p.v_scale ? p.v_scale[kvh] : 1.f;
       const float inv = l == 0.f ? 0.f : vs / l;
       const bool live = r < rows, none = __any_sync(~0u, l == 0.f);
