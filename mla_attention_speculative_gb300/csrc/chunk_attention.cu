@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
   long long total = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    long long upto = sequence_cost(p, b) * p.kv_heads;
+    Sequence own;
+    long long upto = sequence_cost(p, b, own) * p.kv_heads;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, upto, o);
@@ -72,8 +73,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
   if (tid == 0) p.base[0] = s_base[0] = 0;
   __syncthreads();
   auto base = [&](int b) { return p.batch <= kKeep ? s_base[b] : p.base[b]; };
+  auto sequence = [&](int b) {
+    Sequence s;
+    s.load(p, b);
+    return s;
+  };
   for (int c = warp; c <= p.ctas; c += kPlanThreads / 32) {
-    const Place e = find_place(p, c, total, base);
+    const Place e = find_place(p, c, total, base, sequence);
     if (lane == 0) {
       s_start[c] = e.st;
       p.starts[c] = e.st;
@@ -81,7 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
   }
   __syncthreads();
   for (int c = warp; c < p.ctas; c += kPlanThreads / 32) {
-    const Place e = find_place(p, c + 1, total, base);
+    const Place e = find_place(p, c + 1, total, base, sequence);
     if (lane == 0) p.rec[c] = make_record(p, c, total, s_start[c], e);
   }
 }

@@ -119,10 +119,13 @@ struct Walk {
   Sequence seq;
   bool loaded;
 
-  __device__ __forceinline__ void begin(const Start& from, const Start& to) {
+  // `first`: the sequence that `from` names
+  __device__ __forceinline__ void begin(const Start& from, const Start& to,
+                                        const Sequence& first) {
     at = from;
     end = to;
-    loaded = false;
+    seq = first;
+    loaded = true;
   }
   __device__ __forceinline__ bool in_last() const {
     return at.b == end.b && at.kvh == end.kvh && at.q == end.q;
@@ -197,10 +200,10 @@ __device__ __forceinline__ int unit_cost(const Params& p, const Sequence& s, int
 
 // The cost of one sequence and key/value head, b < batch or none; a warp together
 // where a lane's sequence has many units.
-__device__ __forceinline__ long long sequence_cost(const Params& p, int b) {
+__device__ __forceinline__ long long sequence_cost(const Params& p, int b, Sequence& s) {
   constexpr int kAlone = 4;  // units a thread adds up by itself
   const int lane = threadIdx.x & 31;
-  Sequence s = {0, 0, 0, 0, 0};
+  s = {0, 0, 0, 0, 0};
   if (b < p.batch) s.load(p, b);
   long long cost = 0;
   if (s.tiles <= kAlone)
@@ -239,9 +242,10 @@ struct Place {
   __device__ __forceinline__ bool inside() const { return st.tile > 0; }
 };
 
-// The place of share c, by a warp; base(b): the cost before sequence b.
-template <typename Base>
-__device__ __forceinline__ Place find_place(const Params& p, int c, long long total, Base base) {
+// The place of share c, by a warp; base(b): the cost before sequence b, sequence(b).
+template <typename Base, typename Seq>
+__device__ __forceinline__ Place find_place(const Params& p, int c, long long total, Base base,
+                                            Seq sequence) {
   const int lane = threadIdx.x & 31;
   const long long x = (long long)c * share_size(p, total);
   Place r;
@@ -255,7 +259,7 @@ __device__ __forceinline__ Place find_place(const Params& p, int c, long long to
     const int mid = (lo + hi) >> 1;
     if (base(mid + 1) > x) hi = mid; else lo = mid + 1;
   }
-  r.seq.load(p, lo);
+  r.seq = sequence(lo);
   const long long from = base(lo), all = base(lo + 1) - from;
   // (32-bit divisions where the numbers allow, and they mostly do)
   long long one, rest = x - from;
@@ -341,16 +345,22 @@ __device__ __forceinline__ Record make_record(const Params& p, int c, long long 
 // call returns.
 constexpr int kInside = 256;
 struct PlanScratch {
+  Sequence seq[kInside];
   long long cost[kInside], base[kInside + 1];
   long long warp[kInside / 32];
   Start start[2];
 };
 __device__ __forceinline__ void find_share(const Params& p, int cta, PlanScratch& t, Start& from,
-                                           Start& to) {
+                                           Start& to, Sequence& first) {
   constexpr int kWarps = kInside / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // neighbouring sequences in different warps, so that long ones are added up side by side
-  if (warp < kWarps) t.cost[lane * kWarps + warp] = sequence_cost(p, lane * kWarps + warp) * p.kv_heads;
+  if (warp < kWarps) {
+    const int b = lane * kWarps + warp;
+    Sequence s;
+    t.cost[b] = sequence_cost(p, b, s) * p.kv_heads;
+    t.seq[b] = s;
+  }
   __syncthreads();
   long long upto = 0;
   if (warp < kWarps) {
@@ -376,12 +386,13 @@ __device__ __forceinline__ void find_share(const Params& p, int cta, PlanScratch
   auto base = [&](int b) { return t.base[b]; };
   Place e;
   if (warp < 2) {
-    e = find_place(p, cta + warp, total, base);
+    e = find_place(p, cta + warp, total, base, [&](int b) { return t.seq[b]; });
     if (lane == 0) t.start[warp] = e.st;
   }
   __syncthreads();
   from = t.start[0];
   to = t.start[1];
+  if (from.b < p.batch) first = t.seq[from.b];
   if (warp == 1 && lane == 0) p.rec[cta] = make_record(p, cta, total, from, e);
   __syncthreads();
 }

@@ -57,17 +57,19 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
   const int cta = blockIdx.x;
   sm103::pdl_wait();
   Start from, to;
+  Sequence seq = {0, 0, 0, 0, 0};
   if (p.starts == nullptr) {
-    find_share(p, cta, *reinterpret_cast<PlanScratch*>(s_raw), from, to);
+    find_share(p, cta, *reinterpret_cast<PlanScratch*>(s_raw), from, to, seq);
   } else {
     from = p.starts[cta];
     to = p.starts[cta + 1];
+    if (from.b >= 0 && from.b < p.batch) seq.load(p, from.b);
   }
   // columns past the heads' width stay zero
   for (int i = tid; i < 3 * 64 * LD; i += kThreads) sQ[i] = 0.f;
   __syncthreads();
   Walk w;
-  w.begin(from, to);
+  w.begin(from, to, seq);
   Segment g;
   for (; w.next(p, g); w.advance(p, g)) {
     const Sequence& s = w.seq;

@@ -229,16 +229,18 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
   const uint32_t tmem = *slot_word;
   pdl_wait();
   Start from, to;
+  Sequence seq = {0, 0, 0, 0, 0};
   if (p.starts == nullptr) {
     // (the place of the queries, which come later)
-    find_share(p, cta, *reinterpret_cast<PlanScratch*>(smem), from, to);
+    find_share(p, cta, *reinterpret_cast<PlanScratch*>(smem), from, to, seq);
   } else {
     from = p.starts[cta];
     to = p.starts[cta + 1];
+    if (from.b >= 0 && from.b < p.batch) seq.load(p, from.b);
   }
   Walk w;
   Segment g;
-  w.begin(from, to);
+  w.begin(from, to, seq);
   bool ok = true;
 
   if (warp >= 4 * NS) {
@@ -389,11 +391,13 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           }
         };
         auto hide = [&](uint32_t* u, int k) {
+          // bit j: this row sees column j of the piece
+          const int a = first - (pos0 + 32 * k), z = last - (pos0 + 32 * k);
+          uint32_t sees = z < 0 || a > 31 ? 0u : z >= 31 ? ~0u : (2u << z) - 1u;
+          if (a > 0) sees &= ~0u << (a & 31);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int pos = pos0 + 32 * k + j;
-            if (pos < first || pos > last) u[j] = 0xFF800000u;
-          }
+          for (int j = 0; j < 32; ++j)
+            if (!(sees >> j & 1u)) u[j] = 0xFF800000u;
         };
         auto highest = [&](const uint32_t* u) {
 #pragma unroll
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
                                      fmaxf(__uint_as_float(u[j]), __uint_as_float(u[j + 1])));
         };
         if (edge) {
-          // (few tiles: a loop, so that the code of the others stays together)
+          // (few tiles: a loop of its own, so that the code of the others stays together)
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             tmem_ld32(tS + 32 * k, u0);
@@ -484,7 +488,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           for (int k = 0; k < 4; ++k) {
             tmem_wait_ld<32>(u0);
             hide(u0, k);
-            weights(u0, k, std::true_type());
+            if (large) weights(u0, k, std::true_type());
+            else weights(u0, k, std::false_type());
             if (k < 3) tmem_ld32(tS + 32 * (k + 1), u0);
           }
         } else {
@@ -996,8 +1001,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         blk = 0;
         value = false;
       }
-      __device__ __forceinline__ void begin(const Params& p, const Start& from, const Start& to) {
-        w.begin(from, to);
+      __device__ __forceinline__ void begin(const Params& p, const Walk& whole) {
+        w = whole;
         pos = 0;
         seg = 0;
         settle(p);
@@ -1031,7 +1036,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     };
     Blocks z;
     if constexpr (FEED == kRows) {
-      for (z.begin(p, from, to); z.more && ok; z.step(p)) {
+      for (z.begin(p, w); z.more && ok; z.step(p)) {
         const uint32_t sl = z.pos % NB;
         if (z.pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (z.pos / NB - 1) & 1, 121);
         ok = __all_sync(~0u, ok);
@@ -1062,7 +1067,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       }
       cp_async_wait_all();
     } else if constexpr (FEED == kConvert) {
-      for (z.begin(p, from, to); z.more && ok; z.step(p)) {
+      for (z.begin(p, w); z.more && ok; z.step(p)) {
         const uint32_t sl = z.pos % NB, rs = z.pos % C::RS;
         wait_or_fail(ok, bar(C::RFULL + rs), (z.pos / C::RS) & 1, 123);
         if (z.pos >= NB) wait_or_fail(ok, bar(C::EMPTY + sl), (z.pos / NB - 1) & 1, 122);
