@@ -420,6 +420,7 @@ extern "C" mla_status_t mla_chunk_attention(
   p.bm = d.k.bm;
   p.bn = d.k.bn;
   p.ctas = d.ctas;
+  p.unit_cost = d.k.unit_cost;
   p.page_div = PageDiv(cache->page_size);
   p.group_div = PageDiv(p.group);
   const double scale = g->softmax_scale > 0.f ? (double)g->softmax_scale

@@ -4,7 +4,7 @@
 // The queries of one sequence and key/value head are taken as rows: row r is
 // token r / group, head r % group of its group, so that few tokens and many
 // heads fill a tile as well as many tokens and few heads.  A unit is a tile of
-// `bm` such rows; it costs kUnitCost plus one per tile of `bn` cached positions
+// `bm` such rows; it costs `unit_cost` plus one per tile of `bn` cached positions
 // that any of its rows sees.  All units, in order of sequence, key/value head
 // and tile, laid end to end are cut into equal shares, one per CTA, so a unit
 // may fall into several shares: each leaves a part, and the join adds them up.
@@ -20,13 +20,17 @@ namespace mla {
 namespace chunk {
 
 constexpr int kMaxCtas = 512;
-// What a unit costs besides its tiles: its queries, its last wait and its outputs.
-constexpr int kUnitCost = 3;
+// What a unit costs besides its tiles, in tiles: its queries, its first and last
+// waits, its edge tiles and its outputs (us at 3 / 6 / 8 / 11 / 14 on tensor cores:
+// a prompt of 8192 rows 456 / 400 / 406 / 416 / 429, prompts and steps over an e4m3
+// cache 822 / 790 / 770 / 766 / 776, 16 steps of 4 rows 40.2 / 40.1 / 39.6 / 39.5 /
+// 41.9; a window of fp32 on CUDA cores 86.6 at 3, 89.8 at 4, 130 at 6).
+constexpr int kCoresCost = 3, kTensorCost = 8;
 // A share does not begin in the first or last kSnap tiles of a unit: a part of one
 // or two tiles costs more to join than to do.
 constexpr int kSnap = 2;
 // The least a share holds.
-constexpr int kMinShare = kUnitCost + 1;
+constexpr int kMinShare = 4;
 
 // Where a share begins: a unit and a tile within it (b == batch: behind the last).
 struct Start {
@@ -58,7 +62,7 @@ struct Params {
   float* part_o;     // [2 * ctas][bm][dp] unnormalised
   int heads, kv_heads, group, dim, dp, batch, rows, page, width, num_pages, window;
   int capacity;      // rows of a table's pages
-  int bm, bn, ctas;
+  int bm, bn, ctas, unit_cost;
   PageDiv page_div, group_div;
   float scale_log2;  // softmax scale * log2(e)
 };
@@ -195,7 +199,7 @@ struct Walk {
 __device__ __forceinline__ int unit_cost(const Params& p, const Sequence& s, int q) {
   Unit u;
   u.set(p, s, q);
-  return kUnitCost + u.tiles;
+  return p.unit_cost + u.tiles;
 }
 
 // The cost of one sequence and key/value head, b < batch or none; a warp together
@@ -287,7 +291,7 @@ __device__ __forceinline__ Place find_place(const Params& p, int c, long long to
     if (behind) {
       const int at = __ffs(behind) - 1;
       r.q = q0 + at;
-      r.tiles = __shfl_sync(~0u, mine, at) - kUnitCost;
+      r.tiles = __shfl_sync(~0u, mine, at) - p.unit_cost;
       rest -= __shfl_sync(~0u, upto - mine, at);
       break;
     }
@@ -295,7 +299,7 @@ __device__ __forceinline__ Place find_place(const Params& p, int c, long long to
   }
   r.x0 = x - rest;
   r.st.q = r.q;
-  r.st.tile = (int)rest - kUnitCost;
+  r.st.tile = (int)rest - p.unit_cost;
   if (r.st.tile <= kSnap) {
     r.st.tile = 0;
   } else if (r.st.tile >= r.tiles - kSnap) {
@@ -329,7 +333,7 @@ __device__ __forceinline__ Record make_record(const Params& p, int c, long long 
   // the places behind e, a share apart, that lie within the unit as well
   const long long size = share_size(p, total);
   const long long x = (long long)(c + 1) * size;
-  const long long last = e.x0 + kUnitCost + e.tiles - kSnap - 1;
+  const long long last = e.x0 + p.unit_cost + e.tiles - kSnap - 1;
   Unit u;
   u.set(p, e.seq, e.q);
   r.parts = 2 + (int)((last - x) / size);
@@ -405,7 +409,7 @@ enum Kind { kBf16 = 0, kE4m3 = 1, kFp32 = 2 };
 constexpr float kShift = 7.f;
 
 struct Kernel {
-  int bm, bn, dp, threads, smem, occupancy;
+  int bm, bn, dp, occupancy, unit_cost;
   cudaError_t (*launch)(const Params& p, int ctas, cudaStream_t stream);
 };
 // CUDA cores (fp32); tensor cores with a bf16 cache in pages of whole runs of 8

@@ -283,7 +283,7 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
 
 template <int DP>
 Kernel make() {
-  return {kBM, kBN, DP, kThreads, Layout<DP>::SMEM, Layout<DP>::OCC, launch<DP>};
+  return {kBM, kBN, DP, Layout<DP>::OCC, kCoresCost, launch<DP>};
 }
 
 }  // namespace

@@ -1183,7 +1183,7 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
 template <int FEED, int DP>
 Kernel make() {
   using C = Shape<DP, FEED>;
-  return {C::BM, kBN, DP, C::THREADS, C::SMEM, 1, launch<DP, FEED>};
+  return {C::BM, kBN, DP, 1, kTensorCost, launch<DP, FEED>};
 }
 
 template <int FEED>
