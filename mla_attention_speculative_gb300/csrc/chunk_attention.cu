@@ -260,7 +260,7 @@ Plan make_plan(const mla_kv_geometry_t* g, int batch, int rows, int page_size, i
   if (ctas > most) ctas = most;
   if (ctas < 1) ctas = 1;
   d.ctas = (int)ctas;
-  d.cut = tiles > 2 * kSnap + 1;
+  d.cut = tiles > 2 * d.k.snap + 1;
   size_t off = align256(sizeof(Start) * (ctas + 1));
   d.off_rec = off;
   off = align256(off + sizeof(Record) * ctas);
@@ -421,6 +421,7 @@ extern "C" mla_status_t mla_chunk_attention(
   p.bn = d.k.bn;
   p.ctas = d.ctas;
   p.unit_cost = d.k.unit_cost;
+  p.snap = d.k.snap;
   p.page_div = PageDiv(cache->page_size);
   p.group_div = PageDiv(p.group);
   const double scale = g->softmax_scale > 0.f ? (double)g->softmax_scale

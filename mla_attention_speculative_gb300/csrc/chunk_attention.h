@@ -24,11 +24,13 @@ constexpr int kMaxCtas = 512;
 // waits, its edge tiles and its outputs (us at 3 / 6 / 8 / 11 / 14 on tensor cores:
 // a prompt of 8192 rows 456 / 400 / 406 / 416 / 429, prompts and steps over an e4m3
 // cache 822 / 790 / 770 / 766 / 776, 16 steps of 4 rows 40.2 / 40.1 / 39.6 / 39.5 /
-// 41.9; a window of fp32 on CUDA cores 86.6 at 3, 89.8 at 4, 130 at 6).
-constexpr int kCoresCost = 3, kTensorCost = 8;
-// A share does not begin in the first or last kSnap tiles of a unit: a part of one
-// or two tiles costs more to join than to do.
-constexpr int kSnap = 2;
+// 41.9; a window of fp32 on CUDA cores 64.1 at 1, 64.6 at 2, 64.2 at 3).
+constexpr int kCoresCost = 2, kTensorCost = 8;
+// A share does not begin in the first or last `snap` tiles of a unit: on tensor cores
+// a tile takes less than the join of a part (16 steps of 4 rows, us at 0 / 1 / 2 / 3:
+// 38.3 / 37.7 / 39.4 / 41.6; the others the same), on CUDA cores several times as
+// long (the window of fp32, at 0 / 1 / 2: 64 / 75 / 87).
+constexpr int kCoresSnap = 0, kTensorSnap = 1;
 // The least a share holds.
 constexpr int kMinShare = 4;
 
@@ -62,7 +64,7 @@ struct Params {
   float* part_o;     // [2 * ctas][bm][dp] unnormalised
   int heads, kv_heads, group, dim, dp, batch, rows, page, width, num_pages, window;
   int capacity;      // rows of a table's pages
-  int bm, bn, ctas, unit_cost;
+  int bm, bn, ctas, unit_cost, snap;
   PageDiv page_div, group_div;
   float scale_log2;  // softmax scale * log2(e)
 };
@@ -300,9 +302,9 @@ __device__ __forceinline__ Place find_place(const Params& p, int c, long long to
   r.x0 = x - rest;
   r.st.q = r.q;
   r.st.tile = (int)rest - p.unit_cost;
-  if (r.st.tile <= kSnap) {
+  if (r.st.tile <= p.snap) {
     r.st.tile = 0;
-  } else if (r.st.tile >= r.tiles - kSnap) {
+  } else if (r.st.tile >= r.tiles - p.snap) {
     // the next unit's beginning
     r.st.tile = 0;
     if (++r.st.q == r.seq.tiles) {
@@ -333,7 +335,7 @@ __device__ __forceinline__ Record make_record(const Params& p, int c, long long 
   // the places behind e, a share apart, that lie within the unit as well
   const long long size = share_size(p, total);
   const long long x = (long long)(c + 1) * size;
-  const long long last = e.x0 + p.unit_cost + e.tiles - kSnap - 1;
+  const long long last = e.x0 + p.unit_cost + e.tiles - p.snap - 1;
   Unit u;
   u.set(p, e.seq, e.q);
   r.parts = 2 + (int)((last - x) / size);
@@ -409,7 +411,7 @@ enum Kind { kBf16 = 0, kE4m3 = 1, kFp32 = 2 };
 constexpr float kShift = 7.f;
 
 struct Kernel {
-  int bm, bn, dp, occupancy, unit_cost;
+  int bm, bn, dp, occupancy, unit_cost, snap;
   cudaError_t (*launch)(const Params& p, int ctas, cudaStream_t stream);
 };
 // CUDA cores (fp32); tensor cores with a bf16 cache in pages of whole runs of 8

@@ -6,6 +6,12 @@
 // thread, a running maximum and sum per row in registers, P through shared
 // memory, and O += P V with 4 rows of DP / 16 columns to a thread.  Everything
 // is held and summed in fp32.
+//
+// What bounds it is the multiply-adds: a tile of heads of 80 (held as 96) is
+// 64 * 64 * 176 of them, 5632 cycles of an SM.  8 sequences of 1 to 129 rows, a window
+// of 1000 over up to 4129 positions, 20 heads on 4 of 80: 64 us, with 9 to 10 tiles to
+// a CTA.  (Two CTAs on an SM hide each other's loads: asynchronous copies of the next
+// tile 68 us, multiply-adds of pairs 72 and 75 us with both.)
 
 #include <mutex>
 #include <type_traits>
@@ -283,7 +289,7 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
 
 template <int DP>
 Kernel make() {
-  return {kBM, kBN, DP, Layout<DP>::OCC, kCoresCost, launch<DP>};
+  return {kBM, kBN, DP, Layout<DP>::OCC, kCoresCost, kCoresSnap, launch<DP>};
 }
 
 }  // namespace

@@ -78,7 +78,7 @@ struct Shape {
   static constexpr int MMA = 4 * NS, TMA = MMA + 1, CLEAN = MMA + 2, FEEDER = MMA + 4;
   static constexpr int FEEDERS = FEED == kTma ? 0 : 128;
   static constexpr int THREADS = FEEDER * 32 + FEEDERS;
-  // 16 warps start with 128 registers a thread: 168 for the softmax, 88 for the others
+  // 16 warps start with 128 registers a thread: 152 for the softmax, 104 for the others
   static constexpr bool SHARES = THREADS == 512;
   static constexpr uint32_t TM_S = NS * DP;           // tensor memory: O, then two of S
   static constexpr int TAIL = 1024 + (FEED == kConvert ? NS * 128 * 4 : 0);
@@ -88,8 +88,8 @@ struct Shape {
   // barriers
   static constexpr int FULL = 0, EMPTY = NB, LANDED = 2 * NB, RFULL = 3 * NB, REMPTY = RFULL + RS,
                        QFULL = REMPTY + RS, SFULL = QFULL + 1, PHALF = SFULL + 2,
-                       PFULL = PHALF + 2,                       OFULL = PFULL + 2, PVDONE = OFULL + 2, DRAIN = PVDONE + 2,
-                       BARS = DRAIN + 1;
+                       PFULL = PHALF + 2, OFULL = PFULL + 2, PVDONE = OFULL + 2,
+                       DRAIN = PVDONE + 2, BARS = DRAIN + 1;
   static_assert(BARS * 8 + 10 * 4 + 4 * NS * sizeof(Walk) <= 1024, "the barriers do not fit");
 };
 
@@ -1183,7 +1183,7 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
 template <int FEED, int DP>
 Kernel make() {
   using C = Shape<DP, FEED>;
-  return {C::BM, kBN, DP, 1, kTensorCost, launch<DP, FEED>};
+  return {C::BM, kBN, DP, 1, kTensorCost, kTensorSnap, launch<DP, FEED>};
 }
 
 template <int FEED>
