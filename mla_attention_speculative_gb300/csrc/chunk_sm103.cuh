@@ -73,8 +73,8 @@ struct Shape {
       FEED == kConvert ? (DP == 64 ? 6 : 4) : (DP == 64 ? 10 : 5);
   static constexpr int RS = FEED == kConvert ? 2 : 0;
   static_assert(NB >= (NBLK == 1 ? 3 : 2 * NBLK), "the ring is too short");
-  // warps: softmax, then the MMA issuer, the TMA boxes, V where rows are hidden (one is
-  // left over), and four that copy or convert
+  // warps: softmax, then the MMA issuer, the TMA boxes, two for V where rows are hidden, and
+  // four that copy or convert
   static constexpr int MMA = 4 * NS, TMA = MMA + 1, CLEAN = MMA + 2, FEEDER = MMA + 4;
   static constexpr int FEEDERS = FEED == kTma ? 0 : 128;
   static constexpr int THREADS = FEEDER * 32 + FEEDERS;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NB; ++i) {
-      mbar_init(bar(C::FULL + i), FEED == kTma ? 1 : C::FEEDERS);
+      mbar_init(bar(C::FULL + i), FEED == kTma ? 2 : C::FEEDERS);
       mbar_init(bar(C::EMPTY + i), 1);
       mbar_init(bar(C::LANDED + i), FEED == kTma ? 1 : C::FEEDERS);
     }
@@ -390,14 +390,17 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
             f(u1, k + 1);
           }
         };
-        auto hide = [&](uint32_t* u, int k) {
-          // bit j: this row sees column j of the piece
+        // bit j: this row sees column j of piece k
+        auto sees = [&](int k) {
           const int a = first - (pos0 + 32 * k), z = last - (pos0 + 32 * k);
-          uint32_t sees = z < 0 || a > 31 ? 0u : z >= 31 ? ~0u : (2u << z) - 1u;
-          if (a > 0) sees &= ~0u << (a & 31);
+          uint32_t bits = z < 0 || a > 31 ? 0u : z >= 31 ? ~0u : (2u << z) - 1u;
+          if (a > 0) bits &= ~0u << (a & 31);
+          return bits;
+        };
+        auto hide = [&](uint32_t* u, uint32_t bits) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!(sees >> j & 1u)) u[j] = 0xFF800000u;
+            if (!(bits >> j & 1u)) u[j] = 0xFF800000u;
         };
         auto highest = [&](const uint32_t* u) {
 #pragma unroll
@@ -409,9 +412,11 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           // (few tiles: a loop of its own, so that the code of the others stays together)
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
+            const uint32_t bits = sees(k);
+            if (!__any_sync(~0u, bits != 0u)) continue;
             tmem_ld32(tS + 32 * k, u0);
             tmem_wait_ld<32>(u0);
-            hide(u0, k);
+            if (!__all_sync(~0u, bits == ~0u)) hide(u0, bits);
             highest(u0);
           }
         } else {
@@ -455,6 +460,14 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
         const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(shift - base, shift - base);
         const float ref = m == -INFINITY ? 0.f : top;
         uint64_t sum2[2] = {0ull, 0ull};
+        auto store = [&](const uint32_t (&pk)[16], int k) {
+          tmem_st16(tS + 16 * k, pk);
+          if (k & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar((k == 1 ? C::PHALF : C::PFULL) + x));
+          }
+        };
         auto weights = [&](uint32_t* u, int k, auto careful) {
           // (step by step for 32 scores, so that no exponential waits for another)
           float y[32];
@@ -476,20 +489,23 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
             sum2[e & 1] = add2(sum2[e & 1], pack2(y[2 * e], y[2 * e + 1]));
             pk[e] = HALF ? pack_half(y[2 * e], y[2 * e + 1]) : pack_bf16(y[2 * e], y[2 * e + 1]);
           }
-          tmem_st16(tS + 16 * k, pk);
-          if (k & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar((k == 1 ? C::PHALF : C::PFULL) + x));
-          }
+          store(pk, k);
         };
         if (edge || large) {
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
+            const uint32_t bits = sees(k);
             tmem_wait_ld<32>(u0);
-            hide(u0, k);
-            if (large) weights(u0, k, std::true_type());
-            else weights(u0, k, std::false_type());
+            if (!__any_sync(~0u, bits != 0u)) {
+              uint32_t none[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) none[e] = 0u;
+              store(none, k);
+            } else {
+              if (!__all_sync(~0u, bits == ~0u)) hide(u0, bits);
+              if (large) weights(u0, k, std::true_type());
+              else weights(u0, k, std::false_type());
+            }
             if (k < 3) tmem_ld32(tS + 32 * (k + 1), u0);
           }
         } else {
@@ -869,15 +885,20 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           if (one_each) {
             const bool mine = have && ch < chunks;
             const unsigned all = __ballot_sync(~0u, mine);
-            if (lane == 0)
+            if (lane == 0) {
               mbar_arrive_expect_tx(bar(full + sl), (uint32_t)__popc(all) * maps.box * 128);
+              if (FEED == kTma && full == C::FULL) mbar_arrive(bar(full + sl));
+            }
             __syncwarp();
             if (mine) box_load(map, sl, full, blk, rb, ch, row, id);
           } else {
             int boxes = 0;
             for (int k = lane; k < nbox; k += 32) boxes += visible(i, k) ? 1 : 0;
             boxes = __reduce_add_sync(~0u, boxes);
-            if (lane == 0) mbar_arrive_expect_tx(bar(full + sl), (uint32_t)boxes * maps.box * 128);
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar(full + sl), (uint32_t)boxes * maps.box * 128);
+              if (FEED == kTma && full == C::FULL) mbar_arrive(bar(full + sl));
+            }
             __syncwarp();
             for (int k = lane; k < nbox; k += 32) {
               int id1, row1;
@@ -915,9 +936,11 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     // nothing may still be landing when the CTA exits
     for (uint32_t pos = issued > SLOTS ? issued - SLOTS : 0; pos < issued; ++pos)
       mbar_wait(bar(TO_FULL + pos % SLOTS), (pos / SLOTS) & 1);
-  } else if (FEED != kConvert && warp == C::CLEAN) {
+  } else if (FEED != kConvert && (warp == C::CLEAN || warp == C::CLEAN + 1)) {
     // -------------------------------------------------- V where rows are hidden
-    // (its blocks arrive on a barrier of their own, the ring's is for the MMA)
+    // (its blocks arrive on a barrier of their own, the ring's is for the MMA; two warps, half
+    // of the rows each)
+    const int row0 = (warp - C::CLEAN) * 64 + (lane >> 3);
     uint32_t at = 0, uses = 0;
     int seg = 0;
     for (; w.next(p, g); w.advance(p, g)) {
@@ -936,35 +959,34 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           if (!ok) break;
           const int chunks = (DP - 128 * blk < 128 ? DP - 128 * blk : C::BW) / 64;
           bool met = false;
-          // (a 16-byte column of 64-column part c, rows lane / 8 + 4 k: whole lines per warp)
-          for (int c = 0; c < chunks; ++c) {
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-              const int row = 4 * k + (lane >> 3);
-              const uint32_t a = sRing + sl * C::SLOT + c * 16384 + row * 128 + (lane & 7) * 16;
-              if (pos0 + row < u.lo || pos0 + row >= u.hi) {
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u)
-                             : "memory");
-                continue;
-              }
-              uint32_t x[4];
+          // (16-byte columns of whole 64-column lines, four rows of them to a warp's read)
+          constexpr int AT_ONCE = 8;
+#pragma unroll 1
+          for (int k0 = 0; k0 < 16 * chunks; k0 += AT_ONCE) {
+            const uint32_t a = sRing + sl * C::SLOT + (k0 >> 4) * 16384 + (lane & 7) * 16;
+            uint32_t x[AT_ONCE][4];
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k)
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                           : "r"(a)
+                           : "=r"(x[k][0]), "=r"(x[k][1]), "=r"(x[k][2]), "=r"(x[k][3])
+                           : "r"(a + (row0 + 4 * ((k0 & 15) + k)) * 128)
                            : "memory");
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) {
+              const int row = row0 + 4 * ((k0 & 15) + k);
+              const bool nobody = pos0 + row < u.lo || pos0 + row >= u.hi;
               uint32_t bad = 0;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t mask = __vcmpeq2(x[e] & 0x7F807F80u, 0x7F807F80u);
+                const uint32_t mask = __vcmpeq2(x[k][e] & 0x7F807F80u, 0x7F807F80u);
                 bad |= mask;
-                x[e] &= ~mask;
+                x[k][e] = nobody ? 0u : x[k][e] & ~mask;
               }
-              if (bad) {
-                met = true;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x[0]),
-                             "r"(x[1]), "r"(x[2]), "r"(x[3])
+              met |= bad != 0 && !nobody;
+              if (bad != 0 || nobody)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a + row * 128),
+                             "r"(x[k][0]), "r"(x[k][1]), "r"(x[k][2]), "r"(x[k][3])
                              : "memory");
-              }
             }
           }
           if (met) dirty[seg & 7] = seg;
@@ -973,7 +995,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           if constexpr (FEED == kTma) {
             if (lane == 0) mbar_arrive(bar(C::FULL + sl));
           } else {
-            for (int k = 0; k < C::FEEDERS / 32; ++k) mbar_arrive(bar(C::FULL + sl));
+            for (int k = 0; k < C::FEEDERS / 64; ++k) mbar_arrive(bar(C::FULL + sl));
           }
         }
       }
