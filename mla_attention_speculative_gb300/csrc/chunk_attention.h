@@ -22,14 +22,15 @@ namespace chunk {
 constexpr int kMaxCtas = 512;
 // What a unit costs besides its tiles, in tiles: its queries, its first and last
 // waits, its edge tiles and its outputs (us at 3 / 6 / 8 / 11 / 14 on tensor cores:
-// a prompt of 8192 rows 456 / 400 / 406 / 416 / 429, prompts and steps over an e4m3
-// cache 822 / 790 / 770 / 766 / 776, 16 steps of 4 rows 40.2 / 40.1 / 39.6 / 39.5 /
-// 41.9; a window of fp32 on CUDA cores 64.1 at 1, 64.6 at 2, 64.2 at 3).
+// a prompt of 8192 rows 415 / 395 / 400 / 409 / 421, prompts and steps over an e4m3
+// cache 817 / 756 / 745 / 742 / 754, 16 steps of 1 to 8 rows 39.1 / 35.3 / 35.4 / 36.8 /
+// 39.1; a window of fp32 on CUDA cores 64.1 at 1, 64.2 at 2, 64.2 at 3, 75.2 at 4).
 constexpr int kCoresCost = 2, kTensorCost = 8;
 // A share does not begin in the first or last `snap` tiles of a unit: on tensor cores
-// a tile takes less than the join of a part (16 steps of 4 rows, us at 0 / 1 / 2 / 3:
-// 38.3 / 37.7 / 39.4 / 41.6; the others the same), on CUDA cores several times as
-// long (the window of fp32, at 0 / 1 / 2: 64 / 75 / 87).
+// a tile takes less than the join of a part (16 steps of 1 to 8 rows, us at 0 / 1 / 2 / 3:
+// 35.4 / 35.4 / 37.1 / 38.8; the others the same, with fewer parts to join the larger
+// it is), on CUDA cores several times as long (the window of fp32, at 0 / 1 / 2: 64 /
+// 71 / 87).
 constexpr int kCoresSnap = 0, kTensorSnap = 1;
 // The least a share holds.
 constexpr int kMinShare = 4;
