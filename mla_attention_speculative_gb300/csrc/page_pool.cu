@@ -12,6 +12,11 @@
 // Whatever is placed in order (pages of the free list, moves) is placed by
 // exclusive sums over consecutive runs, so results never depend on the order in
 // which threads arrive.
+//
+// Each lets the next launch of the stream take its place early, which waits for all
+// of it before it reads: a launch's time less (us in a graph: 32 forks 11.7 -> 11.4,
+// 32 sequences cut back 8.5 -> 8.2, 256 pages compacted 15.7 -> 15.1).  The copies
+// do not, they fill the machine.
 
 #include <cuda_runtime.h>
 
@@ -223,6 +228,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
   __shared__ Scan s_scan;
   const int rank = (int)sm103::cluster_ctarank();
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   copy_words(p.shares, p.shares_out, p.num_pages);
   const Run run = thread_run(p.batch, rank);
   int wants = 0;
@@ -274,6 +280,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(kThreads) page_fork_entries_kernel(const ForkParams p) {
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   fork_entries(p);
 }
 
@@ -325,6 +332,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
   __shared__ Scan s_scan;
   const int rank = (int)sm103::cluster_ctarank(), lane = threadIdx.x & 31;
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   const FreeSpan free(p.free_span, p.free_capacity);
   if (entries) {
     if (p.shares != p.shares_out) {
@@ -374,11 +382,13 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     copy_words_kernel(const int32_t* from, int32_t* to, const int n) {
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   copy_words(from, to, n);
 }
 
 __global__ void __launch_bounds__(kThreads) page_release_entries_kernel(const ReleaseParams p) {
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   release_entries(p);
 }
 
@@ -452,6 +462,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31;
   const unsigned below = (1u << lane) - 1;
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   if (entries) {
     compact_clear(p);
     sm103::cluster_sync();
@@ -514,14 +525,17 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(kThreads) page_compact_clear_kernel(const CompactParams p) {
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   compact_clear(p);
 }
 __global__ void __launch_bounds__(kThreads) page_compact_mark_kernel(const CompactParams p) {
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   compact_mark(p);
 }
 __global__ void __launch_bounds__(kThreads) page_compact_table_kernel(const CompactParams p) {
   sm103::pdl_wait();
+  sm103::pdl_launch_dependents();
   compact_table(p, p.num_pages - p.span_out[1]);
 }
 
