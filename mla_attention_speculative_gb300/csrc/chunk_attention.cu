@@ -96,7 +96,12 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Params p
 // Join
 // ---------------------------------------------------------------------------
 
-constexpr int kJoinThreads = 256, kJoinY = 32, kJoinLoads = 8;
+// Rows of a unit are spread over kJoinY CTAs, most of which have none in short steps
+// (us at 32 / 16 / 12: 16 steps 35.4 / 33.8 / 33.4, a prompt of 8192 rows 396 / 392 /
+// 391, one context of 131072 with 38 parts a row 64.8 / 64.7 / 74).  Eight loads of a
+// row's parts at once fit 64 registers, so four CTAs an SM (16 loads and two CTAs: 61 for
+// the long context, 36 and 401 for the others).
+constexpr int kJoinThreads = 256, kJoinY = 16, kJoinLoads = 8;
 
 // The parts of a cut unit's rows are weighted by 2^(m - max m) and added up in
 // order, so repeated calls give the same bits.  A warp takes a row, a lane four
