@@ -105,9 +105,8 @@ constexpr int kJoinThreads = 256, kJoinY = 16, kJoinLoads = 8;
 
 // The parts of a cut unit's rows are weighted by 2^(m - max m) and added up in
 // order, so repeated calls give the same bits.  A warp takes a row, a lane four
-// columns of it at a time; with few parts, as in a prompt, two rows side by side,
-// all of whose parts are asked for beside their maxima and sums (152 cut units of
-// 256 rows: one trip to memory, not three).
+// columns of it at a time; few parts, as in a prompt, are all asked for beside their
+// maxima and sums (152 cut units of 256 rows: one trip to memory a row, not three).
 __global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const Params p, const int kind) {
   sm103::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
@@ -145,43 +144,35 @@ __global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const Param
     a.z = fmaf(w, x.z, a.z);
     a.w = fmaf(w, x.w, a.w);
   };
-  constexpr int kWarps = kJoinThreads / 32, kFew = 4, kPair = 1;
+  constexpr int kWarps = kJoinThreads / 32, kFew = 4;
   if (rec.parts <= kFew) {
-    for (int row0 = (blockIdx.y * kWarps + warp) * kPair; row0 < rows;
-         row0 += kJoinY * kWarps * kPair) {
+    for (int row = blockIdx.y * kWarps + warp; row < rows; row += kJoinY * kWarps) {
       for (int c = 4 * lane; c - 4 * lane < p.dim; c += 128) {
-        float2 ml[kPair][kFew];
-        float4 x[kPair][kFew];
+        float2 ml[kFew];
+        float4 x[kFew];
 #pragma unroll
-        for (int r = 0; r < kPair; ++r) {
-#pragma unroll
-          for (int k = 0; k < kFew; ++k) {
-            ml[r][k] = make_float2(-INFINITY, 0.f);
-            x[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k >= rec.parts || row0 + r >= rows) continue;
-            ml[r][k] = p.part_ml[slot(k) * p.bm + row0 + r];
-            if (c < p.dim)
-              x[r][k] = *reinterpret_cast<const float4*>(p.part_o + slot(k) * step +
-                                                         (int64_t)(row0 + r) * p.dp + c);
-          }
+        for (int k = 0; k < kFew; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k >= rec.parts) continue;
+          ml[k] = p.part_ml[slot(k) * p.bm + row];
+          if (c < p.dim)
+            x[k] = *reinterpret_cast<const float4*>(p.part_o + slot(k) * step +
+                                                    (int64_t)row * p.dp + c);
         }
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int r = 0; r < kPair; ++r) {
-          if (row0 + r >= rows) continue;
-          float M = -INFINITY, L = 0.f;
+        for (int k = 0; k < kFew; ++k) M = fmaxf(M, ml[k].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < kFew; ++k) M = fmaxf(M, ml[r][k].x);
-          const float base = M == -INFINITY ? 0.f : M;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < kFew; ++k) {
-            if (k >= rec.parts) continue;
-            const float w = sm103::ex2(ml[r][k].x - base);
-            L = fmaf(w, ml[r][k].y, L);
-            add(a, w, x[r][k]);
-          }
-          write(row0 + r, c, a, M, L);
+        for (int k = 0; k < kFew; ++k) {
+          if (k >= rec.parts) continue;
+          const float w = sm103::ex2(ml[k].x - base);
+          L = fmaf(w, ml[k].y, L);
+          add(a, w, x[k]);
         }
+        write(row, c, a, M, L);
       }
     }
     return;

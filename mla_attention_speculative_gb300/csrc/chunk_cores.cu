@@ -9,9 +9,9 @@
 //
 // What bounds it is the multiply-adds: a tile of heads of 80 (held as 96) is
 // 64 * 64 * 176 of them, 5632 cycles of an SM.  8 sequences of 1 to 129 rows, a window
-// of 1000 over up to 4129 positions, 20 heads on 4 of 80: 64 us, with 9 to 10 tiles to
-// a CTA.  (Two CTAs on an SM hide each other's loads: asynchronous copies of the next
-// tile 68 us, multiply-adds of pairs 72 and 75 us with both.)
+// of 1000 over up to 4129 positions, 20 heads on 4 of 80: 61 us, 2 of them the join's, with
+// 9 to 10 tiles to a CTA.  (Two CTAs on an SM hide each other's loads: asynchronous copies of the next
+// tile 68 us for 64 then, multiply-adds of pairs 72 and 75 us with both.)
 
 #include <mutex>
 #include <type_traits>

@@ -30,12 +30,12 @@
 // such an element is NaN); the latter are put back at the end, for the rows that
 // see them.
 //
-// Measured in a graph, 128 wide: a causal prompt of 8192 rows, 32 heads on 8, 398 us =
-// 1381 TFLOP/s (0.72 of a library product's rate); 24 prompts and steps over an e4m3
-// cache, 64 heads on 8, 741 us; 16 rows at 131072 positions, 32 heads on 4, 65 us =
-// 4.2 TB/s; 16 steps of 1 to 8 rows 35 us.  What bounds the long ones is the chain of a
+// Measured in a graph, 128 wide: a causal prompt of 8192 rows, 32 heads on 8, 395 us =
+// 1392 TFLOP/s (0.72 of a library product's rate); 24 prompts and steps over an e4m3
+// cache, 64 heads on 8, 741 us; 16 rows at 131072 positions, 32 heads on 4, 64 us =
+// 4.2 TB/s; 16 steps of 1 to 8 rows 33.5 us.  What bounds the long ones is the chain of a
 // tile: S, its maximum (9 % of the time), its exponentials (5 %), P, O; the matrix pipe
-// is busy two thirds of the time.  Of the prompt's 398 us about 20 go to the masks and
+// is busy two thirds of the time.  Of the prompt's 395 us about 20 go to the masks and
 // hidden rows of edge tiles and 7 to the outputs.
 #pragma once
 
