@@ -333,12 +333,15 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
 #pragma unroll
               for (int o = LPR / 2; o > 0; o >>= 1)
                 most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-              // 2^-exponent of the largest; the row's scores are scaled back
+              // 2^-exponent of the largest; the row's scores are scaled back.  (Both factors are
+              // normal numbers: beside subnormal queries, whose few bits fp16 holds as they are,
+              // and beside an infinite one, whose row's scores are no finite numbers anyway, the
+              // other elements stay finite.)
               float down = 1.f, up = 1.f;
-              if (most > 0.f && isfinite(most)) {
-                const int ex = ilogbf(most);
-                down = ldexpf(1.f, -ex);
-                up = ldexpf(1.f, ex);
+              if (most > 0.f) {
+                const int ex = min(max((int)(__float_as_uint(most) >> 23) - 127, -120), 120);
+                down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                up = __uint_as_float((uint32_t)(127 + ex) << 23);
               }
               if (c == 0) q_scale[(split ? 0 : 128 * s) + row] = up;
               down *= ksign;

@@ -1,0 +1,49 @@
+"""The chunk attention at values where it can go wrong: queries, key scales and scores of any size,
+infinities and values that are no numbers.
+
+Tolerances are those of the parity tests (derived there): what changes here are the inputs."""
+
+import pytest
+import torch
+
+from mla_attention_speculative_gb300 import binding as B
+from mla_attention_speculative_gb300 import build_lib
+from test_chunk_gpu import BF16, DEV, E4M3, case, check, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build_lib.build()
+    B.lib()
+    yield
+    torch.cuda.synchronize()
+    B.mla_device_status()
+
+
+def scaled(c, factor):
+    """The case with its queries times `factor`, subnormal ones among them."""
+    g = torch.Generator(DEV).manual_seed(3)
+    x = torch.randn(c["q"].shape, generator=g, device=DEV).clamp(-3.0, 3.0)
+    c["q"] = (x.double() * factor).to(BF16)
+    assert c["q"].isfinite().all() and (c["q"] != 0).any()
+    return c
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 5), (192, 16)])
+@pytest.mark.parametrize("factor", [2.0 ** -133, 1e-39, 2.0 ** -128, 2.0 ** -126, 1e-30, 1e-10,
+                                    1e10, 1e30])
+def test_chunk_e4m3_queries_of_any_size(D, page, factor):
+    c = scaled(case([140, 0, 60], [5, 40, 200], 4, 2, D, page, BF16, E4M3, seed=60, spread=0.01),
+               factor)
+    # with key scales that bring the scores back to a few units ...
+    size = min(max(10.0 / factor, 1e-37), 1e38)
+    c["k_scale"].copy_(torch.tensor([size, -0.75 * size], device=DEV))
+    out, lse = run(c)
+    check(c, out, lse)
+    # ... and with ones that leave them small: every position weighs the same
+    if factor < 1:
+        c["k_scale"].fill_(0.01)
+        out, lse = run(c)
+        check(c, out, lse)
