@@ -276,9 +276,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       if constexpr (HALF) {
         const float ks = p.k_scale ? p.k_scale[kvh] : 1.f;
         ksign = ks < 0.f ? -1.f : 1.f;
-        // (a scale that is no finite number makes its heads NaN; one of zero leaves
-        // hidden scores below the others)
-        sl2 = isfinite(ks) ? fmaxf(sl2 * fabsf(ks), 1e-37f) : NAN;
+        // (a scale that is no finite number makes its heads NaN)
+        sl2 = isfinite(ks) ? sl2 * fabsf(ks) : NAN;
       }
       // This stream's queries.  The products that read the ones before are done, and
       // with both streams' arrivals everything of the segment before is.
@@ -365,6 +364,8 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
           if (split) named_bar_sync(1, 256);  // stream 1 reads the scales stream 0 wrote
           else __syncwarp();
           sl2 *= q_scale[r];
+          // (one that vanishes leaves hidden scores, minus infinity, below the others)
+          if (sl2 < 1e-37f) sl2 = 1e-37f;
         }
       }
       // Where the walk stands waits in shared memory while the scores need the registers.

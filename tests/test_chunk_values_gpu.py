@@ -47,3 +47,23 @@ def test_chunk_e4m3_queries_of_any_size(D, page, factor):
         c["k_scale"].fill_(0.01)
         out, lse = run(c)
         check(c, out, lse)
+
+
+@pytest.mark.parametrize("factor", [2.0 ** -133, 2.0 ** -100, 2.0 ** -40, 2.0 ** -27, 1.0])
+@pytest.mark.parametrize("scales", [(0.0, -0.0), (1e-37, 1e-44), (1e-30, -1e-41)])
+def test_chunk_e4m3_score_scales_that_vanish(factor, scales):
+    # scores too small to tell positions apart: hidden ones stay hidden, the others weigh the same
+    for window in (0, 50):
+        c = scaled(case([140, 0, 60], [5, 40, 200], 4, 2, 64, 16, BF16, E4M3, seed=61), factor)
+        c["k_scale"].copy_(torch.tensor(scales, device=DEV))
+        out, lse = run(c, window=window)
+        check(c, out, lse, window)
+
+
+def test_chunk_e4m3_large_queries_under_small_key_scales():
+    for D in (64, 192):
+        c = scaled(case([140, 0, 60], [5, 40, 200], 4, 2, D, 16, BF16, E4M3, seed=66, spread=0.01),
+                   1e38)
+        c["k_scale"].copy_(torch.tensor([1e-37, -8e-38], device=DEV))
+        out, lse = run(c)
+        check(c, out, lse)
