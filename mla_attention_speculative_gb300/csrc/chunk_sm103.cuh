@@ -275,9 +275,10 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
       float ksign = 1.f;
       if constexpr (HALF) {
         const float ks = p.k_scale ? p.k_scale[kvh] : 1.f;
-        ksign = ks < 0.f ? -1.f : 1.f;
-        // (a scale that is no finite number makes its heads NaN)
-        sl2 = isfinite(ks) ? sl2 * fabsf(ks) : NAN;
+        // (one that is no finite number makes its heads' queries NaN, not the scale: a hidden
+        // score times that would be NaN too)
+        ksign = !isfinite(ks) ? NAN : ks < 0.f ? -1.f : 1.f;
+        if (isfinite(ks)) sl2 *= fabsf(ks);
       }
       // This stream's queries.  The products that read the ones before are done, and
       // with both streams' arrivals everything of the segment before is.

@@ -3,12 +3,13 @@ infinities and values that are no numbers.
 
 Tolerances are those of the parity tests (derived there): what changes here are the inputs."""
 
+import numpy as np
 import pytest
 import torch
 
 from mla_attention_speculative_gb300 import binding as B
 from mla_attention_speculative_gb300 import build_lib
-from test_chunk_gpu import BF16, DEV, E4M3, case, check, run
+from test_chunk_gpu import BF16, DEV, E4M3, case, check, npy, run
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,21 @@ def test_chunk_e4m3_large_queries_under_small_key_scales():
         c["k_scale"].copy_(torch.tensor([1e-37, -8e-38], device=DEV))
         out, lse = run(c)
         check(c, out, lse)
+
+
+def test_chunk_e4m3_key_scale_of_no_number_and_rows_that_see_nothing():
+    # fewer cached rows than the step's last positions, a window that ends behind them
+    for bad in (float("nan"), float("inf")):
+        c = case([100, 100], [30, 300], 4, 2, 64, 16, BF16, E4M3, seed=62, lens=[110, 330])
+        c["k_scale"][0] = bad
+        out, lse = run(c, window=5)
+        pos = np.concatenate([100 + np.arange(30), 100 + np.arange(300)])
+        T = np.array([110] * 30 + [330] * 300)
+        sees = pos + 1 - 5 < T
+        assert 0 < sees[:30].sum() < 30 and 0 < sees[30:].sum() < 300
+        o, z = npy(out), npy(lse)
+        assert np.isnan(o[sees, :2]).all() and np.isnan(z[sees, :2]).all()
+        assert not o[~sees].any() and (z[~sees] == -np.inf).all()
+        c["k_scale"][0] = 1.0
+        want, want_lse = run(c, window=5)
+        assert torch.equal(out[:, 2:], want[:, 2:]) and torch.equal(lse[:, 2:], want_lse[:, 2:])
