@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const Param
   auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
   const float vs = p.v_scale ? p.v_scale[rec.kvh] : 1.f;
   const int64_t step = (int64_t)p.bm * p.dp;
-  auto write = [&](int row, int c, const float4& a, float M, float L) {
+  auto write = [&](int row, int c, float4 a, float M, float L) {
     const int i = p.group_div(rec.r0 + row), j = rec.r0 + row - i * p.group;
     const int64_t head = (int64_t)(rec.row0 + i) * p.heads + rec.kvh * p.group + j;
     if (c == 0 && p.lse)
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const Param
           L == 0.f ? -INFINITY
                    : (M + (log2f(L) - (kind == kE4m3 ? kShift : 0.f))) * 0.6931471805599453f;
     if (c >= p.dim) return;
+    if (L == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);  // (it may be no numbers)
     const float inv = L == 0.f ? 0.f : vs / L;
     if (kind == kFp32)
       *reinterpret_cast<float4*>((float*)p.out + head * p.dim + c) =

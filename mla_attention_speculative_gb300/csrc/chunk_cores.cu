@@ -252,12 +252,14 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
       }
       const int i = p.group_div(u.r0 + r), j = u.r0 + r - i * p.group;
       const int64_t head = (int64_t)(s.row0 + i) * p.heads + kvh * p.group + j;
-      const float inv = l[a] == 0.f ? 0.f : 1.f / l[a];
+      const float inv = 1.f / l[a];
 #pragma unroll
       for (int c = 0; c < NO; ++c) {
         const int col = 2 * tx + 32 * c;
         if (col >= p.dim) continue;
-        const float y0 = o[a][2 * c] * inv, y1 = o[a][2 * c + 1] * inv;
+        // (weights that are all zero: the values may be no numbers)
+        const float y0 = l[a] == 0.f ? 0.f : o[a][2 * c] * inv;
+        const float y1 = l[a] == 0.f ? 0.f : o[a][2 * c + 1] * inv;
         *reinterpret_cast<float2*>((float*)p.out + head * p.dim + col) = make_float2(y0, y1);
       }
       if (tx == 0 && p.lse)

@@ -9,7 +9,7 @@ import torch
 
 from mla_attention_speculative_gb300 import binding as B
 from mla_attention_speculative_gb300 import build_lib
-from test_chunk_gpu import BF16, DEV, E4M3, case, check, npy, run
+from test_chunk_gpu import BF16, DEV, E4M3, FP32, case, check, hit, npy, run
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,20 @@ def test_chunk_e4m3_key_scale_of_no_number_and_rows_that_see_nothing():
         c["k_scale"][0] = 1.0
         want, want_lse = run(c, window=5)
         assert torch.equal(out[:, 2:], want[:, 2:]) and torch.equal(lse[:, 2:], want_lse[:, 2:])
+
+
+@pytest.mark.parametrize("dtype,cache", [(FP32, FP32), (BF16, BF16), (BF16, E4M3)])
+@pytest.mark.parametrize("kept", [140, 9000])
+def test_chunk_scores_all_minus_infinity_over_values_of_no_number(dtype, cache, kept):
+    # zeros and -inf, whatever the values: short, and cut between thread blocks
+    c = case([kept], [5], 2, 1, 64, 16, dtype, cache, seed=63)
+    live = c["page_table"][0].long()
+    c["q"][:, :, 0] = -float("inf")
+    k = c["k_cache"].view(torch.uint8) if cache == E4M3 else c["k_cache"]
+    k[live, :, :, 0] = 0x7E if cache == E4M3 else 2.0
+    for t in (3, 70, kept - 1, kept):
+        hit(c, "v_cache", 0, t, 0, 7, 0x7F if cache == E4M3 else float("nan"))
+        if cache != E4M3:
+            hit(c, "v_cache", 0, t, 0, 9, float("inf"))
+    out, lse = run(c)
+    assert not npy(out).any() and (npy(lse) == -np.inf).all()
