@@ -188,9 +188,12 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
         float sum = 0.f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
+          const int pos = pos0 + tx + 16 * b;
           x[a][b] = sm103::ex2(x[a][b] - base);
           sum += x[a][b];
-          sP[(ty * 4 + a) * LP + tx + 16 * b] = x[a][b];
+          // a hidden position's weight is -0, which no exponential is
+          sP[(ty * 4 + a) * LP + tx + 16 * b] =
+              edge && (pos < first[a] || pos > last[a]) ? -0.f : x[a][b];
         }
         l[a] = l[a] * f + sum;  // this thread's columns; the 16 threads' sums meet at the end
         if (f != 1.f) {
@@ -217,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
               // a hidden position's value may be anything, also what zero times it is not zero
-              if (decltype(masked)::value && pw[a][e] == 0.f) continue;
+              // (a seen one counts, whatever its weight)
+              if (decltype(masked)::value && __float_as_uint(pw[a][e]) == 0x80000000u) continue;
 #pragma unroll
               for (int c = 0; c < NO; ++c) {
                 o[a][2 * c] = fmaf(pw[a][e], vv[c].x, o[a][2 * c]);

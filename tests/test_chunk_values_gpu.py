@@ -103,3 +103,37 @@ def test_chunk_scores_all_minus_infinity_over_values_of_no_number(dtype, cache, 
             hit(c, "v_cache", 0, t, 0, 9, float("inf"))
     out, lse = run(c)
     assert not npy(out).any() and (npy(lse) == -np.inf).all()
+
+
+@pytest.mark.parametrize("dtype,cache", [(FP32, FP32), (BF16, BF16), (BF16, E4M3)])
+@pytest.mark.parametrize("t", [10, 70, 100, 120, 139])
+def test_chunk_values_of_no_number_under_weights_of_zero(dtype, cache, t):
+    """A seen value that is no number shows whatever its weight, in tiles that every row sees
+    whole and in those at an edge; a hidden one does not."""
+    c = case([100], [40], 2, 1, 64, 16, dtype, cache, seed=64)
+    live = c["page_table"][0].long()
+    c["q"].zero_()
+    c["q"][:, :, 0] = 1.0
+    if cache == E4M3:
+        c["k_cache"].view(torch.uint8)[live, :, :, 0] = 0x38      # 1.0
+        c["k_scale"].fill_(1.0)
+    else:
+        c["k_cache"][live, :, :, 0] = 0.0
+    # the position's score is 400 below the others' (a weight of 2^-577)
+    low = {FP32: -400.0, BF16: -400.0, E4M3: 0xFE}[cache]         # -448
+    hit(c, "k_cache", 0, t, 0, 0, low)
+    clean, clean_lse = run(c, scale=1.0)
+    check(c, clean, clean_lse, scale=1.0)
+    hit(c, "v_cache", 0, t, 0, 7, 0x7F if cache == E4M3 else float("nan"))
+    if cache != E4M3:
+        hit(c, "v_cache", 0, t, 0, 9, float("inf"))
+    out, lse = run(c, scale=1.0)
+    sees = 100 + np.arange(40) >= t
+    o, z = npy(out), npy(clean)
+    assert np.isnan(o[sees][:, :, 7]).all()
+    z[sees, :, 7] = o[sees, :, 7]
+    if cache != E4M3:
+        assert not np.isfinite(o[sees][:, :, 9]).any()
+        z[sees, :, 9] = o[sees, :, 9]
+    assert np.array_equal(o, z, equal_nan=True)
+    assert torch.equal(lse, clean_lse)
