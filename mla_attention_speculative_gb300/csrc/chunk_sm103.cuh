@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
             tmem_wait_ld<32>(o);
           }
         }
-        if (none) {
+        if (none && whole) {  // (a part's weights may all be zero while another's are not)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : o[e];
         }
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
                          : "memory");
           }
         }
-        if (fix && live && l != 0.f) {
+        if (fix && live && (l != 0.f || !whole)) {
           // what was set to zero, added to the staged values
           const int lo = max(first, (u.tile0 + g.t0) * kBN),
                     hi = min(last, (u.tile0 + g.t1) * kBN - 1);

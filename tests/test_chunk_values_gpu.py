@@ -137,3 +137,36 @@ def test_chunk_values_of_no_number_under_weights_of_zero(dtype, cache, t):
         z[sees, :, 9] = o[sees, :, 9]
     assert np.array_equal(o, z, equal_nan=True)
     assert torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("dtype,cache", [(FP32, FP32), (BF16, BF16), (BF16, E4M3)])
+@pytest.mark.parametrize("kept,low", [(200, 150), (9000, 4500), (9000, 8900)])
+def test_chunk_values_of_no_number_under_scores_of_minus_infinity(dtype, cache, kept, low):
+    """... also where all that a thread block sees of a row has such scores."""
+    c = case([kept], [5], 2, 1, 64, 16, dtype, cache, seed=67)
+    live = c["page_table"][0].long()
+    c["q"].zero_()
+    c["q"][:, :, 0] = -2.0 ** 120                         # times the keys: beyond fp32
+    if cache == E4M3:
+        c["k_cache"].view(torch.uint8)[live, :, :, 0] = 0x7E
+        c["k_scale"].fill_(64.0)
+    else:
+        c["k_cache"][live] = 0.0
+        c["k_cache"][live, :, :, 0] = 2.0 ** 20
+    for t in range(low, kept + 5):                        # finite from here on
+        hit(c, "k_cache", 0, t, 0, 0, 0 if cache == E4M3 else 0.0)
+    clean, clean_lse = run(c, scale=1.0)
+    assert torch.isfinite(clean).all() and torch.isfinite(clean_lse).all()
+    vals = npy(c["v_cache"][live].flatten(0, 1)[:, 0]) * (
+        npy(c["v_scale"])[0] if cache == E4M3 else 1.0)
+    for i in range(5):
+        v = vals[low:kept + 1 + i]
+        assert np.abs(npy(clean)[i] - v.mean(0)).max() <= 2.0 ** -7 * np.abs(v).max()
+    for t in (3, low - 1):
+        hit(c, "v_cache", 0, t, 0, t % 64, 0x7F if cache == E4M3 else float("nan"))
+    out, lse = run(c, scale=1.0)
+    o, z = npy(out), npy(clean)
+    for t in (3, low - 1):
+        assert np.isnan(o[:, :, t % 64]).all()
+        z[:, :, t % 64] = np.nan
+    assert np.array_equal(o, z, equal_nan=True) and torch.equal(lse, clean_lse)
