@@ -657,7 +657,8 @@ mla_status_t mla_chunk_attention(const mla_kv_geometry_t* geom, const void* q,
  *   cache_lens_out[b] = T, held_pages_out[b] = ceil(T / P)
  * When the list has run out the slot gets the whole pages only and is that much
  * shorter, and missing_out counts it.  Sources are taken as they were before the
- * call.
+ * call.  A page id outside [0, num_pages), the source's or the free list's, goes
+ * to the table and to the list of moves as it is, and is recorded.
  *
  *  shares / shares_out  device [num_pages]; may be one array
  *  free_pages / free_span  as for mla_page_step; free_capacity >= 1

@@ -258,7 +258,10 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kThreads)
       own = at < have;
       if (own) {
         const int id = p.free_pages[free.first + at];
-        p.move_src[at] = p.table[(long long)s * p.width + full];
+        const int from = p.table[(long long)s * p.width + full];
+        // (listed all the same: the copy passes over such a move)
+        if (id < 0 || id >= p.num_pages || from < 0 || from >= p.num_pages) bad_page();
+        p.move_src[at] = from;
         p.move_dst[at] = id;
         p.move_rows[at] = rest;
         p.table[(long long)b * p.width + full] = id;

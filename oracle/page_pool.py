@@ -86,6 +86,7 @@ def page_fork(src_of, lens, held, table, shares, free_pages, span, page):
             if first < end:
                 table[b, full] = free_pages[first]
                 moves.append((int(before[s, full]), int(free_pages[first]), total % page))
+                bad = bad or any(not 0 <= m < len(shares) for m in moves[-1][:2])
                 first += 1
                 lens_out[b], held_out[b] = total, full + 1
             else:
