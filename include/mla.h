@@ -610,8 +610,8 @@ mla_status_t mla_chunk_workspace_bytes(const mla_kv_geometry_t* geom, int32_t ba
  *          counts as what it holds)
  *  row_start  device [batch + 1] int32, ascending (cut to [0, rows])
  *  page_table  as for mla_decode_attention
- *  out     device [rows, num_heads, head_dim], dense; no output may overlap
- *          another buffer
+ *  out     device [rows, num_heads, head_dim], dense; neither an output nor the
+ *          workspace may overlap another buffer (refused, but for the caches)
  *  lse     device fp32 [rows, num_heads], may be NULL
  *  workspace  mla_chunk_workspace_bytes() bytes, 256-byte aligned
  *

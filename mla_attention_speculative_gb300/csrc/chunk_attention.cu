@@ -362,13 +362,6 @@ extern "C" mla_status_t mla_chunk_attention(
               (long long)q_row_stride, (long long)row);
     return MLA_ERR_INVALID_ARG;
   }
-  const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
-  const uintptr_t q1 = q0 + (uintptr_t)(((rows - 1) * q_row_stride + row) * eb);
-  const uintptr_t o1 = o0 + (uintptr_t)(rows * row * eb);
-  if (q0 < o1 && o0 < q1) {
-    set_error("chunk: out overlaps q");
-    return MLA_ERR_INVALID_ARG;
-  }
   const chunk::Plan d =
       chunk::make_plan(g, batch, rows, cache->page_size, max_pages_per_seq);
   if (workspace == nullptr || workspace_bytes < d.bytes) {
@@ -379,6 +372,36 @@ extern "C" mla_status_t mla_chunk_attention(
   if ((uintptr_t)workspace & 255u) {
     set_error("workspace is not 256-byte aligned");
     return MLA_ERR_INVALID_ARG;
+  }
+  // (the caches are not looked at: their strides may leave room for other buffers)
+  struct Span {
+    const char* name;
+    const void* at;
+    int64_t bytes;
+  };
+  const int64_t lse_bytes = (int64_t)rows * g->num_heads * 4, scales = (int64_t)g->num_kv_heads * 4;
+  const Span spans[] = {
+      {"out", out, rows * row * eb},
+      {"lse", lse, lse_bytes},
+      {"the workspace", workspace, (int64_t)d.bytes},
+      {"q", q, ((rows - 1) * q_row_stride + row) * eb},
+      {"kept_lens", kept_lens, (int64_t)batch * 4},
+      {"cache_lens", cache_lens, (int64_t)batch * 4},
+      {"row_start", row_start, ((int64_t)batch + 1) * 4},
+      {"page_table", page_table, (int64_t)batch * max_pages_per_seq * 4},
+      {"k_scale", cache->k_scale, scales},
+      {"v_scale", cache->v_scale, scales},
+  };
+  constexpr int kWritten = 3, kSpans = sizeof(spans) / sizeof(spans[0]);
+  for (int i = 0; i < kWritten; ++i) {
+    for (int j = i + 1; j < kSpans; ++j) {
+      const uintptr_t a = (uintptr_t)spans[i].at, b = (uintptr_t)spans[j].at;
+      if (a != 0 && b != 0 && a < b + (uintptr_t)spans[j].bytes &&
+          b < a + (uintptr_t)spans[i].bytes) {
+        set_error("chunk: %s overlaps %s", spans[i].name, spans[j].name);
+        return MLA_ERR_INVALID_ARG;
+      }
+    }
   }
   chunk::Params p;
   p.q = q;
