@@ -967,6 +967,17 @@ def mla_decode_workspace_bytes(num_heads: int, num_kv_heads: int, head_dim: int,
     return out.value
 
 
+def _softmax_scale(scale: Optional[float]) -> float:
+    """The scale as the library takes it, in fp32, where 0 stands for 1/sqrt(head_dim)."""
+    if scale is None:
+        return 0.0
+    fp32 = ctypes.c_float(float(scale)).value
+    if not 0.0 < fp32 < float("inf"):
+        raise ValueError(f"scale must be positive and finite in fp32 (None: 1/sqrt(head_dim)), "
+                         f"got {scale}")
+    return fp32
+
+
 class PreparedDecodeAttention(_PreparedCall):
     """mla_decode_attention with its arguments marshalled once, for a decode loop
     over fixed buffers (lengths and tables are read on the device, so they may
@@ -983,6 +994,8 @@ class PreparedDecodeAttention(_PreparedCall):
         _tensor("k_cache", k_cache, (None, None, None, D), dense=False)
         Hk = k_cache.shape[2]
         cache = _kv_cache(k_cache, v_cache, q.dtype, Hk, D, k_scale, v_scale)
+        geom = KVGeometry(H, Hk, D, _softmax_scale(scale), DTYPES[q.dtype],
+                          CACHE_DTYPES[k_cache.dtype])
         _tensor("cache_lens", cache_lens, (B,), torch.int32)
         _tensor("page_table", page_table, (B, None), torch.int32)
         if out is not None:
@@ -994,10 +1007,6 @@ class PreparedDecodeAttention(_PreparedCall):
         dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, cache_lens=cache_lens,
                           page_table=page_table, k_scale=k_scale, v_scale=v_scale, out=out,
                           lse=lse, workspace=workspace)
-        if scale is not None and not float(scale) > 0.0:
-            raise ValueError("scale must be positive (None: 1/sqrt(head_dim))")
-        geom = KVGeometry(H, Hk, D, float(scale) if scale is not None else 0.0, DTYPES[q.dtype],
-                          CACHE_DTYPES[k_cache.dtype])
         made = []
         if out is None:
             out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
@@ -1067,6 +1076,8 @@ class PreparedChunkAttention(_PreparedCall):
         _tensor("k_cache", k_cache, (None, None, None, D), dense=False)
         Hk = k_cache.shape[2]
         cache = _kv_cache(k_cache, v_cache, q.dtype, Hk, D, k_scale, v_scale)
+        geom = KVGeometry(H, Hk, D, _softmax_scale(scale), DTYPES[q.dtype],
+                          CACHE_DTYPES[k_cache.dtype])
         _tensor("page_table", page_table, (None, None), torch.int32)
         B = page_table.shape[0]
         _tensor("kept_lens", kept_lens, (B,), torch.int32)
@@ -1082,10 +1093,6 @@ class PreparedChunkAttention(_PreparedCall):
                           cache_lens=cache_lens, row_start=row_start, page_table=page_table,
                           k_scale=k_scale, v_scale=v_scale, out=out, lse=lse,
                           workspace=workspace)
-        if scale is not None and not float(scale) > 0.0:
-            raise ValueError("scale must be positive (None: 1/sqrt(head_dim))")
-        geom = KVGeometry(H, Hk, D, float(scale) if scale is not None else 0.0, DTYPES[q.dtype],
-                          CACHE_DTYPES[k_cache.dtype])
         made = []
         # (a row outside every sequence is not written: it starts as zeros, not as whatever was
         # there)
