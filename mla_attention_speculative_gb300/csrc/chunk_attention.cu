@@ -423,8 +423,8 @@ extern "C" mla_status_t mla_chunk_attention(
   p.starts = batch > chunk::kInside ? (chunk::Start*)ws : nullptr;
   p.rec = (chunk::Record*)(ws + d.off_rec);
   p.base = (long long*)(ws + d.off_base);
-  p.part_ml = (float2*)(ws + d.off_ml);
-  p.part_o = (float*)(ws + d.off_o);
+  p.part_ml = d.cut ? (float2*)(ws + d.off_ml) : nullptr;
+  p.part_o = d.cut ? (float*)(ws + d.off_o) : nullptr;
   p.heads = g->num_heads;
   p.kv_heads = g->num_kv_heads;
   p.group = g->num_heads / g->num_kv_heads;

@@ -62,7 +62,7 @@ struct Params {
   Record* rec;       // [ctas]
   long long* base;   // [batch + 1] cost before each sequence
   float2* part_ml;   // [2 * ctas][bm] running maximum (base 2) and sum
-  float* part_o;     // [2 * ctas][bm][dp] unnormalised
+  float* part_o;     // [2 * ctas][bm][dp] unnormalised; both NULL where no unit may be cut
   int heads, kv_heads, group, dim, dp, batch, rows, page, width, num_pages, window;
   int capacity;      // rows of a table's pages
   int bm, bn, ctas, unit_cost, snap;
@@ -401,6 +401,24 @@ __device__ __forceinline__ void find_share(const Params& p, int cta, PlanScratch
   to = t.start[1];
   if (from.b < p.batch) first = t.seq[from.b];
   if (warp == 1 && lane == 0) p.rec[cta] = make_record(p, cta, total, from, e);
+  __syncthreads();
+}
+
+// The same from the workspace, where a launch ahead has put them.  (All threads get what
+// one of them read, and units that no share may cut are not: a workspace that another
+// call is writing at the same time gives wrong results, but no threads that disagree on
+// the barriers to come, and no parts where there is no room for them.)
+__device__ __forceinline__ void read_share(const Params& p, int cta, PlanScratch& t, Start& from,
+                                           Start& to, Sequence& first) {
+  if (threadIdx.x < 2) {
+    Start s = p.starts[cta + threadIdx.x];
+    if (p.part_o == nullptr) s.tile = 0;
+    t.start[threadIdx.x] = s;
+  }
+  __syncthreads();
+  from = t.start[0];
+  to = t.start[1];
+  if (from.b >= 0 && from.b < p.batch) first.load(p, from.b);
   __syncthreads();
 }
 

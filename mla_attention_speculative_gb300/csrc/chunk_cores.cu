@@ -67,9 +67,7 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
   if (p.starts == nullptr) {
     find_share(p, cta, *reinterpret_cast<PlanScratch*>(s_raw), from, to, seq);
   } else {
-    from = p.starts[cta];
-    to = p.starts[cta + 1];
-    if (from.b >= 0 && from.b < p.batch) seq.load(p, from.b);
+    read_share(p, cta, *reinterpret_cast<PlanScratch*>(s_raw), from, to, seq);
   }
   // columns past the heads' width stay zero
   for (int i = tid; i < 3 * 64 * LD; i += kThreads) sQ[i] = 0.f;

@@ -242,9 +242,7 @@ __global__ void __launch_bounds__(Shape<DP, FEED>::THREADS, 1)
     // (the place of the queries, which come later)
     find_share(p, cta, *reinterpret_cast<PlanScratch*>(smem), from, to, seq);
   } else {
-    from = p.starts[cta];
-    to = p.starts[cta + 1];
-    if (from.b >= 0 && from.b < p.batch) seq.load(p, from.b);
+    read_share(p, cta, *reinterpret_cast<PlanScratch*>(smem), from, to, seq);
   }
   Walk w;
   Segment g;
