@@ -170,3 +170,33 @@ def test_chunk_values_of_no_number_under_scores_of_minus_infinity(dtype, cache, 
         assert np.isnan(o[:, :, t % 64]).all()
         z[:, :, t % 64] = np.nan
     assert np.array_equal(o, z, equal_nan=True) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("dtype,cache", [(FP32, FP32), (BF16, BF16), (BF16, E4M3)])
+@pytest.mark.parametrize("kept", [300, 9000])
+def test_chunk_equal_scores_of_any_size_weigh_the_same(dtype, cache, kept):
+    # (products of the score and its scale that fp32 has to round)
+    for scale in (1.1, 3.3e5, 2.0 ** 21, 1.37e9, 2.0 ** 33, 3.3e11):
+        c = case([kept], [4], 2, 1, 64, 16, dtype, cache, seed=65)
+        live = c["page_table"][0].long()
+        c["q"].zero_()
+        c["q"][:, :, 0] = 1.3
+        if cache == E4M3:
+            c["k_scale"].fill_(0.7)
+            c["k_cache"].view(torch.uint8)[live, :, :, 0] = 0x3B  # 1.375
+        else:
+            c["k_cache"][live] = 0.0
+            c["k_cache"][live, :, :, 0] = 1.1
+        out, lse = run(c, scale=scale)
+        vals = npy(c["v_cache"][live].flatten(0, 1)[:kept + 4, 0])
+        if cache == E4M3:
+            vals = vals * npy(c["v_scale"])[0]
+        # every weight is the same number, rounded the same way (bf16 2^-8, fp16 2^-11), which
+        # leaves the sums, the quotient and the output (fp32 2^-24, bf16 2^-8)
+        tol = {FP32: 2.0 ** -22, BF16: 2.0 ** -7 * (1 + 2.0 ** -7),
+               E4M3: (2.0 ** -8 + 2.0 ** -11) * (1 + 2.0 ** -7)}[cache]
+        got = npy(out)
+        for i in range(4):
+            v = vals[:kept + 1 + i]
+            bound = tol * np.abs(v.mean(0)) + 2 * (kept + 4) * 2.0 ** -23 * np.abs(v).mean(0)
+            assert (np.abs(got[i] - v.mean(0)) <= bound).all(), (scale, i)
