@@ -186,18 +186,26 @@ __global__ void __launch_bounds__(kThreads, Layout<DP>::OCC) chunk_cores_kernel(
         float sum = 0.f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const int pos = pos0 + tx + 16 * b;
           x[a][b] = sm103::ex2(x[a][b] - base);
           sum += x[a][b];
-          // a hidden position's weight is -0, which no exponential is
-          sP[(ty * 4 + a) * LP + tx + 16 * b] =
-              edge && (pos < first[a] || pos > last[a]) ? -0.f : x[a][b];
+          sP[(ty * 4 + a) * LP + tx + 16 * b] = x[a][b];
         }
         l[a] = l[a] * f + sum;  // this thread's columns; the 16 threads' sums meet at the end
         if (f != 1.f) {
 #pragma unroll
           for (int c = 0; c < 2 * NO; ++c) o[a][c] *= f;
         }
+      }
+      // A hidden position's weight is -0, which no exponential is (put here, behind all of
+      // them, since few tiles have any: chosen where they are stored 63.4 us for 61.1).
+      if (edge) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int pos = pos0 + tx + 16 * b;
+            if (pos < first[a] || pos > last[a]) sP[(ty * 4 + a) * LP + tx + 16 * b] = -0.f;
+          }
       }
       __syncwarp();  // a row's weights are made and used by one warp
       auto products = [&](auto masked) {
