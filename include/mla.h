@@ -616,10 +616,13 @@ mla_status_t mla_chunk_workspace_bytes(const mla_kv_geometry_t* geom, int32_t ba
  *  workspace  mla_chunk_workspace_bytes() bytes, 256-byte aligned
  *
  * What a row does not see does not touch it, infinities and NaN included; an
- * infinite value seen gives that infinity (NaN beside its opposite, or under a
- * weight below 2^-24 of the largest).  The lengths are read on the device and
- * the work is cut into equal shares there; parts are joined in a fixed order, so
- * repeated calls give the same bits.  Concurrent calls need a workspace each. */
+ * infinite value seen gives that infinity (NaN beside its opposite; either under
+ * a weight below 2^-24 of the largest), and NaN gives NaN whatever its weight.
+ * Queries and scores may be of any size that fp32 holds; beside an e4m3 cache
+ * scale * |k_scale| times a head's largest query element has to stay below 2^127.
+ * The lengths are read on the device and the work is cut into equal shares there;
+ * parts are joined in a fixed order, so repeated calls give the same bits.
+ * Concurrent calls need a workspace each. */
 mla_status_t mla_chunk_attention(const mla_kv_geometry_t* geom, const void* q,
                                  int64_t q_row_stride, int32_t rows, const mla_kv_cache_t* cache,
                                  const int32_t* kept_lens, const int32_t* cache_lens,
@@ -633,9 +636,11 @@ mla_status_t mla_chunk_attention(const mla_kv_geometry_t* geom, const void* q,
  * sequences: shares[page] counts its holders beyond the first, so a page that
  * one sequence holds and a page on the free list both have 0 (mla_page_step
  * needs to know nothing of it).  Only whole pages are ever shared, so the rows
- * that a sequence appends never fall into a shared one; a sequence cut back
- * into a shared page is forked to an idle slot, which gets its last page's rows
- * as a copy, and released.
+ * that a sequence appends never fall into a shared one, unless it has been cut
+ * back into it: such a sequence must be forked to an idle slot, which gets its last
+ * page's rows as a copy, and released, before anything is appended.  No call
+ * notices when that is left out (a cut alone is no mistake, and the page step does
+ * not see the holders); the appended rows then overwrite the other holders'.
  *
  * As above nothing is read on the host.  Outputs must not overlap inputs or one
  * another, except where an argument says so; a call with separate outputs can be
@@ -680,7 +685,8 @@ mla_status_t mla_page_fork(const int32_t* src_of, const int32_t* cache_lens,
  * held_pages[b] - 1 of its table row.  A page that has holders left only loses
  * one of them; the others go back to the free list in ascending order, in front
  * of its first entry as far as there is room (mla_page_step takes from there),
- * the rest behind its last one.
+ * the rest behind its last one.  A last page that is kept in part stays held, by
+ * others too where it is shared: nothing may be appended behind it then (above).
  *
  *  page_table  device [batch, max_pages_per_seq], read only
  *  free_pages  device [free_capacity], free_capacity >= num_pages (so there is

@@ -1275,7 +1275,9 @@ def mla_page_release(kept_lens, held_pages, page_table, shares, free_pages, free
     ``free_pages`` has room for every page (as many entries as ``shares``) and is
     written outside ``free_span``; ``page_table`` is only read.  ``out.held_pages``,
     ``out.shares`` and ``out.free_span`` are the next call's inputs;
-    ``out.shares`` may be ``shares``."""
+    ``out.shares`` may be ``shares``.  A sequence cut back into a page that others
+    hold must be forked and released before rows are appended to it: they would
+    overwrite the others' rows, and no call notices."""
     with _allocating_on(stream, page_table.device):
         call = PreparedPageRelease(kept_lens, held_pages, page_table, shares, free_pages,
                                    free_span, page_size, out)

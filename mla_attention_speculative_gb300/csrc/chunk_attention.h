@@ -25,6 +25,13 @@ constexpr int kMaxCtas = 512;
 // a prompt of 8192 rows 415 / 395 / 400 / 409 / 421, prompts and steps over an e4m3
 // cache 817 / 756 / 745 / 742 / 754, 16 steps of 1 to 8 rows 39.1 / 35.3 / 35.4 / 36.8 /
 // 39.1; a window of fp32 on CUDA cores 64.1 at 1, 64.2 at 2, 64.2 at 3, 75.2 at 4).
+// Those are 128 wide in pages of 64.  One number serves all widths and feeds, and at 3 / 5 /
+// 8 / 12 / 18 it is near the best one for prompts of any width (4096 rows, 16 heads on 4:
+// 64 wide 67 / 68 / 69 / 71 / 77, 192 wide 144 / 136 / 135 / 143 / 154, 256 wide 159 / 144 /
+// 146 / 154 / 165; e4m3 87 / 82 / 80 / 83 / 89, 263 / 227 / 219 / 233 / 252 and 247 / 228 /
+// 222 / 234 / 264), too high for steps of wide heads and slow feeds (16 steps, 256 wide 66 /
+// 66 / 70 / 74 / 78, e4m3 69 / 74 / 80 / 88 / 96; bf16 in pages of 20 98 / 108 / 119 / 136 /
+// 150, e4m3 in pages of 17 187 / 189 / 221 / 243 / 279).
 constexpr int kCoresCost = 2, kTensorCost = 8;
 // A share does not begin in the first or last `snap` tiles of a unit: on tensor cores
 // a tile takes less than the join of a part (16 steps of 1 to 8 rows, us at 0 / 1 / 2 / 3:

@@ -7,11 +7,15 @@
 // memory, and O += P V with 4 rows of DP / 16 columns to a thread.  Everything
 // is held and summed in fp32.
 //
-// What bounds it is the multiply-adds: a tile of heads of 80 (held as 96) is
-// 64 * 64 * 176 of them, 5632 cycles of an SM.  8 sequences of 1 to 129 rows, a window
-// of 1000 over up to 4129 positions, 20 heads on 4 of 80: 61 us, 2 of them the join's, with
-// 9 to 10 tiles to a CTA.  (Two CTAs on an SM hide each other's loads: asynchronous copies of the next
-// tile 68 us for 64 then, multiply-adds of pairs 72 and 75 us with both.)
+// 8 sequences of 1 to 129 rows, a window of 1000 over up to 4129 positions, 20 heads on 4
+// of 80: 61 us in a graph, 2 of them the join's.  A tile of heads of 80 (held as 96) is
+// 64 * 64 * 176 multiply-adds, 5632 cycles of an SM.  The cut gives no CTA more than 4 of
+// the 1012 tiles (kMinShare), so the fullest SM multiplies for 45000 of the 107000 cycles
+// that it is active: the multiply-add pipe is 40 % busy, issue slots 56 %, and a third of
+// the instructions are no multiply-adds.  The rest is waiting: a tile's page ids, then the
+// rows they lead to, then the barrier, with nothing of the next tile under way.  (Tried:
+// asynchronous copies of the next tile, behind its page ids all the same, 68 us for 64
+// then, multiply-adds of pairs 72, both 75.)
 
 #include <mutex>
 #include <type_traits>

@@ -30,13 +30,20 @@
 // such an element is NaN); the latter are put back at the end, for the rows that
 // see them.
 //
-// Measured in a graph, 128 wide: a causal prompt of 8192 rows, 32 heads on 8, 395 us =
-// 1392 TFLOP/s (0.72 of a library product's rate); 24 prompts and steps over an e4m3
-// cache, 64 heads on 8, 741 us; 16 rows at 131072 positions, 32 heads on 4, 64 us =
-// 4.2 TB/s; 16 steps of 1 to 8 rows 33.5 us.  What bounds the long ones is the chain of a
-// tile: S, its maximum (9 % of the time), its exponentials (5 %), P, O; the matrix pipe
-// is busy two thirds of the time.  Of the prompt's 395 us about 20 go to the masks and
-// hidden rows of edge tiles and 7 to the outputs.
+// Measured in a graph, 128 wide: a causal prompt of 8192 rows, 32 heads on 8, 395 to 398 us
+// = 1390 TFLOP/s (0.72 of a library product's rate; call by call 417); 24 prompts and steps
+// over an e4m3 cache, 64 heads on 8, 731 us; 16 rows at 131072 positions, 32 heads on 4, 64
+// us = 4.2 TB/s; 16 steps of 1 to 8 rows 33.6 us.  What bounds the long ones is the chain of
+// a tile: S, its maximum (9 % of the time), its exponentials (5 %), P, O; the matrix pipe
+// is busy two thirds of the time.  And a unit takes 6 to 8 tiles' time beside its tiles:
+// O is waited for and written, the next queries are read, and only then its first S
+// begins, nothing of which overlaps but K and V in the ring.  With 6.7 units and 219 tiles
+// a CTA that is 15 to 20 % of the prompt.
+// Other forms, 16 steps of 1 to 8 rows, 32 heads on 8, other inputs each time (us, share of
+// the copy rate): bf16 40 (0.50), e4m3 53 (0.22), bf16 in pages of 20 by rows 119 (0.16),
+// e4m3 in pages of 17, a box a row, 221 (0.05); 192 wide 65 and 94 (e4m3), 256 wide 70 and
+// 80.  So a step over an e4m3 cache, half the bytes, takes longer than over a bf16 one: its
+// conversion, four warps with one block at a time, is slower than the memory.
 #pragma once
 
 #include <cuda_bf16.h>
